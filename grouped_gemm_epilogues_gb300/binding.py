@@ -56,6 +56,34 @@ class GgePlanInfo(ctypes.Structure):
                 ("raster_along_n", c_i32), ("tail_tiles", c_i32), ("tail_splits", c_i32)]
 
 
+class GgeMxTensor(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p),
+                ("tensor_scale", ctypes.c_void_p), ("format", c_i32), ("reserved", c_i32),
+                ("rows", c_i64), ("cols", c_i64), ("batch", c_i64), ("stride_row", c_i64),
+                ("stride_batch", c_i64), ("scale_stride_batch", c_i64)]
+
+
+class GgeGemmMxArgs(ctypes.Structure):
+    _fields_ = [("A", GgeMxTensor), ("B", GgeMxTensor), ("C", ctypes.c_void_p),
+                ("D", ctypes.c_void_p), ("PostAct", ctypes.c_void_p),
+                ("alpha", ctypes.c_float), ("beta", ctypes.c_float),
+                ("alpha_dev", ctypes.c_void_p), ("beta_dev", ctypes.c_void_p),
+                ("act", c_i32), ("reserved", c_i32), ("config", ctypes.c_void_p)]
+
+
+class GgeRmsnormArgs(ctypes.Structure):
+    _fields_ = [("x", GgeTensor), ("residual", ctypes.c_void_p),
+                ("residual_out", ctypes.c_void_p), ("y", ctypes.c_void_p),
+                ("q", ctypes.c_void_p), ("values", ctypes.c_void_p), ("weight", ctypes.c_void_p),
+                ("weight_dtype", c_i32), ("eps", ctypes.c_float), ("inv_rms", ctypes.c_void_p)]
+
+
+class GgeRmsnormBwdArgs(ctypes.Structure):
+    _fields_ = [("dy", GgeTensor), ("h", GgeTensor), ("dh", ctypes.c_void_p), ("dx", GgeTensor),
+                ("weight", ctypes.c_void_p), ("weight_dtype", c_i32), ("reserved", c_i32),
+                ("inv_rms", ctypes.c_void_p), ("dweight", ctypes.c_void_p)]
+
+
 # every function include/gge.h declares, with its ctypes signature
 _SIGNATURES = {
     "gge_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(GgeGemmArgs), c_i32]),
@@ -92,6 +120,16 @@ _SIGNATURES = {
                              ctypes.POINTER(GgeConfig), ctypes.POINTER(ctypes.c_float)]),
     "gge_tuned_config": (c_i32, [ctypes.POINTER(GgeGemmArgs), c_i32, c_i32,
                                  ctypes.POINTER(GgeConfig)]),
+    "gge_mx_row_bytes": (ctypes.c_size_t, [c_i32, c_i64]),
+    "gge_mx_scale_bytes": (ctypes.c_size_t, [c_i32, c_i64, c_i64]),
+    "gge_mx_quantize": (c_i32, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                ctypes.c_void_p]),
+    "gge_mx_dequantize": (c_i32, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
+    "gge_gemm_mx": (c_i32, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    "gge_rmsnorm": (c_i32, [ctypes.c_void_p, ctypes.c_void_p]),
+    "gge_workspace_size_rmsnorm_bwd": (ctypes.c_size_t, [c_i64]),
+    "gge_rmsnorm_bwd": (c_i32, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t,
+                                ctypes.c_void_p]),
 }
 
 _lib = None
@@ -445,3 +483,186 @@ def gge_tuned_config(op, A, B, C=None, D=None, PostAct=None, act="none", num_gro
     if lib.gge_tuned_config(ctypes.byref(args), OP[op], num_groups, ctypes.byref(c)) != 0:
         return None
     return config_dict(c)
+
+
+# ------------------------------------------------- low-precision linear layers
+
+MX_FORMAT = {"mxfp8": 0, "mxfp4": 1, "nvfp4": 2}
+_MX_BLOCK = (32, 32, 16)
+
+
+def _mx_row_bytes(fmt, cols):
+    return (cols + 31) // 32 * (32 if fmt == 0 else 16)
+
+
+def _mx_kgroups(fmt, cols):
+    block = _MX_BLOCK[fmt]
+    return ((cols + block - 1) // block + 3) // 4
+
+
+def _mx_scale_bytes(fmt, rows, cols):
+    return (rows + 127) // 128 * _mx_kgroups(fmt, cols) * 512
+
+
+class MxTensor:
+    """A microscaled matrix (gge_mx_tensor): codes (rows, bytes) or (batch, rows, bytes)
+    uint8, scales a contiguous uint8 tensor of gge_mx_scale_bytes a batch, tensor_scale None
+    or a one-element fp32 tensor on the device (nvfp4)."""
+
+    __slots__ = ("codes", "scales", "format", "rows", "cols", "batch", "tensor_scale", "c")
+
+    def __init__(self, codes, scales, format, rows, cols, tensor_scale=None):
+        fmt = MX_FORMAT[format]
+        if codes.dtype != torch.uint8 or scales.dtype != torch.uint8:
+            raise TypeError("MxTensor: codes and scales are uint8 tensors")
+        if codes.dim() not in (2, 3):
+            raise ValueError("MxTensor: codes are 2-D or 3-D (batch first)")
+        batch = codes.shape[0] if codes.dim() == 3 else 1
+        if codes.shape[-2] != rows or codes.shape[-1] != _mx_row_bytes(fmt, cols) or \
+                (codes.numel() and codes.stride(-1) != 1):
+            raise ValueError("MxTensor: codes do not match rows, cols and format")
+        per = _mx_scale_bytes(fmt, rows, cols)
+        if scales.numel() != batch * per or not scales.is_contiguous():
+            raise ValueError("MxTensor: scales do not match rows, cols and format")
+        if tensor_scale is not None and (tensor_scale.dtype != torch.float32 or
+                                         tensor_scale.numel() != 1):
+            raise ValueError("MxTensor: tensor_scale is one fp32 value")
+        if scales.device != codes.device or (tensor_scale is not None and
+                                             tensor_scale.device != codes.device):
+            raise ValueError("MxTensor: codes, scales and tensor_scale on different devices")
+        self.codes, self.scales, self.format = codes, scales, format
+        self.rows, self.cols, self.batch, self.tensor_scale = rows, cols, batch, tensor_scale
+        self.c = GgeMxTensor(codes.data_ptr(), scales.data_ptr(),
+                             tensor_scale.data_ptr() if tensor_scale is not None else None, fmt, 0,
+                             rows, cols, batch, codes.stride(-2),
+                             codes.stride(0) if batch > 1 else 0, per)
+
+
+def mx_empty(rows, cols, format, device=None, batch=None, tensor_scale=None):
+    """An MxTensor with room for (rows, cols) or (batch, rows, cols) values: its codes and
+    scales share one allocation."""
+    fmt = MX_FORMAT[format]
+    dev = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
+    b = 1 if batch is None else batch
+    row = _mx_row_bytes(fmt, cols)
+    n_codes, n_scales = b * rows * row, b * _mx_scale_bytes(fmt, rows, cols)
+    start = (n_codes + 511) // 512 * 512
+    buf = torch.empty(start + n_scales, dtype=torch.uint8, device=dev)
+    shape, stride = ((rows, row), (row, 1)) if batch is None else ((b, rows, row), (rows * row, row, 1))
+    return MxTensor(buf.as_strided(shape, stride), buf.as_strided((n_scales,), (1,), start), format,
+                    rows, cols, tensor_scale)
+
+
+def _same_device(device, *tensors):
+    for t in tensors:
+        if t is not None and t.device != device:
+            raise ValueError("tensors on different devices")
+
+
+def _ref(struct):
+    return ctypes.addressof(struct) if struct is not None else None
+
+
+def _view_or_none(t, kind):
+    return view(t, kind) if t is not None else None
+
+
+def gge_mx_quantize(X, Q, values=None):
+    """Q (an MxTensor) = X quantised; X (rows, cols) or (batch, rows, cols), row-major or a
+    transposed view.  values: optional output, the numbers that the codes stand for."""
+    lib = load()
+    _same_device(X.device, Q.codes, values)
+    x, v = view(X, "X"), _view_or_none(values, "values")
+    _check(lib.gge_mx_quantize(_ref(x), _ref(Q.c), _ref(v), _stream(X)), "gge_mx_quantize")
+
+
+def gge_mx_dequantize(Q, Y):
+    """Y (bf16, f16 or f32) = the numbers that Q's codes stand for."""
+    lib = load()
+    _same_device(Y.device, Q.codes)
+    y = view(Y, "Y")
+    _check(lib.gge_mx_dequantize(_ref(Q.c), _ref(y), _stream(Y)), "gge_mx_dequantize")
+
+
+def gge_gemm_mx(A, B, D=None, C=None, PostAct=None, act="none", alpha=1.0, beta=1.0,
+                alpha_dev=None, beta_dev=None, config=None, workspace=None):
+    """D = alpha * A @ B^T + beta * C and / or PostAct = act(same) of MxTensors A (M, K) and
+    B (N, K) (or batched), their tensor scales included."""
+    lib = load()
+    out = D if D is not None else PostAct
+    if out is None:
+        raise ValueError("gge_gemm_mx: D or PostAct is required")
+    _same_device(out.device, A.codes, B.codes, C, D, PostAct, alpha_dev, beta_dev)
+    c, d, p = _view_or_none(C, "mn"), _view_or_none(D, "mn"), _view_or_none(PostAct, "mn")
+    args = GgeGemmMxArgs(A.c, B.c, _ref(c), _ref(d), _ref(p), alpha, beta,
+                         alpha_dev.data_ptr() if alpha_dev is not None else None,
+                         beta_dev.data_ptr() if beta_dev is not None else None, ACT[act], 0,
+                         _ref(config))
+    ws = _ws(out.device, _gemm_workspace_bytes(lib, out.device), workspace)
+    _check(lib.gge_gemm_mx(_ref(args), ws.data_ptr(), ws.numel(), _stream(out)), "gge_gemm_mx")
+
+
+_workspace_bytes = {}
+
+
+def _gemm_workspace_bytes(lib, device):
+    """gge_workspace_size of a device (it depends on nothing else), asked once."""
+    n = _workspace_bytes.get(device)
+    if n is None:
+        with torch.cuda.device(device):
+            n = _workspace_bytes[device] = lib.gge_workspace_size(None, 0)
+    return n
+
+
+def gge_rmsnorm(X, weight, Y=None, residual=None, residual_out=None, Q=None, values=None,
+                inv_rms=None, eps=1e-6):
+    """h = X + residual (rounded to X's type, written to residual_out), inv_rms = 1 / sqrt(mean
+    h^2 + eps) a row, Y = h * inv_rms * weight; Q (an MxTensor) = the same quantised, values =
+    the numbers that Q's codes stand for.  X (rows, cols); every output is optional."""
+    lib = load()
+    _same_device(X.device, weight, Y, residual, residual_out, Q.codes if Q is not None else None,
+                 values, inv_rms)
+    if X.dim() != 2 or weight.dim() != 1 or weight.shape[0] != X.shape[1] or \
+            (weight.numel() > 1 and weight.stride(0) != 1):
+        raise ValueError("gge_rmsnorm: X (rows, cols) and weight (cols,), contiguous")
+    if inv_rms is not None and (inv_rms.dtype != torch.float32 or inv_rms.numel() != X.shape[0] or
+                                not inv_rms.is_contiguous()):
+        raise ValueError("gge_rmsnorm: inv_rms is fp32, one value a row")
+    r, ro = _view_or_none(residual, "residual"), _view_or_none(residual_out, "residual_out")
+    y, v = _view_or_none(Y, "Y"), _view_or_none(values, "values")
+    if weight.dtype not in DTYPE:
+        raise TypeError(f"weight: unsupported dtype {weight.dtype}")
+    args = GgeRmsnormArgs(view(X, "X"), _ref(r), _ref(ro), _ref(y), _ref(Q.c if Q is not None else None),
+                          _ref(v), weight.data_ptr(), DTYPE[weight.dtype], eps,
+                          inv_rms.data_ptr() if inv_rms is not None else None)
+    _check(lib.gge_rmsnorm(_ref(args), _stream(X)), "gge_rmsnorm")
+
+
+def gge_rmsnorm_bwd(dY, H, weight, inv_rms, dX, dW=None, dH=None, workspace=None):
+    """Backward of gge_rmsnorm: dX (the gradient of X and of the residual) from dY, the saved H
+    (residual_out, or X) and inv_rms; dW (fp32, optional); dH the gradient reaching H directly."""
+    lib = load()
+    _same_device(dY.device, H, weight, inv_rms, dX, dW, dH)
+    cols = dY.shape[-1]
+    if dY.dim() != 2 or weight.shape != (cols,) or (weight.numel() > 1 and weight.stride(0) != 1):
+        raise ValueError("gge_rmsnorm_bwd: dY (rows, cols) and weight (cols,), contiguous")
+    if inv_rms.dtype != torch.float32 or inv_rms.numel() != dY.shape[0] or not inv_rms.is_contiguous():
+        raise ValueError("gge_rmsnorm_bwd: inv_rms is fp32, one value a row")
+    if dW is not None and (dW.dtype != torch.float32 or dW.shape != (cols,) or not dW.is_contiguous()):
+        raise ValueError("gge_rmsnorm_bwd: dW is fp32 (cols,), contiguous")
+    if weight.dtype not in DTYPE:
+        raise TypeError(f"weight: unsupported dtype {weight.dtype}")
+    dh = _view_or_none(dH, "dH")
+    args = GgeRmsnormBwdArgs(view(dY, "dY"), view(H, "H"), _ref(dh), view(dX, "dX"),
+                             weight.data_ptr(), DTYPE[weight.dtype], 0, inv_rms.data_ptr(),
+                             dW.data_ptr() if dW is not None else None)
+    ws, n = None, 0
+    if dW is not None:
+        buf = _ws(dY.device, _norm_workspace_bytes(lib, dY.device, cols), workspace)
+        ws, n = buf.data_ptr(), buf.numel()
+    _check(lib.gge_rmsnorm_bwd(_ref(args), ws, n, _stream(dY)), "gge_rmsnorm_bwd")
+
+
+def _norm_workspace_bytes(lib, device, cols):
+    with torch.cuda.device(device):
+        return lib.gge_workspace_size_rmsnorm_bwd(cols)

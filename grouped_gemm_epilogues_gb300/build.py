@@ -1,6 +1,6 @@
 """Builds libgge.so in-tree with nvcc for sm_103a.
 
-Each .cu under csrc/ is compiled in parallel into _build/, then linked into
+Each .cu under csrc/ and csrc/lowp/ is compiled in parallel into _build/, then linked into
 ``_build/libgge.so``.  ``python -m grouped_gemm_epilogues_gb300.build`` or
 ``build()`` from Python; ``-Xptxas -v`` output goes to ``_build/ptxas.log``.
 """
@@ -31,12 +31,13 @@ def nvcc() -> str:
 
 
 def _sources():
-    return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
+    return sorted(glob.glob(os.path.join(CSRC, "*.cu")) +
+                  glob.glob(os.path.join(CSRC, "lowp", "*.cu")))
 
 
 def _deps():
-    return _sources() + sorted(glob.glob(os.path.join(CSRC, "*.cuh")) +
-                               glob.glob(os.path.join(CSRC, "*.h")) +
+    return _sources() + sorted(glob.glob(os.path.join(CSRC, "**", "*.cuh"), recursive=True) +
+                               glob.glob(os.path.join(CSRC, "**", "*.h"), recursive=True) +
                                glob.glob(os.path.join(ROOT, "include", "*.h")))
 
 

@@ -15,6 +15,7 @@
 #include <mutex>
 
 #include "../../include/gge.h"
+#include "gge_host.h"
 #include "gge_launch.h"
 #include "gge_params.h"
 #include "gge_sched.cuh"
@@ -24,21 +25,11 @@ namespace {
 
 constexpr int kTileM = 128;
 constexpr int kRowBytesHost = 128;
-constexpr int kMaxSmemOptin = 232448;  // 227 KiB per block on sm_100 / sm_103
-constexpr int kCtrlBytesHost = 1024;
-constexpr int kEpiWarpsHost = 8;          // epilogue warps of the TMA variants (4 with gathers)
 constexpr int kMaxGroupsHost = 1024;
 constexpr int kIdxChunkHost = 2048;       // gather-K index entries staged in shared memory
-constexpr size_t kWorkspaceBytes = 256;
-// the split last wave's tickets (one int32 per tail tile, CTA, epilogue warp and chunk)
-// follow the status words in a region of their own: no other call writes there,
-// so a ticket is never mistaken for another call's data
-constexpr size_t kTicketBytes = 16384;
 constexpr size_t kMapSlotsHost = 16;     // varlen-K tensor-map slots per CTA (kernel kMapSlots)
 constexpr size_t kMapSlotBytesHost = 256;
 constexpr int kMaxStages = 8;            // fewer stages than map slots
-constexpr uint64_t kDefaultTimeoutNs = 2000000000ull;
-constexpr int64_t kMaxExtent = (int64_t(1) << 31) - 1;
 
 using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
                                    const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
@@ -60,6 +51,8 @@ EncodeTiledFn encode_fn() {
   return fn;
 }
 
+}  // namespace
+
 int sm_count() {
   static int cache[64] = {0};
   int dev = 0;
@@ -80,10 +73,6 @@ int elem_bytes(int32_t dt) {
   }
 }
 
-bool is16(int32_t dt) { return dt == GGE_BF16 || dt == GGE_F16; }
-bool is8(int32_t dt) { return dt == GGE_E4M3 || dt == GGE_E5M2; }
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
 gge_status check_view(const gge_tensor& t) {
   // an empty view (no elements) may carry a NULL pointer: it is never dereferenced
   const bool empty = (t.rows == 0 || t.cols == 0);
@@ -97,7 +86,7 @@ gge_status check_view(const gge_tensor& t) {
 }
 
 // An output / C view: [M, N, L] N-major with 16-byte aligned rows and batches.
-gge_status check_mn(const gge_tensor* t, int64_t M, int64_t N, int64_t L, bool is_output) {
+gge_status check_mn(const gge_tensor* t, int64_t M, int64_t N, int64_t L) {
   gge_status s = check_view(*t);
   if (s != GGE_OK) return s;
   if (t->dtype != GGE_BF16 && t->dtype != GGE_F16 && t->dtype != GGE_F32) return GGE_ERR_UNSUPPORTED;
@@ -107,9 +96,13 @@ gge_status check_mn(const gge_tensor* t, int64_t M, int64_t N, int64_t L, bool i
   if (M > 1 && t->stride_row < N) return GGE_ERR_INVALID_ARG;
   if ((t->stride_row * es) % 16 != 0) return GGE_ERR_ALIGNMENT;
   if (L > 1 && (t->stride_batch * es) % 16 != 0) return GGE_ERR_ALIGNMENT;
-  (void)is_output;
   return GGE_OK;
 }
+
+namespace {
+
+bool is16(int32_t dt) { return dt == GGE_BF16 || dt == GGE_F16; }
+bool is8(int32_t dt) { return dt == GGE_E4M3 || dt == GGE_E5M2; }
 
 enum class Form { Plain, Varlen, Gather, GatherVarlen, VarlenK, GatherK };
 
@@ -133,7 +126,6 @@ struct Plan {
 // the split's partial accumulators (one 128 x BN fp32 block per tail tile, slice
 // and CTA) or, for varlen-K and gather-K, the per-CTA tensor-map slots.  Each
 // region starts 256-byte aligned.
-constexpr size_t kTailBase = kWorkspaceBytes + kTicketBytes;
 size_t tail_workspace(const Plan& pl) {
   if (pl.p.tail_tiles <= 0) return 0;
   const int64_t blocks = static_cast<int64_t>(pl.p.tail_tiles) * pl.p.tail_splits * pl.cg;
@@ -154,11 +146,12 @@ CUtensorMapDataType tmap_type(int es) {
 struct TmapKey {
   void* ptr;
   uint64_t d0, d1, d2, s1, s2;
-  uint32_t b0, b1;
+  uint32_t b0, b1, b2;
   int es;
+  bool swizzle;
   bool operator==(const TmapKey& o) const {
     return ptr == o.ptr && d0 == o.d0 && d1 == o.d1 && d2 == o.d2 && s1 == o.s1 && s2 == o.s2 &&
-           b0 == o.b0 && b1 == o.b1 && es == o.es;
+           b0 == o.b0 && b1 == o.b1 && b2 == o.b2 && es == o.es && swizzle == o.swizzle;
   }
 };
 
@@ -176,9 +169,12 @@ TmapCache& tmap_cache() {
   return c;
 }
 
+}  // namespace
+
 gge_status encode_3d(CUtensorMap* m, void* ptr, int es, uint64_t d0, uint64_t d1, uint64_t d2,
-                     uint64_t s1_bytes, uint64_t s2_bytes, uint32_t b0, uint32_t b1) {
-  const TmapKey k{ptr, d0, d1, d2, s1_bytes, s2_bytes, b0, b1, es};
+                     uint64_t s1_bytes, uint64_t s2_bytes, uint32_t b0, uint32_t b1, uint32_t b2,
+                     bool swizzle) {
+  const TmapKey k{ptr, d0, d1, d2, s1_bytes, s2_bytes, b0, b1, b2, es, swizzle};
   TmapCache& c = tmap_cache();
   {
     std::lock_guard<std::mutex> g(c.mu);
@@ -194,11 +190,11 @@ gge_status encode_3d(CUtensorMap* m, void* ptr, int es, uint64_t d0, uint64_t d1
   if (fn == nullptr) return GGE_ERR_CUDA;
   const cuuint64_t dims[3] = {d0, d1, d2};
   const cuuint64_t strides[2] = {s1_bytes, s2_bytes};
-  const cuuint32_t box[3] = {b0, b1, 1};
+  const cuuint32_t box[3] = {b0, b1, b2};
   const cuuint32_t estr[3] = {1, 1, 1};
   CUresult r = fn(m, tmap_type(es), 3, ptr, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                  swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return GGE_ERR_CUDA;
   std::lock_guard<std::mutex> g(c.mu);
   int victim = 0;
@@ -209,6 +205,8 @@ gge_status encode_3d(CUtensorMap* m, void* ptr, int es, uint64_t d0, uint64_t d1
   c.used[victim] = ++c.tick;
   return GGE_OK;
 }
+
+namespace {
 
 uint64_t batch_stride_bytes(const gge_tensor& t, int es) {
   if (t.batch > 1) return static_cast<uint64_t>(t.stride_batch) * es;
@@ -400,9 +398,9 @@ gge_status make_plan(const gge_gemm_args* a, Form form, const int32_t* a_idx,
   // gather-K: A is the source X^T [M, K_src]; the contraction runs over B's columns
   const int64_t K = gk ? a->B.cols : a->A.cols;
   if (M < 0 || N < 0 || K < 0) return GGE_ERR_INVALID_ARG;
-  if (a->D) { s = check_mn(a->D, out_rows, out_cols, L, true); if (s != GGE_OK) return s; }
-  if (a->PostAct) { s = check_mn(a->PostAct, out_rows, out_cols, L, true); if (s != GGE_OK) return s; }
-  if (a->C) { s = check_mn(a->C, out_rows, out_cols, L, false); if (s != GGE_OK) return s; }
+  if (a->D) { s = check_mn(a->D, out_rows, out_cols, L); if (s != GGE_OK) return s; }
+  if (a->PostAct) { s = check_mn(a->PostAct, out_rows, out_cols, L); if (s != GGE_OK) return s; }
+  if (a->C) { s = check_mn(a->C, out_rows, out_cols, L); if (s != GGE_OK) return s; }
   // the caller's output rows are stored in whole 16-byte pieces
   if (out_cols % 8 != 0) return GGE_ERR_UNSUPPORTED;
   // epilogue staging per warp: a 32 x 32 chunk of the widest output
@@ -703,12 +701,16 @@ size_t varlen_k_workspace(const Plan& pl) {
                          kMapSlotBytesHost;
 }
 
+}  // namespace
+
 gge_status check_workspace(void* ws, size_t bytes) {
   if (ws == nullptr) return bytes == 0 ? GGE_OK : GGE_ERR_WORKSPACE;
   if (bytes < kWorkspaceBytes) return GGE_ERR_WORKSPACE;
   if (!aligned16(ws)) return GGE_ERR_ALIGNMENT;
   return GGE_OK;
 }
+
+namespace {
 
 gge_status run(const gge_gemm_args* a, Form form, const int32_t* a_idx, const int32_t* cu,
                int32_t G, bool want_act, bool act_entry, void* ws, size_t ws_bytes,

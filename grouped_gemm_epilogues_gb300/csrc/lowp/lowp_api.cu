@@ -1,0 +1,516 @@
+// Host side of the low-precision entry points: argument checks and launches of
+// the RMS norm, microscaled quantisation and the block-scaled product.
+#include <algorithm>
+#include <cstring>
+#include <mutex>
+
+#include "../gge_host.h"
+#include "lowp_launch.h"
+#include "mx_launch.h"
+
+namespace gge {
+namespace {
+
+using lowp::QuantPtrs;
+
+int mx_block(int32_t f) { return f == GGE_NVFP4 ? 16 : 32; }
+int mx_bits(int32_t f) { return f == GGE_MXFP8 ? 8 : 4; }
+bool mx_known(int32_t f) { return f >= GGE_MXFP8 && f <= GGE_NVFP4; }
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int64_t mx_row_bytes(int32_t f, int64_t cols) { return ceil_div(cols, 32) * 32 * mx_bits(f) / 8; }
+int64_t mx_kgroups(int32_t f, int64_t cols) { return ceil_div(ceil_div(cols, mx_block(f)), 4); }
+
+bool is_value_type(int32_t dt) { return dt == GGE_BF16 || dt == GGE_F16 || dt == GGE_F32; }
+
+gge_status check_mx(const gge_mx_tensor& q) {
+  if (!mx_known(q.format) || q.reserved != 0) return GGE_ERR_INVALID_ARG;
+  if (q.rows < 0 || q.cols < 0 || q.batch < 1) return GGE_ERR_INVALID_ARG;
+  // (cols: whole scale words of columns still have to fit 32 bits)
+  if (q.rows > kMaxExtent || q.cols > kMaxExtent - 128 || q.batch > 65535) return GGE_ERR_UNSUPPORTED;
+  if (q.tensor_scale != nullptr && q.format != GGE_NVFP4) return GGE_ERR_INVALID_ARG;
+  if (q.tensor_scale != nullptr && (reinterpret_cast<uintptr_t>(q.tensor_scale) & 3u) != 0)
+    return GGE_ERR_ALIGNMENT;
+  if (q.rows == 0 || q.cols == 0) return GGE_OK;
+  if (q.codes == nullptr || q.scales == nullptr) return GGE_ERR_INVALID_ARG;
+  const int64_t need = mx_row_bytes(q.format, q.cols);
+  const int64_t block_scales = mx_kgroups(q.format, q.cols) * 512;  // of 128 rows
+  if (q.stride_row < need) return GGE_ERR_INVALID_ARG;
+  if (q.batch > 1 && (q.stride_batch < (q.rows - 1) * q.stride_row + need ||
+                      q.scale_stride_batch < ceil_div(q.rows, 128) * block_scales ||
+                      q.scale_stride_batch % block_scales != 0))
+    return GGE_ERR_INVALID_ARG;
+  if (!aligned16(q.codes) || q.stride_row % 16 != 0 || (q.batch > 1 && q.stride_batch % 16 != 0) ||
+      (reinterpret_cast<uintptr_t>(q.scales) & 127u) != 0)
+    return GGE_ERR_ALIGNMENT;
+  return GGE_OK;
+}
+
+// A row-major (or, `any_major`, column-major) view of 16- or 32-bit values that
+// may start on any element.
+gge_status check_values(const gge_tensor& t, bool any_major) {
+  if (t.reserved != 0) return GGE_ERR_INVALID_ARG;
+  if (!is_value_type(t.dtype)) return GGE_ERR_UNSUPPORTED;
+  if (t.rows < 0 || t.cols < 0 || t.batch < 1) return GGE_ERR_INVALID_ARG;
+  if (t.rows > kMaxExtent || t.cols > kMaxExtent - 128 || t.batch > 65535) return GGE_ERR_UNSUPPORTED;
+  if (t.rows == 0 || t.cols == 0) return GGE_OK;
+  if (t.ptr == nullptr) return GGE_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(t.ptr) & (elem_bytes(t.dtype) - 1)) != 0) return GGE_ERR_ALIGNMENT;
+  if (t.stride_row < 0 || t.stride_col < 0 || t.stride_batch < 0) return GGE_ERR_INVALID_ARG;
+  if (t.cols == 1 || t.stride_col == 1) return GGE_OK;
+  if (any_major && (t.rows == 1 || t.stride_row == 1)) return GGE_OK;
+  return GGE_ERR_UNSUPPORTED;
+}
+
+// Rows of an output must not overlap.
+bool rows_apart(const gge_tensor& t) { return t.rows <= 1 || t.stride_row >= t.cols; }
+
+bool same_shape(const gge_tensor& t, int64_t rows, int64_t cols, int64_t batch) {
+  return t.rows == rows && t.cols == cols && t.batch == batch;
+}
+
+// Every row (and batch) of the view starts on a 16-byte boundary.
+bool rows_aligned(const gge_tensor& t) {
+  const int es = elem_bytes(t.dtype);
+  return aligned16(t.ptr) && (t.rows <= 1 || t.stride_row * es % 16 == 0) &&
+         (t.batch <= 1 || t.stride_batch * es % 16 == 0);
+}
+
+// A quantised output (and its values) as the kernels take it.
+gge_status quant_ptrs(const gge_mx_tensor& q, const gge_tensor* values, QuantPtrs* out) {
+  gge_status s = check_mx(q);
+  if (s != GGE_OK) return s;
+  std::memset(out, 0, sizeof(*out));
+  out->format = q.format;
+  out->codes = static_cast<uint8_t*>(q.codes);
+  out->ld = q.stride_row;
+  out->batch_stride = q.batch > 1 ? q.stride_batch : 0;
+  out->scales = static_cast<uint8_t*>(q.scales);
+  out->kgroups = mx_kgroups(q.format, q.cols);
+  out->scale_batch_stride = q.batch > 1 ? q.scale_stride_batch : 0;
+  out->tensor_scale = q.tensor_scale;
+  if (values != nullptr) {
+    s = check_values(*values, false);
+    if (s != GGE_OK) return s;
+    if (!same_shape(*values, q.rows, q.cols, q.batch) || !rows_apart(*values)) return GGE_ERR_INVALID_ARG;
+    out->values = values->ptr;
+    out->ldv = values->stride_row;
+    out->values_batch_stride = values->batch > 1 ? values->stride_batch : 0;
+    out->v_dtype = values->dtype;
+    out->v_vec = rows_aligned(*values) ? 1 : 0;
+  }
+  return GGE_OK;
+}
+
+gge_status launched(cudaError_t e) { return e == cudaSuccess ? GGE_OK : GGE_ERR_CUDA; }
+
+// ------------------------------------------------------------ the product
+
+struct MxPlan {
+  mx::MxParams mp;
+  mx::MxMaps maps;
+  LaunchShape shape;
+  int tile;
+  int bn, cg;
+  int64_t tiles;
+  int units;
+  bool empty;
+};
+
+int tile_units(int32_t format, int tile, size_t smem) {
+  struct Entry { int dev, format, tile; size_t smem; int units; };
+  static std::mutex mu;
+  static Entry cache[64];
+  static int n = 0;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return -1;
+  {
+    std::lock_guard<std::mutex> g(mu);
+    for (int i = 0; i < n; ++i)
+      if (cache[i].dev == dev && cache[i].format == format && cache[i].tile == tile &&
+          cache[i].smem == smem)
+        return cache[i].units;
+  }
+  int units;
+  {
+    RelaxedCaptureMode relaxed;  // the first query may run inside a stream capture
+    units = format == GGE_MXFP8   ? mx::mx_units<GGE_MXFP8>(tile, smem)
+            : format == GGE_MXFP4 ? mx::mx_units<GGE_MXFP4>(tile, smem)
+                                  : mx::mx_units<GGE_NVFP4>(tile, smem);
+  }
+  if (units > 0) {
+    std::lock_guard<std::mutex> g(mu);
+    if (n < 64) cache[n++] = Entry{dev, format, tile, smem, units};
+  }
+  return units;
+}
+
+constexpr int kFlagsTaken = FLAG_TEST_DROP_ACC_FULL | FLAG_DIRECT_STORES | FLAG_NO_SPLIT | FLAG_RASTER_N;
+constexpr int64_t kTicketsATile = 8 * 4;  // epilogue warps x chunks, a CTA
+
+gge_status plan_mx(const gge_gemm_mx_args* a, void* ws, size_t ws_bytes, MxPlan* out) {
+  if (a == nullptr) return GGE_ERR_INVALID_ARG;
+  MxPlan& pl = *out;
+  std::memset(&pl, 0, sizeof(pl));
+  Params& p = pl.mp.p;
+  const gge_config* cfg = a->config;
+  if (a->reserved != 0 || a->act < GGE_ACT_NONE || a->act > GGE_ACT_RELU_SQ) return GGE_ERR_INVALID_ARG;
+  if (cfg && (cfg->flags & ~kFlagsTaken)) return GGE_ERR_UNSUPPORTED;
+  if (cfg && (cfg->batch_idx_permute != nullptr || cfg->cta_group != 0)) return GGE_ERR_UNSUPPORTED;
+  if (a->D == nullptr && a->PostAct == nullptr) return GGE_ERR_INVALID_ARG;
+  if (a->PostAct == nullptr && a->act != GGE_ACT_NONE) return GGE_ERR_INVALID_ARG;
+  gge_status s = check_mx(a->A);
+  if (s != GGE_OK) return s;
+  s = check_mx(a->B);
+  if (s != GGE_OK) return s;
+  const int32_t format = a->A.format;
+  if (a->B.format != format) return GGE_ERR_UNSUPPORTED;
+  const gge_tensor* o = a->D ? a->D : a->PostAct;
+  const int64_t M = o->rows, N = o->cols, L = o->batch, K = a->A.cols;
+  if (a->A.rows != M || a->B.rows != N || a->B.cols != K || a->A.batch != L || a->B.batch != L)
+    return GGE_ERR_INVALID_ARG;
+  for (const gge_tensor* t : {a->D, a->PostAct, a->C}) {
+    if (t == nullptr) continue;
+    s = check_mn(t, M, N, L);
+    if (s != GGE_OK) return s;
+  }
+  if (N % 8 != 0) return GGE_ERR_UNSUPPORTED;
+  s = check_workspace(ws, ws_bytes);
+  if (s != GGE_OK) return s;
+  pl.empty = M == 0 || N == 0;
+  if (pl.empty) return GGE_OK;
+
+  // tile shape
+  const int sms = sm_count();
+  if (sms <= 0) return GGE_ERR_CUDA;
+  int bn = cfg ? cfg->tile_n : 0;
+  if (bn == 0) {
+    const int64_t pair_tiles = ceil_div(M, 256) * ceil_div(N, 256) * L;
+    bn = M <= 64 ? 64 : (2 * pair_tiles >= sms ? 256 : 128);
+  }
+  if (bn != 256 && bn != 128 && bn != 64) return GGE_ERR_UNSUPPORTED;
+  const bool swap = bn == 64;
+  pl.tile = bn == 256 ? mx::TILE_PAIR_256 : (bn == 128 ? mx::TILE_128 : mx::TILE_SWAP_64);
+  pl.bn = bn;
+  pl.cg = bn == 256 ? 2 : 1;
+  const gge_mx_tensor& ka = swap ? a->B : a->A;  // the kernel's A and B
+  const gge_mx_tensor& kb = swap ? a->A : a->B;
+  const int64_t kM = ka.rows, kN = kb.rows;
+  const int tile_m = 128 * pl.cg;
+  const int64_t tiles_m = ceil_div(kM, tile_m), tiles_n = ceil_div(kN, bn);
+  pl.tiles = tiles_m * tiles_n * L;
+  if (pl.tiles > kMaxExtent / 8) return GGE_ERR_UNSUPPORTED;
+
+  const int bk = 128 * 8 / mx_bits(format);
+  const int groups = bk / (4 * mx_block(format));
+  const int b_tiles = static_cast<int>(ceil_div(bn, 128));
+  // (codes and scales of a stage, in whole KiB: MxCfg::kStageBytes)
+  const int stage = (128 * 128 + bn / pl.cg * 128 + 512 * groups * (1 + b_tiles) + 1023) / 1024 * 1024;
+  const int out_es = std::max(a->D ? elem_bytes(a->D->dtype) : 0,
+                              a->PostAct ? elem_bytes(a->PostAct->dtype) : 0);
+  p.out_stage_bytes = cfg && (cfg->flags & FLAG_DIRECT_STORES) ? 0 : 32 * 32 * out_es;
+  const int fixed = 1024 + kCtrlBytesHost + kEpiWarpsHost * p.out_stage_bytes;
+  int stages = std::min(8, (kMaxSmemOptin - fixed) / stage);
+  if (cfg && cfg->stages > 0) stages = std::min(stages, cfg->stages);
+  if (stages < 2) return GGE_ERR_UNSUPPORTED;
+  pl.shape.smem = static_cast<size_t>(fixed + stages * stage);
+  pl.shape.cluster = pl.cg;
+
+  p.M = static_cast<int32_t>(kM);
+  p.N = static_cast<int32_t>(kN);
+  p.K = static_cast<int32_t>(K);
+  p.L = static_cast<int32_t>(L);
+  p.bk = bk;
+  p.k_tiles = static_cast<int32_t>(ceil_div(K, bk));
+  p.stages = stages;
+  p.tiles_n = static_cast<int32_t>(tiles_n);
+  if (a->D) {
+    p.d = a->D->ptr; p.ldd = a->D->stride_row; p.sbd = a->D->stride_batch; p.d_dtype = a->D->dtype;
+  }
+  if (a->PostAct) {
+    p.post = a->PostAct->ptr; p.ldp = a->PostAct->stride_row; p.sbp = a->PostAct->stride_batch;
+    p.p_dtype = a->PostAct->dtype;
+  }
+  if (a->C) {
+    p.c = a->C->ptr; p.ldc = a->C->stride_row; p.sbc = a->C->stride_batch; p.c_dtype = a->C->dtype;
+  }
+  p.act = a->act;
+  p.out_trans = swap ? 1 : 0;
+  p.alpha = a->alpha;
+  p.beta = a->beta;
+  p.alpha_dev = a->alpha_dev;
+  p.beta_dev = a->beta_dev;
+  // instruction descriptor of the block-scaled kinds: operand formats (e4m3 is 0,
+  // e2m1 is 1 in the 4-bit kinds), N >> 3, power-of-two scales, M >> 4; the kernel
+  // adds the scale bytes' index
+  const uint32_t fmt = format == GGE_MXFP8 ? 0u : 1u;
+  p.idesc = (fmt << 7) | (fmt << 10) | ((static_cast<uint32_t>(bn) >> 3) << 17) |
+            ((format == GGE_NVFP4 ? 0u : 1u) << 23) | ((static_cast<uint32_t>(tile_m) >> 4) << 24);
+  p.flags = cfg ? cfg->flags : 0;
+  p.timeout_ns = (cfg && cfg->timeout_ns) ? cfg->timeout_ns : kDefaultTimeoutNs;
+  p.status = static_cast<int32_t*>(ws);
+  pl.mp.tscale_a = ka.tensor_scale;
+  pl.mp.tscale_b = kb.tensor_scale;
+
+  pl.units = tile_units(format, pl.tile, pl.shape.smem);
+  if (pl.units <= 0) return GGE_ERR_CUDA;
+  if (cfg && cfg->num_ctas > 0) pl.units = std::min(pl.units, std::max(1, cfg->num_ctas / pl.cg));
+  const bool along_n = (p.flags & FLAG_RASTER_N) != 0;
+  const int band = cfg && cfg->raster_band > 0 ? cfg->raster_band
+                                               : auto_band(pl.units, tile_m, bn, along_n);
+  p.sched = PlainSchedule::create(static_cast<int32_t>(tiles_m), static_cast<int32_t>(tiles_n),
+                                  static_cast<int32_t>(L), band, along_n);
+  p.num_tiles = static_cast<int32_t>(pl.tiles);
+  // split the last wave along K, as far as the workspace holds the partial sums
+  if (K > 0 && !(p.flags & FLAG_NO_SPLIT) && ws != nullptr &&
+      (reinterpret_cast<uintptr_t>(ws) & 255u) == 0) {
+    const TailSplit ts = plan_tail_split(pl.tiles, pl.units, p.k_tiles);
+    const int64_t blocks = static_cast<int64_t>(ts.tail) * ts.splits * pl.cg;
+    const size_t need = kTailBase + static_cast<size_t>(blocks) * 128 * bn * sizeof(float);
+    if (ts.tail > 0 && need <= ws_bytes &&
+        static_cast<size_t>(ts.tail) * pl.cg * kTicketsATile * 4 <= kTicketBytes) {
+      p.full_tiles = ts.full;
+      p.tail_tiles = ts.tail;
+      p.tail_splits = ts.splits;
+      p.num_tiles = ts.full + ts.tail * ts.splits;
+      uint8_t* base = static_cast<uint8_t*>(ws);
+      p.tail_tickets = reinterpret_cast<int32_t*>(base + kWorkspaceBytes);
+      p.partials = reinterpret_cast<float*>(base + kTailBase);
+    }
+  }
+  pl.shape.grid = pl.cg * static_cast<int>(std::min<int64_t>(p.num_tiles, pl.units));
+  if (K == 0) return GGE_OK;  // nothing is loaded
+
+  const auto codes_map = [&](CUtensorMap* m, const gge_mx_tensor& q, uint32_t box_rows) {
+    const uint64_t sb = q.batch > 1 ? static_cast<uint64_t>(q.stride_batch)
+                                    : static_cast<uint64_t>(q.rows) * static_cast<uint64_t>(q.stride_row);
+    return encode_3d(m, q.codes, 1, static_cast<uint64_t>(mx_row_bytes(format, K)),
+                     static_cast<uint64_t>(q.rows), static_cast<uint64_t>(q.batch),
+                     static_cast<uint64_t>(q.stride_row), sb, 128, box_rows);
+  };
+  // scale tiles: 256 16-bit elements each, then along K, then row tiles of all batches
+  const int64_t kg = mx_kgroups(format, K);
+  const auto scales_map = [&](CUtensorMap* m, const gge_mx_tensor& q, uint32_t box_tiles, int32_t* a_batch) {
+    const int64_t mine = ceil_div(q.rows, 128);
+    const int64_t step = q.batch > 1 ? q.scale_stride_batch / (kg * 512) : mine;
+    *a_batch = static_cast<int32_t>(step);
+    return encode_3d(m, q.scales, 2, 256, static_cast<uint64_t>(kg),
+                     static_cast<uint64_t>(step * (q.batch - 1) + mine), 512,
+                     static_cast<uint64_t>(kg) * 512, 256, static_cast<uint32_t>(groups), box_tiles,
+                     false);
+  };
+  s = codes_map(&pl.maps.a, ka, 128);
+  if (s == GGE_OK) s = codes_map(&pl.maps.b, kb, static_cast<uint32_t>(bn / pl.cg));
+  if (s == GGE_OK) s = scales_map(&pl.maps.sa, ka, 1, &pl.mp.sfa_batch);
+  if (s == GGE_OK) s = scales_map(&pl.maps.sb, kb, static_cast<uint32_t>(b_tiles), &pl.mp.sfb_batch);
+  return s;
+}
+
+}  // namespace
+}  // namespace gge
+
+using namespace gge;
+
+extern "C" {
+
+size_t gge_mx_row_bytes(int32_t format, int64_t cols) {
+  if (!mx_known(format) || cols < 0) return 0;
+  return static_cast<size_t>(mx_row_bytes(format, cols));
+}
+
+size_t gge_mx_scale_bytes(int32_t format, int64_t rows, int64_t cols) {
+  if (!mx_known(format) || rows < 0 || cols < 0) return 0;
+  return static_cast<size_t>(ceil_div(rows, 128)) * static_cast<size_t>(mx_kgroups(format, cols)) * 512;
+}
+
+gge_status gge_mx_quantize(const gge_tensor* x, const gge_mx_tensor* q, const gge_tensor* values,
+                           gge_stream_t stream) {
+  if (x == nullptr || q == nullptr) return GGE_ERR_INVALID_ARG;
+  gge_status s = check_values(*x, true);
+  if (s != GGE_OK) return s;
+  lowp::QuantParams p;
+  std::memset(&p, 0, sizeof(p));
+  s = quant_ptrs(*q, values, &p.q);
+  if (s != GGE_OK) return s;
+  if (!same_shape(*x, q->rows, q->cols, q->batch)) return GGE_ERR_INVALID_ARG;
+  if (x->rows == 0 || x->cols == 0) return GGE_OK;
+  p.rows = x->rows;
+  p.cols = x->cols;
+  p.batch = x->batch;
+  p.dtype = x->dtype;
+  p.x = x->ptr;
+  p.stride_row = x->stride_row;
+  p.stride_col = x->stride_col;
+  p.stride_batch = x->batch > 1 ? x->stride_batch : 0;
+  // (a transposed view: its contiguous dimension is the rows)
+  if (x->cols == 1 || x->stride_col == 1) {
+    p.vec = rows_aligned(*x) ? 1 : 0;
+  } else {
+    const int es = elem_bytes(x->dtype);
+    p.vec = aligned16(x->ptr) && x->stride_col * es % 16 == 0 &&
+                    (x->batch <= 1 || x->stride_batch * es % 16 == 0) ? 1 : 0;
+    if (x->cols > 65535 * int64_t(128)) return GGE_ERR_UNSUPPORTED;
+  }
+  const int sms = sm_count();
+  if (sms <= 0) return GGE_ERR_CUDA;
+  return launched(lowp::launch_quantize(p, sms, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+gge_status gge_mx_dequantize(const gge_mx_tensor* q, const gge_tensor* y, gge_stream_t stream) {
+  if (q == nullptr || y == nullptr) return GGE_ERR_INVALID_ARG;
+  gge_status s = check_mx(*q);
+  if (s != GGE_OK) return s;
+  s = check_values(*y, false);
+  if (s != GGE_OK) return s;
+  if (!same_shape(*y, q->rows, q->cols, q->batch) || !rows_apart(*y)) return GGE_ERR_INVALID_ARG;
+  if (q->rows == 0 || q->cols == 0) return GGE_OK;
+  lowp::DequantParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.rows = q->rows;
+  p.cols = q->cols;
+  p.batch = q->batch;
+  p.format = q->format;
+  p.codes = static_cast<const uint8_t*>(q->codes);
+  p.scales = static_cast<const uint8_t*>(q->scales);
+  p.ld = q->stride_row;
+  p.batch_stride = q->batch > 1 ? q->stride_batch : 0;
+  p.kgroups = mx_kgroups(q->format, q->cols);
+  p.scale_batch_stride = q->batch > 1 ? q->scale_stride_batch : 0;
+  p.tensor_scale = q->tensor_scale;
+  p.y = y->ptr;
+  p.ldy = y->stride_row;
+  p.y_batch_stride = y->batch > 1 ? y->stride_batch : 0;
+  p.dtype = y->dtype;
+  p.vec = rows_aligned(*y) ? 1 : 0;
+  const int sms = sm_count();
+  if (sms <= 0) return GGE_ERR_CUDA;
+  return launched(lowp::launch_dequantize(p, sms, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+gge_status gge_gemm_mx(const gge_gemm_mx_args* args, void* ws, size_t ws_bytes, gge_stream_t stream) {
+  MxPlan pl;
+  const gge_status s = plan_mx(args, ws, ws_bytes, &pl);
+  if (s != GGE_OK || pl.empty) return s;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const int32_t format = args->A.format;
+  const cudaError_t e =
+      format == GGE_MXFP8   ? mx::launch_mx<GGE_MXFP8>(pl.tile, pl.maps, pl.mp, pl.shape, st)
+      : format == GGE_MXFP4 ? mx::launch_mx<GGE_MXFP4>(pl.tile, pl.maps, pl.mp, pl.shape, st)
+                            : mx::launch_mx<GGE_NVFP4>(pl.tile, pl.maps, pl.mp, pl.shape, st);
+  return launched(e);
+}
+
+gge_status gge_rmsnorm(const gge_rmsnorm_args* a, gge_stream_t stream) {
+  if (a == nullptr) return GGE_ERR_INVALID_ARG;
+  const gge_tensor& x = a->x;
+  gge_status s = check_values(x, false);
+  if (s != GGE_OK) return s;
+  if (x.batch != 1) return GGE_ERR_UNSUPPORTED;
+  if (!is_value_type(a->weight_dtype)) return GGE_ERR_UNSUPPORTED;
+  lowp::NormParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.q.format = 3;  // no quantised output
+  bool vec = rows_aligned(x) && aligned16(a->weight);
+  const auto take = [&](const gge_tensor* t, bool output) {
+    if (t == nullptr) return GGE_OK;
+    const gge_status r = check_values(*t, false);
+    if (r != GGE_OK) return r;
+    if (t->dtype != x.dtype) return GGE_ERR_UNSUPPORTED;
+    if (!same_shape(*t, x.rows, x.cols, 1) || (output && !rows_apart(*t))) return GGE_ERR_INVALID_ARG;
+    vec = vec && rows_aligned(*t);
+    return GGE_OK;
+  };
+  if ((s = take(a->residual, false)) != GGE_OK) return s;
+  if ((s = take(a->residual_out, true)) != GGE_OK) return s;
+  if ((s = take(a->y, true)) != GGE_OK) return s;
+  if (a->residual_out != nullptr && a->residual == nullptr) return GGE_ERR_INVALID_ARG;
+  if (a->values != nullptr && a->q == nullptr) return GGE_ERR_INVALID_ARG;
+  if (a->q != nullptr) {
+    s = quant_ptrs(*a->q, a->values, &p.q);
+    if (s != GGE_OK) return s;
+    if (a->q->rows != x.rows || a->q->cols != x.cols || a->q->batch != 1) return GGE_ERR_INVALID_ARG;
+  }
+  if (x.rows == 0 || x.cols == 0) return GGE_OK;
+  if (a->weight == nullptr) return GGE_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(a->weight) & (elem_bytes(a->weight_dtype) - 1)) != 0 ||
+      (reinterpret_cast<uintptr_t>(a->inv_rms) & 3u) != 0)
+    return GGE_ERR_ALIGNMENT;
+  p.rows = x.rows;
+  p.cols = static_cast<int32_t>(x.cols);
+  p.dtype = x.dtype;
+  p.x = x.ptr;
+  p.ldx = x.stride_row;
+  if (a->residual) { p.residual = a->residual->ptr; p.ldr = a->residual->stride_row; }
+  if (a->residual_out) { p.h = a->residual_out->ptr; p.ldh = a->residual_out->stride_row; }
+  if (a->y) { p.y = a->y->ptr; p.ldy = a->y->stride_row; }
+  p.weight = a->weight;
+  p.w_dtype = a->weight_dtype;
+  p.eps = a->eps;
+  p.inv = a->inv_rms;
+  p.vec = vec ? 1 : 0;
+  const int sms = sm_count();
+  if (sms <= 0) return GGE_ERR_CUDA;
+  return launched(lowp::launch_norm(p, sms, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t gge_workspace_size_rmsnorm_bwd(int64_t cols) {
+  const int sms = sm_count();
+  if (sms <= 0 || cols < 0) return 0;
+  return kTailBase + static_cast<size_t>(lowp::norm_bwd_blocks(kMaxExtent, sms)) *
+                         static_cast<size_t>(cols) * sizeof(float);
+}
+
+gge_status gge_rmsnorm_bwd(const gge_rmsnorm_bwd_args* a, void* ws, size_t ws_bytes,
+                           gge_stream_t stream) {
+  if (a == nullptr || a->reserved != 0) return GGE_ERR_INVALID_ARG;
+  const gge_tensor& dy = a->dy;
+  gge_status s = check_values(dy, false);
+  if (s != GGE_OK) return s;
+  if (dy.batch != 1) return GGE_ERR_UNSUPPORTED;
+  if (!is_value_type(a->weight_dtype)) return GGE_ERR_UNSUPPORTED;
+  bool vec = rows_aligned(dy) && aligned16(a->weight);
+  for (const gge_tensor* t : {&a->h, a->dh, &a->dx}) {
+    if (t == nullptr) continue;
+    s = check_values(*t, false);
+    if (s != GGE_OK) return s;
+    if (t->dtype != dy.dtype) return GGE_ERR_UNSUPPORTED;
+    if (!same_shape(*t, dy.rows, dy.cols, 1)) return GGE_ERR_INVALID_ARG;
+    vec = vec && rows_aligned(*t);
+  }
+  if (!rows_apart(a->dx)) return GGE_ERR_INVALID_ARG;
+  if (dy.cols == 0 || (dy.rows == 0 && a->dweight == nullptr)) return GGE_OK;
+  if (a->weight == nullptr || (a->inv_rms == nullptr && dy.rows > 0)) return GGE_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(a->weight) & (elem_bytes(a->weight_dtype) - 1)) != 0 ||
+      (reinterpret_cast<uintptr_t>(a->inv_rms) & 3u) != 0 ||
+      (reinterpret_cast<uintptr_t>(a->dweight) & 3u) != 0)
+    return GGE_ERR_ALIGNMENT;
+  lowp::NormBwdParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.rows = dy.rows;
+  p.cols = static_cast<int32_t>(dy.cols);
+  p.dtype = dy.dtype;
+  p.dy = dy.ptr;
+  p.lddy = dy.stride_row;
+  p.h = a->h.ptr;
+  p.ldh = a->h.stride_row;
+  if (a->dh) { p.dh = a->dh->ptr; p.lddh = a->dh->stride_row; }
+  p.dx = a->dx.ptr;
+  p.lddx = a->dx.stride_row;
+  p.weight = a->weight;
+  p.w_dtype = a->weight_dtype;
+  p.inv = a->inv_rms;
+  p.dw = a->dweight;
+  p.vec = vec ? 1 : 0;
+  const int sms = sm_count();
+  if (sms <= 0) return GGE_ERR_CUDA;
+  if (a->dweight != nullptr) {
+    if (ws == nullptr) return GGE_ERR_WORKSPACE;
+    if ((reinterpret_cast<uintptr_t>(ws) & 255u) != 0) return GGE_ERR_ALIGNMENT;
+    if (ws_bytes < kTailBase + static_cast<size_t>(lowp::norm_bwd_blocks(dy.rows, sms)) *
+                                   static_cast<size_t>(dy.cols) * sizeof(float))
+      return GGE_ERR_WORKSPACE;
+    p.partials = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kTailBase);
+  }
+  return launched(lowp::launch_norm_bwd(p, sms, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"

@@ -1,0 +1,103 @@
+// Kernel parameters and launchers of the low-precision operators: RMS norm
+// (forward and backward) and microscaled quantisation.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+namespace gge {
+namespace lowp {
+
+// A quantised output as the kernels see it (see mx::QuantOut).
+struct QuantPtrs {
+  int32_t format;  // gge_mx_format, or mx::FMT_NONE
+  uint8_t* codes;
+  int64_t ld, batch_stride;
+  uint8_t* scales;
+  int64_t kgroups, scale_batch_stride;
+  const float* tensor_scale;
+  void* values;
+  int64_t ldv, values_batch_stride;
+  int32_t v_dtype, v_vec;
+};
+
+struct NormParams {
+  int64_t rows;
+  int32_t cols;
+  int32_t dtype;  // of x, residual, residual_out and y
+  const void *x, *residual;
+  void *h, *y;  // residual_out, y (each may be NULL)
+  int64_t ldx, ldr, ldh, ldy;
+  const void* weight;
+  int32_t w_dtype;
+  float eps;
+  float* inv;  // NULL: not wanted
+  QuantPtrs q;
+  int32_t vec;  // every row of every tensor starts on a 16-byte boundary
+};
+
+struct NormBwdParams {
+  int64_t rows;
+  int32_t cols;
+  int32_t dtype;  // of dy, h, dh and dx
+  const void *dy, *h, *dh;
+  void* dx;
+  int64_t lddy, ldh, lddh, lddx;
+  const void* weight;
+  int32_t w_dtype;
+  const float* inv;
+  float* dw;        // NULL: not wanted
+  float* partials;  // [grid][cols] sums of the blocks' rows
+  int32_t vec;
+};
+
+struct QuantParams {
+  int64_t rows, cols;
+  int64_t batch;
+  int32_t dtype;
+  const void* x;
+  int64_t stride_row, stride_col, stride_batch;  // elements; one of the first two is 1
+  int32_t vec;  // 16-byte pieces of the contiguous dimension
+  QuantPtrs q;
+};
+
+struct DequantParams {
+  int64_t rows, cols, batch;
+  int32_t format;
+  const uint8_t *codes, *scales;
+  int64_t ld, batch_stride, kgroups, scale_batch_stride;
+  const float* tensor_scale;
+  void* y;
+  int64_t ldy, y_batch_stride;
+  int32_t dtype, vec;
+};
+
+cudaError_t launch_norm(const NormParams& p, int sms, cudaStream_t st);
+// Blocks a backward launch uses at most (each leaves `cols` partial sums).
+int norm_bwd_blocks(int64_t rows, int sms);
+cudaError_t launch_norm_bwd(const NormBwdParams& p, int sms, cudaStream_t st);
+cudaError_t launch_quantize(const QuantParams& p, int sms, cudaStream_t st);
+cudaError_t launch_dequantize(const DequantParams& p, int sms, cudaStream_t st);
+
+// Launch with programmatic stream serialisation: the kernel sets up, then waits
+// (griddepcontrol.wait) for the stream's previous kernel before it touches
+// global memory.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
+                       Args... args) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+}  // namespace lowp
+}  // namespace gge

@@ -1,0 +1,105 @@
+// Shared body of the block-scaled product's translation units.
+#pragma once
+
+#include <atomic>
+
+#include "mx_gemm.cuh"
+
+namespace gge {
+namespace mx {
+
+template <int BN, int CG, int FMT, bool TR>
+cudaError_t mx_smem_limit(size_t smem) {
+  // the dynamic shared-memory limit is a per-device function attribute
+  static std::atomic<size_t> smem_set[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64 || smem_set[dev].load() < smem) {
+    RelaxedCaptureMode relaxed;
+    e = cudaFuncSetAttribute(mx_gemm_kernel<BN, CG, FMT, TR>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) smem_set[dev].store(smem);
+  }
+  return cudaSuccess;
+}
+
+template <int BN, int CG, int FMT, bool TR>
+cudaLaunchConfig_t mx_config(int grid, size_t smem, cudaStream_t stream, cudaLaunchAttribute* attr) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid, 1, 1);
+  cfg.blockDim = dim3(MxCfg<BN, CG, FMT>::kThreads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.numAttrs = 1;
+  if (CG == 2) {
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = CG;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.numAttrs = 2;
+  }
+  return cfg;
+}
+
+template <int BN, int CG, int FMT, bool TR>
+cudaError_t mx_launch_one(const MxMaps& m, const MxParams& mp, const LaunchShape& shape,
+                          cudaStream_t stream) {
+  const cudaError_t e = mx_smem_limit<BN, CG, FMT, TR>(shape.smem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr[2];
+  const cudaLaunchConfig_t cfg = mx_config<BN, CG, FMT, TR>(shape.grid, shape.smem, stream, attr);
+  return cudaLaunchKernelEx(&cfg, mx_gemm_kernel<BN, CG, FMT, TR>, m.a, m.b, m.sa, m.sb, mp);
+}
+
+template <int BN, int CG, int FMT, bool TR>
+int mx_units_one(size_t smem) {
+  if (mx_smem_limit<BN, CG, FMT, TR>(smem) != cudaSuccess) return -1;
+  if (CG == 1) {
+    int per_sm = 0, dev = 0, sms = 0;
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, mx_gemm_kernel<BN, CG, FMT, TR>,
+                                                      MxCfg<BN, CG, FMT>::kThreads, smem) != cudaSuccess ||
+        cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+      return -1;
+    return per_sm * sms;
+  }
+  cudaLaunchAttribute attr[2];
+  cudaLaunchConfig_t cfg = mx_config<BN, CG, FMT, TR>(CG * 64, smem, nullptr, attr);
+  cfg.attrs = attr + 1;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, mx_gemm_kernel<BN, CG, FMT, TR>, &cfg) != cudaSuccess) return -1;
+  return n;
+}
+
+template <int FMT>
+cudaError_t launch_mx(int tile, const MxMaps& maps, const MxParams& mp, const LaunchShape& shape,
+                      cudaStream_t stream) {
+  switch (tile) {
+    case TILE_PAIR_256: return mx_launch_one<256, 2, FMT, false>(maps, mp, shape, stream);
+    case TILE_128: return mx_launch_one<128, 1, FMT, false>(maps, mp, shape, stream);
+    default: return mx_launch_one<64, 1, FMT, true>(maps, mp, shape, stream);
+  }
+}
+
+template <int FMT>
+int mx_units(int tile, size_t smem) {
+  switch (tile) {
+    case TILE_PAIR_256: return mx_units_one<256, 2, FMT, false>(smem);
+    case TILE_128: return mx_units_one<128, 1, FMT, false>(smem);
+    default: return mx_units_one<64, 1, FMT, true>(smem);
+  }
+}
+
+#define GGE_MX_INSTANTIATE(FMT)                                                                    \
+  template cudaError_t launch_mx<FMT>(int, const MxMaps&, const MxParams&, const LaunchShape&,   \
+                                      cudaStream_t);                                              \
+  template int mx_units<FMT>(int, size_t);
+
+}  // namespace mx
+}  // namespace gge

@@ -303,6 +303,148 @@ gge_status gge_gemm_gather_a(const gge_gemm_args* args, const int32_t* a_idx,
                              const int32_t* cu_seqlens_m, int32_t num_groups, void* workspace,
                              size_t workspace_bytes, gge_stream_t stream);
 
+/* ---- low-precision linear layers ----------------------------------------
+ * Microscaled operands (narrow codes, one scale per block of K), what makes
+ * them (quantisation, and the RMS norm that ends in one), their product, and
+ * the norm's backward.  The pages have no counterpart: these are additions of
+ * this library.  The conventions above hold (asynchronous on `stream`,
+ * validated before any launch, strides in elements unless a field says bytes). */
+
+/* Formats.  value = code * block scale (* the tensor scale, GGE_NVFP4).
+ *   GGE_MXFP8  e4m3 codes, blocks of 32, scales 2^(byte - 127), byte 255 = NaN
+ *   GGE_MXFP4  e2m1 codes, blocks of 32, scales as above
+ *   GGE_NVFP4  e2m1 codes, blocks of 16, e4m3 scales, one fp32 scale a tensor   */
+typedef enum gge_mx_format { GGE_MXFP8 = 0, GGE_MXFP4 = 1, GGE_NVFP4 = 2 } gge_mx_format;
+
+/*
+ * A microscaled matrix [rows, cols, batch] whose blocks run along cols (a
+ * product's K).
+ *   codes  row-major; two 4-bit codes a byte, the even column in the low half.
+ *          A row takes gge_mx_row_bytes bytes (whole 32s of columns; the codes
+ *          past `cols` are zero).  16-byte aligned, as are the byte strides.
+ *   scales tiles of 512 bytes for 128 rows x 4 blocks, ceil(blocks / 4) tiles
+ *          along K for each 128 rows: the scale of row r, block b is byte
+ *          (r % 32) * 16 + (r % 128 / 32) * 4 + b % 4 of tile [r / 128][b / 4].
+ *          Bytes of blocks past the row's last one are zero; rows past the last
+ *          one may hold anything.  gge_mx_scale_bytes in all, 128-byte aligned.
+ */
+typedef struct gge_mx_tensor {
+  void* codes;
+  void* scales;
+  const float* tensor_scale; /* device scalar (GGE_NVFP4; NULL: 1), must be > 0   */
+  int32_t format;            /* gge_mx_format                                     */
+  int32_t reserved;          /* must be 0                                         */
+  int64_t rows, cols, batch;
+  int64_t stride_row;        /* BYTES between rows of codes                       */
+  int64_t stride_batch;      /* BYTES between batches of codes                    */
+  int64_t scale_stride_batch; /* BYTES between batches of scales (a multiple of a
+                                128-row block's scales)                           */
+} gge_mx_tensor;
+
+/* Bytes of one row of codes, and of one batch's scales (0 for a bad format). */
+size_t gge_mx_row_bytes(int32_t format, int64_t cols);
+size_t gge_mx_scale_bytes(int32_t format, int64_t rows, int64_t cols);
+
+/* q = x quantised.  x: [rows, cols, batch] in bf16, f16 or f32, with
+ * stride_col == 1 or stride_row == 1 (the transpose of a row-major matrix, as
+ * the weight-gradient products need it); rows may start on any element.
+ *   GGE_MXFP8, GGE_MXFP4: a block's scale is the smallest power of two 2^e (e >=
+ *     -127) with max|x| <= 2^e * (448 or 6); code = round(x / 2^e), exact but for
+ *     the rounding (to nearest, ties to even).
+ *   GGE_NVFP4, t the tensor scale: scale s = e4m3(min(max(max|x| / (6 t), 2^-9),
+ *     448)), code = round(x * (1 / (s t))) in fp32 arithmetic, at most 6 in size.
+ *     t = max over the tensor / (6 * 448) uses the scales' whole range.
+ * A block that holds an infinity or a NaN becomes NaN throughout.
+ * values (may be NULL): the numbers that the codes stand for, [rows, cols,
+ * batch] row-major in bf16, f16 or f32 (rounded once). */
+gge_status gge_mx_quantize(const gge_tensor* x, const gge_mx_tensor* q, const gge_tensor* values,
+                           gge_stream_t stream);
+
+/* y = the numbers that q's codes stand for, row-major in bf16, f16 or f32. */
+gge_status gge_mx_dequantize(const gge_mx_tensor* q, const gge_tensor* y, gge_stream_t stream);
+
+/*
+ * D       = alpha * tA * tB * sum_k (a_k sa_k) (b_k sb_k) + beta * C
+ * PostAct = act(same value, before rounding)
+ *   A [M, K, L] and B [N, K, L] of one format (tA, tB: their tensor scales);
+ *   C, D, PostAct, act, alpha, beta as in gge_gemm_act (D and PostAct each
+ *   optional, not both NULL; PostAct required when act is not NONE).  N must be
+ *   a multiple of 8, M, K and L may be anything.  K == 0 gives beta * C.
+ *   config (may be NULL): tile_n 0 (automatic), 256 (a CTA pair, 256 x 256), 128
+ *   (one CTA, 128 x 128) or 64 (one CTA, for few rows of A: the roles of A and B
+ *   are exchanged); num_ctas, raster_band, stages, timeout_ns; of the flags
+ *   those for direct stores, no split, raster along N and the test hook.
+ * The workspace is gge_workspace_size's (it may be smaller, and then no tile is
+ * split along K).
+ */
+typedef struct gge_gemm_mx_args {
+  gge_mx_tensor A;
+  gge_mx_tensor B;
+  const gge_tensor* C;
+  const gge_tensor* D;
+  const gge_tensor* PostAct;
+  float alpha;
+  float beta;
+  const float* alpha_dev;
+  const float* beta_dev;
+  int32_t act;
+  int32_t reserved;
+  const gge_config* config;
+} gge_gemm_mx_args;
+gge_status gge_gemm_mx(const gge_gemm_mx_args* args, void* workspace, size_t workspace_bytes,
+                       gge_stream_t stream);
+
+/*
+ * RMS norm with the residual's addition:
+ *   h = round(x + residual)  (h = x without one)
+ *   inv = 1 / sqrt(mean over a row of h^2 + eps)       y = (h * inv) * weight
+ *   x, residual, residual_out (h), y: [rows, cols, 1] of one type (bf16, f16 or
+ *     f32), stride_col == 1, rows may start on any element; every output may be
+ *     NULL, and residual_out may be x or residual itself.  residual_out is
+ *     written only when there is a residual.
+ *   weight: `cols` contiguous values of weight_dtype.  inv_rms: fp32 [rows].
+ *   q, values: y quantised from fp32 as gge_mx_quantize does, and the numbers
+ *     that its codes stand for (values needs q).
+ */
+typedef struct gge_rmsnorm_args {
+  gge_tensor x;
+  const gge_tensor* residual;
+  const gge_tensor* residual_out;
+  const gge_tensor* y;
+  const gge_mx_tensor* q;
+  const gge_tensor* values;
+  const void* weight;
+  int32_t weight_dtype; /* gge_dtype */
+  float eps;
+  float* inv_rms;
+} gge_rmsnorm_args;
+gge_status gge_rmsnorm(const gge_rmsnorm_args* args, gge_stream_t stream);
+
+/*
+ * Its backward, from the saved h and inv_rms:
+ *   g = dy * weight      dx = inv * (g - h * inv^2 * mean(g * h)) + dh
+ *   dweight = sum over rows of dy * (h * inv)     (fp32, in a fixed order)
+ * dx is the gradient of x and of the residual alike.  dh (may be NULL): the
+ * gradient that reaches residual_out directly.  dy, h, dh and dx: [rows, cols, 1]
+ * of one type; dx may be dy, h or dh itself.  dweight may be NULL.  A quantised
+ * output's dy passes through unchanged.  The workspace (256-byte aligned) must hold
+ * gge_workspace_size_rmsnorm_bwd(cols) bytes when dweight is given.
+ */
+typedef struct gge_rmsnorm_bwd_args {
+  gge_tensor dy;
+  gge_tensor h;
+  const gge_tensor* dh;
+  gge_tensor dx;
+  const void* weight;
+  int32_t weight_dtype;
+  int32_t reserved;
+  const float* inv_rms;
+  float* dweight;
+} gge_rmsnorm_bwd_args;
+size_t gge_workspace_size_rmsnorm_bwd(int64_t cols);
+gge_status gge_rmsnorm_bwd(const gge_rmsnorm_bwd_args* args, void* workspace,
+                           size_t workspace_bytes, gge_stream_t stream);
+
 /* gge_gemm_act without a caller workspace, for callers that cannot allocate
  * device memory where they run the GEMM (a host framework that owns all device
  * memory through its own arena or caching allocator, or a latency-critical path
