@@ -146,6 +146,8 @@ class GgeError(RuntimeError):
 def load(path: str = None, build_if_missing: bool = True) -> ctypes.CDLL:
     """Load libgge.so (building it in-tree first if it is missing)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -509,48 +511,82 @@ class MxTensor:
     uint8, scales a contiguous uint8 tensor of gge_mx_scale_bytes a batch, tensor_scale None
     or a one-element fp32 tensor on the device (nvfp4)."""
 
-    __slots__ = ("codes", "scales", "format", "rows", "cols", "batch", "tensor_scale", "c")
+    __slots__ = ("format", "rows", "cols", "batch", "tensor_scale", "device", "c", "_codes",
+                 "_scales", "_buffer")
 
     def __init__(self, codes, scales, format, rows, cols, tensor_scale=None):
         fmt = MX_FORMAT[format]
-        if codes.dtype != torch.uint8 or scales.dtype != torch.uint8:
-            raise TypeError("MxTensor: codes and scales are uint8 tensors")
-        if codes.dim() not in (2, 3):
+        shape, stride = codes.shape, codes.stride()
+        if len(shape) == 2:
+            batch, step = 1, 0
+        elif len(shape) == 3:
+            batch, step = shape[0], stride[0]
+        else:
             raise ValueError("MxTensor: codes are 2-D or 3-D (batch first)")
-        batch = codes.shape[0] if codes.dim() == 3 else 1
-        if codes.shape[-2] != rows or codes.shape[-1] != _mx_row_bytes(fmt, cols) or \
-                (codes.numel() and codes.stride(-1) != 1):
+        if codes.dtype is not torch.uint8 or scales.dtype is not torch.uint8:
+            raise TypeError("MxTensor: codes and scales are uint8 tensors")
+        if shape[-2] != rows or shape[-1] != _mx_row_bytes(fmt, cols) or \
+                (stride[-1] != 1 and codes.numel() > 0):
             raise ValueError("MxTensor: codes do not match rows, cols and format")
         per = _mx_scale_bytes(fmt, rows, cols)
         if scales.numel() != batch * per or not scales.is_contiguous():
             raise ValueError("MxTensor: scales do not match rows, cols and format")
-        if tensor_scale is not None and (tensor_scale.dtype != torch.float32 or
-                                         tensor_scale.numel() != 1):
-            raise ValueError("MxTensor: tensor_scale is one fp32 value")
-        if scales.device != codes.device or (tensor_scale is not None and
-                                             tensor_scale.device != codes.device):
-            raise ValueError("MxTensor: codes, scales and tensor_scale on different devices")
-        self.codes, self.scales, self.format = codes, scales, format
-        self.rows, self.cols, self.batch, self.tensor_scale = rows, cols, batch, tensor_scale
-        self.c = GgeMxTensor(codes.data_ptr(), scales.data_ptr(),
-                             tensor_scale.data_ptr() if tensor_scale is not None else None, fmt, 0,
-                             rows, cols, batch, codes.stride(-2),
-                             codes.stride(0) if batch > 1 else 0, per)
+        self.device = codes.device
+        t = None
+        if tensor_scale is not None:
+            if tensor_scale.dtype is not torch.float32 or tensor_scale.numel() != 1:
+                raise ValueError("MxTensor: tensor_scale is one fp32 value")
+            _same_device(self.device, tensor_scale)
+            t = tensor_scale.data_ptr()
+        _same_device(self.device, scales)
+        self.format, self.rows, self.cols, self.batch = format, rows, cols, batch
+        self.tensor_scale, self._codes, self._scales, self._buffer = tensor_scale, codes, scales, None
+        self.c = GgeMxTensor(codes.data_ptr(), scales.data_ptr(), t, fmt, 0, rows, cols, batch,
+                             stride[-2], step, per)
+
+    @property
+    def codes(self):
+        if self._codes is None:   # mx_empty: a view of its one buffer, made when asked for
+            c, row = self.c, self.c.stride_row
+            if c.stride_batch:
+                self._codes = self._buffer.as_strided((c.batch, c.rows, row), (c.stride_batch, row, 1))
+            else:
+                self._codes = self._buffer.as_strided((c.rows, row), (row, 1))
+        return self._codes
+
+    @property
+    def scales(self):
+        if self._scales is None:
+            c = self.c
+            self._scales = self._buffer.as_strided((c.batch * c.scale_stride_batch,), (1,),
+                                                   c.scales - c.codes)
+        return self._scales
 
 
 def mx_empty(rows, cols, format, device=None, batch=None, tensor_scale=None):
     """An MxTensor with room for (rows, cols) or (batch, rows, cols) values: its codes and
     scales share one allocation."""
     fmt = MX_FORMAT[format]
-    dev = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
+    if device is None:
+        device = torch.device("cuda", torch.cuda.current_device())
+    row, per = _mx_row_bytes(fmt, cols), _mx_scale_bytes(fmt, rows, cols)
     b = 1 if batch is None else batch
-    row = _mx_row_bytes(fmt, cols)
-    n_codes, n_scales = b * rows * row, b * _mx_scale_bytes(fmt, rows, cols)
-    start = (n_codes + 511) // 512 * 512
-    buf = torch.empty(start + n_scales, dtype=torch.uint8, device=dev)
-    shape, stride = ((rows, row), (row, 1)) if batch is None else ((b, rows, row), (rows * row, row, 1))
-    return MxTensor(buf.as_strided(shape, stride), buf.as_strided((n_scales,), (1,), start), format,
-                    rows, cols, tensor_scale)
+    start = (b * rows * row + 511) & ~511
+    q = MxTensor.__new__(MxTensor)
+    q._buffer = buf = torch.empty(start + b * per, dtype=torch.uint8, device=device)
+    q.device = buf.device
+    t = None
+    if tensor_scale is not None:
+        if tensor_scale.dtype is not torch.float32 or tensor_scale.numel() != 1:
+            raise ValueError("mx_empty: tensor_scale is one fp32 value")
+        _same_device(q.device, tensor_scale)
+        t = tensor_scale.data_ptr()
+    q.format, q.rows, q.cols, q.batch, q.tensor_scale = format, rows, cols, b, tensor_scale
+    q._codes = q._scales = None
+    ptr = buf.data_ptr()
+    q.c = GgeMxTensor(ptr, ptr + start, t, fmt, 0, rows, cols, b, row,
+                      0 if batch is None else rows * row, per)
+    return q
 
 
 def _same_device(device, *tensors):
@@ -559,59 +595,111 @@ def _same_device(device, *tensors):
             raise ValueError("tensors on different devices")
 
 
-def _ref(struct):
-    return ctypes.addressof(struct) if struct is not None else None
+def _tensor(t, kind):
+    """The C view of a tensor, as view() makes it."""
+    shape, stride = t.shape, t.stride()
+    code = DTYPE.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{kind}: unsupported dtype {t.dtype}")
+    if len(shape) == 2:
+        return GgeTensor(t.data_ptr(), code, 0, shape[0], shape[1], 1, stride[0], stride[1], 0)
+    if len(shape) == 3:
+        return GgeTensor(t.data_ptr(), code, 0, shape[1], shape[2], shape[0], stride[1], stride[2],
+                         stride[0])
+    raise ValueError(f"{kind}: expected a 2-D or 3-D tensor")
 
 
-def _view_or_none(t, kind):
-    return view(t, kind) if t is not None else None
+def _output(t, kind, device):
+    """The address of an optional tensor's C view (0: none), and the view to keep."""
+    if t is None:
+        return None, None
+    if t.device != device:
+        raise ValueError(f"{kind}: tensors on different devices")
+    v = _tensor(t, kind)
+    return _address(v), v
+
+
+_address = ctypes.addressof
+
+
+def _vector(t, kind, device, n, dtype=None):
+    """The address of a contiguous vector of n values."""
+    if t.device != device:
+        raise ValueError(f"{kind}: tensors on different devices")
+    if t.numel() != n or not t.is_contiguous() or (dtype is not None and t.dtype is not dtype):
+        raise ValueError(f"{kind}: expected {n} contiguous values" + (f" of {dtype}" if dtype else ""))
+    return t.data_ptr()
+
+
+def _raw_stream(device):
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
+def _shared(device, need):
+    """The shared workspace of a device, at least `need` bytes."""
+    ws = _workspaces.get(device.index)
+    if ws is None or ws.numel() < need:
+        ws = _shared_workspace(device, need)
+    return ws
 
 
 def gge_mx_quantize(X, Q, values=None):
     """Q (an MxTensor) = X quantised; X (rows, cols) or (batch, rows, cols), row-major or a
     transposed view.  values: optional output, the numbers that the codes stand for."""
-    lib = load()
-    _same_device(X.device, Q.codes, values)
-    x, v = view(X, "X"), _view_or_none(values, "values")
-    _check(lib.gge_mx_quantize(_ref(x), _ref(Q.c), _ref(v), _stream(X)), "gge_mx_quantize")
+    dev = X.device
+    if Q.device != dev:
+        raise ValueError("Q: tensors on different devices")
+    x = _tensor(X, "X")
+    v, keep = _output(values, "values", dev)
+    code = load().gge_mx_quantize(_address(x), _address(Q.c), v, _raw_stream(dev))
+    if code:
+        raise GgeError(code, "gge_mx_quantize")
 
 
 def gge_mx_dequantize(Q, Y):
     """Y (bf16, f16 or f32) = the numbers that Q's codes stand for."""
-    lib = load()
-    _same_device(Y.device, Q.codes)
-    y = view(Y, "Y")
-    _check(lib.gge_mx_dequantize(_ref(Q.c), _ref(y), _stream(Y)), "gge_mx_dequantize")
+    dev = Y.device
+    if Q.device != dev:
+        raise ValueError("Q: tensors on different devices")
+    y = _tensor(Y, "Y")
+    code = load().gge_mx_dequantize(_address(Q.c), _address(y), _raw_stream(dev))
+    if code:
+        raise GgeError(code, "gge_mx_dequantize")
+
+
+_workspace_bytes = {}   # per device: gge_workspace_size, gge_workspace_size_rmsnorm_bwd(0), and a column
+
+
+def _need(device):
+    n = _workspace_bytes.get(device.index)
+    if n is None:
+        lib = load()
+        with torch.cuda.device(device):
+            fixed = lib.gge_workspace_size_rmsnorm_bwd(0)
+            n = (lib.gge_workspace_size(None, 0), fixed, lib.gge_workspace_size_rmsnorm_bwd(1) - fixed)
+        _workspace_bytes[device.index] = n
+    return n
 
 
 def gge_gemm_mx(A, B, D=None, C=None, PostAct=None, act="none", alpha=1.0, beta=1.0,
                 alpha_dev=None, beta_dev=None, config=None, workspace=None):
     """D = alpha * A @ B^T + beta * C and / or PostAct = act(same) of MxTensors A (M, K) and
     B (N, K) (or batched), their tensor scales included."""
-    lib = load()
-    out = D if D is not None else PostAct
-    if out is None:
-        raise ValueError("gge_gemm_mx: D or PostAct is required")
-    _same_device(out.device, A.codes, B.codes, C, D, PostAct, alpha_dev, beta_dev)
-    c, d, p = _view_or_none(C, "mn"), _view_or_none(D, "mn"), _view_or_none(PostAct, "mn")
-    args = GgeGemmMxArgs(A.c, B.c, _ref(c), _ref(d), _ref(p), alpha, beta,
-                         alpha_dev.data_ptr() if alpha_dev is not None else None,
-                         beta_dev.data_ptr() if beta_dev is not None else None, ACT[act], 0,
-                         _ref(config))
-    ws = _ws(out.device, _gemm_workspace_bytes(lib, out.device), workspace)
-    _check(lib.gge_gemm_mx(_ref(args), ws.data_ptr(), ws.numel(), _stream(out)), "gge_gemm_mx")
-
-
-_workspace_bytes = {}
-
-
-def _gemm_workspace_bytes(lib, device):
-    """gge_workspace_size of a device (it depends on nothing else), asked once."""
-    n = _workspace_bytes.get(device)
-    if n is None:
-        with torch.cuda.device(device):
-            n = _workspace_bytes[device] = lib.gge_workspace_size(None, 0)
-    return n
+    dev = A.device
+    if B.device != dev:
+        raise ValueError("B: tensors on different devices")
+    d, keep_d = _output(D, "D", dev)
+    c, keep_c = _output(C, "C", dev)
+    p, keep_p = _output(PostAct, "PostAct", dev)
+    args = GgeGemmMxArgs(A.c, B.c, c, d, p, alpha, beta,
+                         _vector(alpha_dev, "alpha_dev", dev, 1, torch.float32) if alpha_dev is not None else None,
+                         _vector(beta_dev, "beta_dev", dev, 1, torch.float32) if beta_dev is not None else None,
+                         ACT[act], 0, _address(config) if config is not None else None)
+    need = _need(dev)[0]
+    ws = _shared(dev, need) if workspace is None else _ws(dev, need, workspace)
+    code = load().gge_gemm_mx(_address(args), ws.data_ptr(), ws.numel(), _raw_stream(dev))
+    if code:
+        raise GgeError(code, "gge_gemm_mx")
 
 
 def gge_rmsnorm(X, weight, Y=None, residual=None, residual_out=None, Q=None, values=None,
@@ -619,50 +707,54 @@ def gge_rmsnorm(X, weight, Y=None, residual=None, residual_out=None, Q=None, val
     """h = X + residual (rounded to X's type, written to residual_out), inv_rms = 1 / sqrt(mean
     h^2 + eps) a row, Y = h * inv_rms * weight; Q (an MxTensor) = the same quantised, values =
     the numbers that Q's codes stand for.  X (rows, cols); every output is optional."""
-    lib = load()
-    _same_device(X.device, weight, Y, residual, residual_out, Q.codes if Q is not None else None,
-                 values, inv_rms)
-    if X.dim() != 2 or weight.dim() != 1 or weight.shape[0] != X.shape[1] or \
-            (weight.numel() > 1 and weight.stride(0) != 1):
-        raise ValueError("gge_rmsnorm: X (rows, cols) and weight (cols,), contiguous")
-    if inv_rms is not None and (inv_rms.dtype != torch.float32 or inv_rms.numel() != X.shape[0] or
-                                not inv_rms.is_contiguous()):
-        raise ValueError("gge_rmsnorm: inv_rms is fp32, one value a row")
-    r, ro = _view_or_none(residual, "residual"), _view_or_none(residual_out, "residual_out")
-    y, v = _view_or_none(Y, "Y"), _view_or_none(values, "values")
-    if weight.dtype not in DTYPE:
+    dev = X.device
+    x = _tensor(X, "X")
+    if x.batch != 1:
+        raise ValueError("X: expected a 2-D tensor")
+    w = _vector(weight, "weight", dev, x.cols)
+    w_type = DTYPE.get(weight.dtype)
+    if w_type is None:
         raise TypeError(f"weight: unsupported dtype {weight.dtype}")
-    args = GgeRmsnormArgs(view(X, "X"), _ref(r), _ref(ro), _ref(y), _ref(Q.c if Q is not None else None),
-                          _ref(v), weight.data_ptr(), DTYPE[weight.dtype], eps,
-                          inv_rms.data_ptr() if inv_rms is not None else None)
-    _check(lib.gge_rmsnorm(_ref(args), _stream(X)), "gge_rmsnorm")
+    q = None
+    if Q is not None:
+        if Q.device != dev:
+            raise ValueError("Q: tensors on different devices")
+        q = _address(Q.c)
+    r, keep_r = _output(residual, "residual", dev)
+    h, keep_h = _output(residual_out, "residual_out", dev)
+    y, keep_y = _output(Y, "Y", dev)
+    v, keep_v = _output(values, "values", dev)
+    args = GgeRmsnormArgs(x, r, h, y, q, v, w, w_type, eps,
+                          _vector(inv_rms, "inv_rms", dev, x.rows, torch.float32) if inv_rms is not None else None)
+    code = load().gge_rmsnorm(_address(args), _raw_stream(dev))
+    if code:
+        raise GgeError(code, "gge_rmsnorm")
 
 
 def gge_rmsnorm_bwd(dY, H, weight, inv_rms, dX, dW=None, dH=None, workspace=None):
     """Backward of gge_rmsnorm: dX (the gradient of X and of the residual) from dY, the saved H
     (residual_out, or X) and inv_rms; dW (fp32, optional); dH the gradient reaching H directly."""
-    lib = load()
-    _same_device(dY.device, H, weight, inv_rms, dX, dW, dH)
-    cols = dY.shape[-1]
-    if dY.dim() != 2 or weight.shape != (cols,) or (weight.numel() > 1 and weight.stride(0) != 1):
-        raise ValueError("gge_rmsnorm_bwd: dY (rows, cols) and weight (cols,), contiguous")
-    if inv_rms.dtype != torch.float32 or inv_rms.numel() != dY.shape[0] or not inv_rms.is_contiguous():
-        raise ValueError("gge_rmsnorm_bwd: inv_rms is fp32, one value a row")
-    if dW is not None and (dW.dtype != torch.float32 or dW.shape != (cols,) or not dW.is_contiguous()):
-        raise ValueError("gge_rmsnorm_bwd: dW is fp32 (cols,), contiguous")
-    if weight.dtype not in DTYPE:
+    dev = dY.device
+    dy = _tensor(dY, "dY")
+    if dy.batch != 1:
+        raise ValueError("dY: expected a 2-D tensor")
+    if H.device != dev or dX.device != dev:
+        raise ValueError("H, dX: tensors on different devices")
+    w = _vector(weight, "weight", dev, dy.cols)
+    w_type = DTYPE.get(weight.dtype)
+    if w_type is None:
         raise TypeError(f"weight: unsupported dtype {weight.dtype}")
-    dh = _view_or_none(dH, "dH")
-    args = GgeRmsnormBwdArgs(view(dY, "dY"), view(H, "H"), _ref(dh), view(dX, "dX"),
-                             weight.data_ptr(), DTYPE[weight.dtype], 0, inv_rms.data_ptr(),
-                             dW.data_ptr() if dW is not None else None)
-    ws, n = None, 0
+    inv = _vector(inv_rms, "inv_rms", dev, dy.rows, torch.float32)
+    dh, keep_dh = _output(dH, "dH", dev)
+    dw = ws = None
+    n = 0
     if dW is not None:
-        buf = _ws(dY.device, _norm_workspace_bytes(lib, dY.device, cols), workspace)
+        dw = _vector(dW, "dW", dev, dy.cols, torch.float32)
+        _, fixed, a_col = _need(dev)
+        need = fixed + a_col * dy.cols
+        buf = _shared(dev, need) if workspace is None else _ws(dev, need, workspace)
         ws, n = buf.data_ptr(), buf.numel()
-    _check(lib.gge_rmsnorm_bwd(_ref(args), ws, n, _stream(dY)), "gge_rmsnorm_bwd")
-
-
-def _norm_workspace_bytes(lib, device, cols):
-    with torch.cuda.device(device):
-        return lib.gge_workspace_size_rmsnorm_bwd(cols)
+    args = GgeRmsnormBwdArgs(dy, _tensor(H, "H"), dh, _tensor(dX, "dX"), w, w_type, 0, inv, dw)
+    code = load().gge_rmsnorm_bwd(_address(args), ws, n, _raw_stream(dev))
+    if code:
+        raise GgeError(code, "gge_rmsnorm_bwd")

@@ -13,6 +13,9 @@ namespace {
 
 using lowp::QuantPtrs;
 
+// (a warp's and a block's columns past the last one still have to fit 32 bits)
+constexpr int64_t kMaxCols = kMaxExtent - 4096;
+
 int mx_block(int32_t f) { return f == GGE_NVFP4 ? 16 : 32; }
 int mx_bits(int32_t f) { return f == GGE_MXFP8 ? 8 : 4; }
 bool mx_known(int32_t f) { return f >= GGE_MXFP8 && f <= GGE_NVFP4; }
@@ -25,8 +28,7 @@ bool is_value_type(int32_t dt) { return dt == GGE_BF16 || dt == GGE_F16 || dt ==
 gge_status check_mx(const gge_mx_tensor& q) {
   if (!mx_known(q.format) || q.reserved != 0) return GGE_ERR_INVALID_ARG;
   if (q.rows < 0 || q.cols < 0 || q.batch < 1) return GGE_ERR_INVALID_ARG;
-  // (cols: whole scale words of columns still have to fit 32 bits)
-  if (q.rows > kMaxExtent || q.cols > kMaxExtent - 128 || q.batch > 65535) return GGE_ERR_UNSUPPORTED;
+  if (q.rows > kMaxExtent || q.cols > kMaxCols || q.batch > 65535) return GGE_ERR_UNSUPPORTED;
   if (q.tensor_scale != nullptr && q.format != GGE_NVFP4) return GGE_ERR_INVALID_ARG;
   if (q.tensor_scale != nullptr && (reinterpret_cast<uintptr_t>(q.tensor_scale) & 3u) != 0)
     return GGE_ERR_ALIGNMENT;
@@ -51,7 +53,7 @@ gge_status check_values(const gge_tensor& t, bool any_major) {
   if (t.reserved != 0) return GGE_ERR_INVALID_ARG;
   if (!is_value_type(t.dtype)) return GGE_ERR_UNSUPPORTED;
   if (t.rows < 0 || t.cols < 0 || t.batch < 1) return GGE_ERR_INVALID_ARG;
-  if (t.rows > kMaxExtent || t.cols > kMaxExtent - 128 || t.batch > 65535) return GGE_ERR_UNSUPPORTED;
+  if (t.rows > kMaxExtent || t.cols > kMaxCols || t.batch > 65535) return GGE_ERR_UNSUPPORTED;
   if (t.rows == 0 || t.cols == 0) return GGE_OK;
   if (t.ptr == nullptr) return GGE_ERR_INVALID_ARG;
   if ((reinterpret_cast<uintptr_t>(t.ptr) & (elem_bytes(t.dtype) - 1)) != 0) return GGE_ERR_ALIGNMENT;
@@ -96,7 +98,6 @@ gge_status quant_ptrs(const gge_mx_tensor& q, const gge_tensor* values, QuantPtr
     out->ldv = values->stride_row;
     out->values_batch_stride = values->batch > 1 ? values->stride_batch : 0;
     out->v_dtype = values->dtype;
-    out->v_vec = rows_aligned(*values) ? 1 : 0;
   }
   return GGE_OK;
 }
@@ -263,7 +264,11 @@ gge_status plan_mx(const gge_gemm_mx_args* a, void* ws, size_t ws_bytes, MxPlan*
   // split the last wave along K, as far as the workspace holds the partial sums
   if (K > 0 && !(p.flags & FLAG_NO_SPLIT) && ws != nullptr &&
       (reinterpret_cast<uintptr_t>(ws) & 255u) == 0) {
-    const TailSplit ts = plan_tail_split(pl.tiles, pl.units, p.k_tiles);
+    TailSplit ts = plan_tail_split(pl.tiles, pl.units, p.k_tiles);
+    // only where the tiles leave units idle from the start: behind full waves the
+    // partial sums' traffic costs more than the shorter last wave saves (8192^3 nvfp4
+    // 178 us split, 172 us whole; 4096^3 mxfp8 55 and 47 us)
+    if (ts.full > 0) ts.tail = 0;
     const int64_t blocks = static_cast<int64_t>(ts.tail) * ts.splits * pl.cg;
     const size_t need = kTailBase + static_cast<size_t>(blocks) * 128 * bn * sizeof(float);
     if (ts.tail > 0 && need <= ws_bytes &&
@@ -341,18 +346,13 @@ gge_status gge_mx_quantize(const gge_tensor* x, const gge_mx_tensor* q, const gg
   p.stride_row = x->stride_row;
   p.stride_col = x->stride_col;
   p.stride_batch = x->batch > 1 ? x->stride_batch : 0;
-  // (a transposed view: its contiguous dimension is the rows)
-  if (x->cols == 1 || x->stride_col == 1) {
-    p.vec = rows_aligned(*x) ? 1 : 0;
-  } else {
-    const int es = elem_bytes(x->dtype);
-    p.vec = aligned16(x->ptr) && x->stride_col * es % 16 == 0 &&
-                    (x->batch <= 1 || x->stride_batch * es % 16 == 0) ? 1 : 0;
-    if (x->cols > 65535 * int64_t(128)) return GGE_ERR_UNSUPPORTED;
-  }
-  const int sms = sm_count();
-  if (sms <= 0) return GGE_ERR_CUDA;
-  return launched(lowp::launch_quantize(p, sms, reinterpret_cast<cudaStream_t>(stream)));
+  p.aligned = x->cols == 1 || x->stride_col == 1
+                  ? rows_aligned(*x) && (values == nullptr || rows_aligned(*values))
+                  : aligned16(x->ptr) && x->stride_col * elem_bytes(x->dtype) % 16 == 0 &&
+                        (x->batch <= 1 || x->stride_batch * elem_bytes(x->dtype) % 16 == 0);
+  // (a transposed view takes the columns' tiles as a second grid dimension)
+  if (x->cols != 1 && x->stride_col != 1 && x->cols > 65535 * int64_t(128)) return GGE_ERR_UNSUPPORTED;
+  return launched(lowp::launch_quantize(p, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 gge_status gge_mx_dequantize(const gge_mx_tensor* q, const gge_tensor* y, gge_stream_t stream) {
@@ -380,10 +380,8 @@ gge_status gge_mx_dequantize(const gge_mx_tensor* q, const gge_tensor* y, gge_st
   p.ldy = y->stride_row;
   p.y_batch_stride = y->batch > 1 ? y->stride_batch : 0;
   p.dtype = y->dtype;
-  p.vec = rows_aligned(*y) ? 1 : 0;
-  const int sms = sm_count();
-  if (sms <= 0) return GGE_ERR_CUDA;
-  return launched(lowp::launch_dequantize(p, sms, reinterpret_cast<cudaStream_t>(stream)));
+  p.aligned = rows_aligned(*y) ? 1 : 0;
+  return launched(lowp::launch_dequantize(p, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 gge_status gge_gemm_mx(const gge_gemm_mx_args* args, void* ws, size_t ws_bytes, gge_stream_t stream) {
@@ -409,14 +407,14 @@ gge_status gge_rmsnorm(const gge_rmsnorm_args* a, gge_stream_t stream) {
   lowp::NormParams p;
   std::memset(&p, 0, sizeof(p));
   p.q.format = 3;  // no quantised output
-  bool vec = rows_aligned(x) && aligned16(a->weight);
+  bool aligned = rows_aligned(x) && (a->values == nullptr || rows_aligned(*a->values));
   const auto take = [&](const gge_tensor* t, bool output) {
     if (t == nullptr) return GGE_OK;
     const gge_status r = check_values(*t, false);
     if (r != GGE_OK) return r;
     if (t->dtype != x.dtype) return GGE_ERR_UNSUPPORTED;
     if (!same_shape(*t, x.rows, x.cols, 1) || (output && !rows_apart(*t))) return GGE_ERR_INVALID_ARG;
-    vec = vec && rows_aligned(*t);
+    aligned = aligned && rows_aligned(*t);
     return GGE_OK;
   };
   if ((s = take(a->residual, false)) != GGE_OK) return s;
@@ -446,7 +444,8 @@ gge_status gge_rmsnorm(const gge_rmsnorm_args* a, gge_stream_t stream) {
   p.w_dtype = a->weight_dtype;
   p.eps = a->eps;
   p.inv = a->inv_rms;
-  p.vec = vec ? 1 : 0;
+  p.w_vec = aligned16(a->weight) ? 1 : 0;
+  p.aligned = aligned ? 1 : 0;
   const int sms = sm_count();
   if (sms <= 0) return GGE_ERR_CUDA;
   return launched(lowp::launch_norm(p, sms, reinterpret_cast<cudaStream_t>(stream)));
@@ -467,14 +466,14 @@ gge_status gge_rmsnorm_bwd(const gge_rmsnorm_bwd_args* a, void* ws, size_t ws_by
   if (s != GGE_OK) return s;
   if (dy.batch != 1) return GGE_ERR_UNSUPPORTED;
   if (!is_value_type(a->weight_dtype)) return GGE_ERR_UNSUPPORTED;
-  bool vec = rows_aligned(dy) && aligned16(a->weight);
+  bool aligned = rows_aligned(dy);
   for (const gge_tensor* t : {&a->h, a->dh, &a->dx}) {
     if (t == nullptr) continue;
     s = check_values(*t, false);
     if (s != GGE_OK) return s;
     if (t->dtype != dy.dtype) return GGE_ERR_UNSUPPORTED;
     if (!same_shape(*t, dy.rows, dy.cols, 1)) return GGE_ERR_INVALID_ARG;
-    vec = vec && rows_aligned(*t);
+    aligned = aligned && rows_aligned(*t);
   }
   if (!rows_apart(a->dx)) return GGE_ERR_INVALID_ARG;
   if (dy.cols == 0 || (dy.rows == 0 && a->dweight == nullptr)) return GGE_OK;
@@ -499,7 +498,8 @@ gge_status gge_rmsnorm_bwd(const gge_rmsnorm_bwd_args* a, void* ws, size_t ws_by
   p.w_dtype = a->weight_dtype;
   p.inv = a->inv_rms;
   p.dw = a->dweight;
-  p.vec = vec ? 1 : 0;
+  p.w_vec = aligned16(a->weight) ? 1 : 0;
+  p.aligned = aligned ? 1 : 0;
   const int sms = sm_count();
   if (sms <= 0) return GGE_ERR_CUDA;
   if (a->dweight != nullptr) {

@@ -19,7 +19,7 @@ struct QuantPtrs {
   const float* tensor_scale;
   void* values;
   int64_t ldv, values_batch_stride;
-  int32_t v_dtype, v_vec;
+  int32_t v_dtype;
 };
 
 struct NormParams {
@@ -34,7 +34,8 @@ struct NormParams {
   float eps;
   float* inv;  // NULL: not wanted
   QuantPtrs q;
-  int32_t vec;  // every row of every tensor starts on a 16-byte boundary
+  int32_t w_vec;    // the weight starts on a 16-byte boundary
+  int32_t aligned;  // and so does every row of every tensor
 };
 
 struct NormBwdParams {
@@ -49,7 +50,7 @@ struct NormBwdParams {
   const float* inv;
   float* dw;        // NULL: not wanted
   float* partials;  // [grid][cols] sums of the blocks' rows
-  int32_t vec;
+  int32_t w_vec, aligned;
 };
 
 struct QuantParams {
@@ -58,7 +59,7 @@ struct QuantParams {
   int32_t dtype;
   const void* x;
   int64_t stride_row, stride_col, stride_batch;  // elements; one of the first two is 1
-  int32_t vec;  // 16-byte pieces of the contiguous dimension
+  int32_t aligned;  // every row of the source's storage and of the values starts on a 16-byte boundary
   QuantPtrs q;
 };
 
@@ -70,15 +71,16 @@ struct DequantParams {
   const float* tensor_scale;
   void* y;
   int64_t ldy, y_batch_stride;
-  int32_t dtype, vec;
+  int32_t dtype;
+  int32_t aligned;
 };
 
 cudaError_t launch_norm(const NormParams& p, int sms, cudaStream_t st);
 // Blocks a backward launch uses at most (each leaves `cols` partial sums).
 int norm_bwd_blocks(int64_t rows, int sms);
 cudaError_t launch_norm_bwd(const NormBwdParams& p, int sms, cudaStream_t st);
-cudaError_t launch_quantize(const QuantParams& p, int sms, cudaStream_t st);
-cudaError_t launch_dequantize(const DequantParams& p, int sms, cudaStream_t st);
+cudaError_t launch_quantize(const QuantParams& p, cudaStream_t st);
+cudaError_t launch_dequantize(const DequantParams& p, cudaStream_t st);
 
 // Launch with programmatic stream serialisation: the kernel sets up, then waits
 // (griddepcontrol.wait) for the stream's previous kernel before it touches

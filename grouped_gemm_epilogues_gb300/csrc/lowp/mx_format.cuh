@@ -10,14 +10,15 @@
 // 1.c * 2^top that is e = k - top, plus one where the fraction f is above c:
 // integer arithmetic on the float's bits, and x * 2^-e is exact.  nvfp4 takes
 // s = e4m3(max(amax / (6 t), 2^-9)) and codes e2m1(x * (1 / (s t))).  A block
-// that holds an infinity or a NaN gets a NaN scale and zero codes: all its
-// values read back as NaN.
+// that holds an infinity or a NaN gets a NaN scale: all its values read back as
+// NaN.
 #pragma once
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
 #include <cstdint>
+#include <type_traits>
 
 namespace gge {
 namespace mx {
@@ -81,7 +82,8 @@ __device__ __forceinline__ float2 e2m1x2_to_float2(uint32_t two) {
 }
 
 // A block's scale: the stored byte, and the factor its values are multiplied
-// by before rounding to codes (0 where the block is not finite).
+// by before rounding to codes (0 where the block is not finite: its codes are of
+// no account then, NaN times anything is NaN).
 template <int FMT>
 __device__ __forceinline__ uint32_t block_scale(uint32_t amax_bits, float tensor_scale,
                                                 float& factor) {
@@ -114,11 +116,12 @@ __device__ __forceinline__ float scale_value(uint32_t s) {
 // are above every finite value's).
 __device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
 
-// x * factor, with 0 for a block that is not finite (inf * 0 would be NaN)
-__device__ __forceinline__ float scaled(float x, float factor) {
-  return factor == 0.f ? 0.f : x * factor;
+// The larger of |a| and |b|, NaN if either is, with a sign of no meaning.
+__device__ __forceinline__ float max_abs(float a, float b) {
+  float r;
+  asm("max.NaN.xorsign.abs.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
 }
-
 __device__ __forceinline__ uint32_t pack_e4m3x4(float a, float b, float c, float d) {
   uint16_t lo, hi;
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
@@ -193,20 +196,28 @@ __device__ __forceinline__ void store8(T* p, const Raw8<T>& r) {
   for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) reinterpret_cast<uint4*>(p)[i] = r.w[i];
 }
 
+// The packed pair of a 16-bit type, and its two values.
+template <typename T> struct Pair;
+template <> struct Pair<__nv_bfloat16> { using type = __nv_bfloat162; };
+template <> struct Pair<__half> { using type = __half2; };
+
 template <typename T>
-__device__ __forceinline__ void widen(const Raw8<T>& r, float (&v)[8]) {
-  const T* t = reinterpret_cast<const T*>(&r);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = to_float<T>(t[i]);
+__device__ __forceinline__ float2 widen_pair(uint32_t w) {
+  if constexpr (sizeof(T) == 2 && std::is_same<T, __nv_bfloat16>::value)
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+  else
+    return __half22float2(*reinterpret_cast<const __half2*>(&w));
 }
 
 template <typename T>
-__device__ __forceinline__ Raw8<T> narrow(const float (&v)[8]) {
-  Raw8<T> r;
-  T* t = reinterpret_cast<T*>(&r);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) t[i] = from_float<T>(v[i]);
-  return r;
+__device__ __forceinline__ uint32_t narrow_pair(float2 v) {
+  if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(v.x, v.y);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  } else {
+    const __half2 h = __floats2half2_rn(v.x, v.y);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
 }
 
 // One value of a runtime type (0 bf16, 1 f16, 4 f32: gge_dtype).
@@ -220,18 +231,6 @@ __device__ __forceinline__ void store_any(void* p, int64_t i, int32_t dtype, flo
   else if (dtype == 1) static_cast<__half*>(p)[i] = __float2half_rn(v);
   else static_cast<float*>(p)[i] = v;
 }
-// Eight consecutive ones, 16-byte aligned.
-__device__ __forceinline__ void load8_any(const void* p, int64_t i, int32_t dtype, float (&v)[8]) {
-  if (dtype == 0) widen(load8(static_cast<const __nv_bfloat16*>(p) + i), v);
-  else if (dtype == 1) widen(load8(static_cast<const __half*>(p) + i), v);
-  else widen(load8(static_cast<const float*>(p) + i), v);
-}
-__device__ __forceinline__ void store8_any(void* p, int64_t i, int32_t dtype, const float (&v)[8]) {
-  if (dtype == 0) store8(static_cast<__nv_bfloat16*>(p) + i, narrow<__nv_bfloat16>(v));
-  else if (dtype == 1) store8(static_cast<__half*>(p) + i, narrow<__half>(v));
-  else store8(static_cast<float*>(p) + i, narrow<float>(v));
-}
-
 // ------------------------------------------------ quantising a warp's chunks
 
 // Where one matrix's codes, scales and (optional) values go.
@@ -244,63 +243,117 @@ struct QuantOut {
   void* values;      // NULL: not wanted
   int64_t ldv;
   int32_t v_dtype;
-  int32_t v_vec;     // the values can be stored in 16-byte pieces
 };
 
-// Quantise eight consecutive values a lane; neighbouring lanes hold
-// neighbouring chunks, four (mx) or two (nvfp4) lanes to a block, and a group of
-// four blocks never straddles a warp.  `col` is the lane's first column; columns
-// >= cols hold zeros.  Every lane of the warp calls this (shuffles); `live`
-// lanes store.
-template <int FMT>
-__device__ __forceinline__ void quantise_chunk(const QuantOut& q, const float (&v)[8], int64_t row,
-                                               int32_t col, int32_t cols, float tensor_scale,
-                                               bool live) {
-  constexpr int kLanes = Fmt<FMT>::kBlock / 8;  // lanes that share a scale
-  uint32_t amax = 0u;
+// Eight consecutive values as four pairs: the packed fp32 operations take two.
+template <typename T>
+__device__ __forceinline__ void widen(const Raw8<T>& r, float2 (&v)[4]) {
+  if constexpr (sizeof(T) == 4) {
+    const float2* f = reinterpret_cast<const float2*>(&r);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) amax = max(amax, abs_bits(v[i]));
+    for (int i = 0; i < 4; ++i) v[i] = f[i];
+  } else {
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(&r);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = widen_pair<T>(w[i]);
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ Raw8<T> narrow(const float2 (&v)[4]) {
+  Raw8<T> r;
+  if constexpr (sizeof(T) == 4) {
+    float2* f = reinterpret_cast<float2*>(&r);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = v[i];
+  } else {
+    uint32_t* w = reinterpret_cast<uint32_t*>(&r);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = narrow_pair<T>(v[i]);
+  }
+  return r;
+}
+
+// round(a + b), value by value.
+template <typename T>
+__device__ __forceinline__ Raw8<T> add8(const Raw8<T>& a, const Raw8<T>& b) {
+  Raw8<T> r;
+  if constexpr (sizeof(T) == 4) {
+    const float* x = reinterpret_cast<const float*>(&a);
+    const float* y = reinterpret_cast<const float*>(&b);
+    float* z = reinterpret_cast<float*>(&r);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) z[i] = x[i] + y[i];
+  } else {
+    using T2 = typename Pair<T>::type;
+    const T2* x = reinterpret_cast<const T2*>(&a);
+    const T2* y = reinterpret_cast<const T2*>(&b);
+    T2* z = reinterpret_cast<T2*>(&r);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) z[i] = __hadd2_rn(x[i], y[i]);
+  }
+  return r;
+}
+
+// Eight quantised values of a lane: their codes, their block's scale as a number,
+// and, in the first lane of each group of four blocks, the group's scale bytes.
+struct Quantised {
+  uint2 codes;
+  float unit;
+  uint32_t word;
+};
+
+// Quantise eight consecutive values a lane; neighbouring lanes hold neighbouring
+// chunks, four (mx) or two (nvfp4) lanes to a block, and a group of four blocks
+// never straddles a warp.  Values past a row's end are zeros; `past`: the lane's
+// block lies past the row's last one (its scale byte is padding, 0).  Every lane
+// of the warp calls this.
+template <int FMT>
+__device__ __forceinline__ Quantised quantise8(const float2 (&v)[4], float tensor_scale, bool past) {
+  constexpr int kLanes = Fmt<FMT>::kBlock / 8;  // lanes that share a scale
+  Quantised r;
+  uint32_t amax = abs_bits(max_abs(max_abs(max_abs(v[0].x, v[0].y), max_abs(v[1].x, v[1].y)),
+                                   max_abs(max_abs(v[2].x, v[2].y), max_abs(v[3].x, v[3].y))));
 #pragma unroll
   for (int o = 1; o < kLanes; o <<= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, o));
   float factor;
   uint32_t s = block_scale<FMT>(amax, tensor_scale, factor);
-  const int32_t group_end = (cols + Fmt<FMT>::kBlock - 1) / Fmt<FMT>::kBlock * Fmt<FMT>::kBlock;
-  const float unit = scale_value<FMT>(s);
-  if (col >= group_end) s = 0u;  // blocks past the last one: the padding of the row's last word
+  r.unit = scale_value<FMT>(s);
+  if (past) s = 0u;
   float c[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) c[i] = scaled(v[i], factor);
-  const uint2 w = pack8<FMT>(c);
-  const int lane = threadIdx.x & 31;
-  // the group's first lane collects the four scale bytes
-  uint32_t word = s;
-#pragma unroll
-  for (int j = 1; j < 4; ++j)
-    word |= __shfl_down_sync(0xffffffffu, s, j * kLanes) << (8 * j);
-  if (!live) return;
-  if (lane % (4 * kLanes) == 0)
-    *reinterpret_cast<uint32_t*>(q.scales + scale_word(row, col / Fmt<FMT>::kGroup, q.kgroups)) = word;
-  if (col < ((cols + 31) & ~31)) {  // codes of a row are padded with zeros to whole 32s
-    uint8_t* p = q.codes + row * q.ld + static_cast<int64_t>(col) * Fmt<FMT>::kBits / 8;
-    if constexpr (FMT == FMT_MXFP8) *reinterpret_cast<uint2*>(p) = w;
-    else *reinterpret_cast<uint32_t*>(p) = w.x;
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = __fmul2_rn(v[i], make_float2(factor, factor));
+    c[2 * i] = f.x;
+    c[2 * i + 1] = f.y;
   }
-  if (q.values != nullptr && col < cols) {
-    float back[8];
-    unpack8<FMT>(w, back);
+  r.codes = pack8<FMT>(c);
+  const uint32_t two = s | (__shfl_down_sync(0xffffffffu, s, kLanes) << 8);
+  r.word = two | (__shfl_down_sync(0xffffffffu, two, 2 * kLanes) << 16);
+  return r;
+}
+
+// Whether this lane is the one that holds its group's scale bytes.
+template <int FMT>
+__device__ __forceinline__ bool holds_word() {
+  return (threadIdx.x & 31) % (Fmt<FMT>::kGroup / 8) == 0;
+}
+
+template <int FMT>
+__device__ __forceinline__ void store_codes(uint8_t* p, uint2 codes) {
+  if constexpr (FMT == FMT_MXFP8) *reinterpret_cast<uint2*>(p) = codes;
+  else *reinterpret_cast<uint32_t*>(p) = codes.x;
+}
+
+// The numbers that eight codes stand for.
+template <int FMT>
+__device__ __forceinline__ void code_values(uint2 w, float unit, float tensor_scale, float2 (&v)[4]) {
+  float c[8];
+  unpack8<FMT>(w, c);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      back[i] = back[i] * unit;
-      if constexpr (FMT == FMT_NVFP4) back[i] *= tensor_scale;
-    }
-    const int64_t at = row * q.ldv + col;
-    if (q.v_vec && col + 8 <= cols) {
-      store8_any(q.values, at, q.v_dtype, back);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (col + i < cols) store_any(q.values, at + i, q.v_dtype, back[i]);
-    }
+  for (int i = 0; i < 4; ++i) {
+    v[i] = __fmul2_rn(make_float2(c[2 * i], c[2 * i + 1]), make_float2(unit, unit));
+    if constexpr (FMT == FMT_NVFP4) v[i] = __fmul2_rn(v[i], make_float2(tensor_scale, tensor_scale));
   }
 }
 

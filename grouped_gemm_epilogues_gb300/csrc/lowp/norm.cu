@@ -10,11 +10,14 @@
 // directly, along the residual stream):
 //   g = dy w    dx = inv (g - h inv^2 mean(g h)) + dh    dw = sum over rows of dy (h inv)
 //
-// Both are bound by memory: a row is read once into registers, reduced, and
-// written from there.
-#include "../gge_ptx.cuh"
+// Both are bound by memory.  Blocks walk the rows with a grid stride; cp.async
+// keeps the next rows on their way to shared memory while a row is reduced in
+// registers and written, so every value is read once.
+#include <atomic>
+
+#include "../gge_launch.h"
 #include "lowp_launch.h"
-#include "mx_format.cuh"
+#include "rows.cuh"
 
 namespace gge {
 namespace lowp {
@@ -22,7 +25,8 @@ namespace {
 
 using namespace mx;
 
-constexpr int kBlockThreads = 256;
+constexpr int kMaxThreads = 1024;
+constexpr int kMaxCols = kMaxThreads * 2 * 8;  // longer rows take the *_long kernels
 
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
@@ -30,129 +34,219 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-// Sum over the `tpr` threads (a multiple of 32) that share a row.  `slots` is
-// shared memory for one float a warp; `flip` alternates between its two halves,
-// so one barrier a row is enough.  Every thread of the block calls it.
-__device__ __forceinline__ float row_sum(float v, int tpr, float* slots, int flip) {
+// Sum over the `tpr` threads (a multiple of 32) that share a row, the block's
+// `sub`-th.  `slots` is shared memory for one float a warp, twice; `flip`
+// alternates between the two, so one barrier a row is enough.
+__device__ __forceinline__ float row_sum(float v, int tpr, float* slots, int flip, int sub) {
   v = warp_sum(v);
   if (tpr == 32) return v;
   const int warp = threadIdx.x >> 5;
   const int per = tpr >> 5;
   float* s = slots + flip * 32;
   if ((threadIdx.x & 31) == 0) s[warp] = v;
-  __syncthreads();
-  const int first = warp / per * per;
-  float t = 0.f;
-  for (int i = 0; i < per; ++i) t += s[first + i];
-  return t;
+  // (a barrier of its own for each row group: the groups do not run in step, and
+  // barrier 0 is the whole block's)
+  asm volatile("bar.sync %0, %1;" ::"r"(sub + 1), "r"(tpr) : "memory");
+  const float* mine = s + warp / per * per;
+  const int lane = threadIdx.x & 31;
+  return warp_sum(lane < per ? mine[lane] : 0.f);
 }
 
-// ------------------------------------------------------------ forward
-
-// A row is spread over `tpr` threads; thread i holds the 8-value chunks i, i + tpr, ...
-template <typename T, int C, int FMT>
-__global__ void __launch_bounds__(C == 4 ? 512 : 1024) norm_kernel(const __grid_constant__ NormParams p, int tpr) {
-  __shared__ float slots[64];
-  ptx::griddep_launch_dependents();
-  const int per_block = blockDim.x / tpr;
-  const int sub = threadIdx.x / tpr, t = threadIdx.x % tpr;
-  const int32_t cols = p.cols;
-  QuantOut q{p.q.codes, p.q.ld, p.q.scales, p.q.kgroups, p.q.tensor_scale, p.q.values, p.q.ldv,
-             p.q.v_dtype, p.q.v_vec};
-  ptx::griddep_wait();
-  const float tscale = (FMT == FMT_NVFP4 && q.tensor_scale) ? *q.tensor_scale : 1.f;
-  const T* x = static_cast<const T*>(p.x);
-  const T* res = static_cast<const T*>(p.residual);
-  int flip = 0;
-  for (int64_t row0 = static_cast<int64_t>(blockIdx.x) * per_block; row0 < p.rows;
-       row0 += static_cast<int64_t>(gridDim.x) * per_block) {
-    const int64_t row = row0 + sub;
-    const bool live = row < p.rows;
-    float v[C][8];
-    float ss = 0.f;
-    Raw8<T> xr[C], rr[C];
+// Eight weights from column col on (zeros past the last one).
+__device__ __forceinline__ void load_weight(const void* w, int32_t dtype, int32_t vec, int32_t col,
+                                            int32_t cols, float2 (&v)[4]) {
+  if (vec && col + 8 <= cols) {
+    if (dtype == 0) widen(load8(static_cast<const __nv_bfloat16*>(w) + col), v);
+    else if (dtype == 1) widen(load8(static_cast<const __half*>(w) + col), v);
+    else widen(load8(static_cast<const float*>(w) + col), v);
+  } else {
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const int32_t col = (t + c * tpr) * 8;
-      if (live && col + 8 <= cols) {
-        xr[c] = load8(x + row * p.ldx + col);
-        if (res != nullptr) rr[c] = load8(res + row * p.ldr + col);
-      }
-    }
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const int32_t col = (t + c * tpr) * 8;
-      if (live && col + 8 <= cols) {
-        widen(xr[c], v[c]);
-        if (res != nullptr) {
-          float r[8];
-          widen(rr[c], r);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) v[c][i] += r[i];
-          const Raw8<T> h = narrow<T>(v[c]);
-          widen(h, v[c]);
-          if (p.h != nullptr) store8(static_cast<T*>(p.h) + row * p.ldh + col, h);
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          v[c][i] = 0.f;
-          if (live && col + i < cols) {  // the row's last, partly filled chunk
-            float a = to_float<T>(x[row * p.ldx + col + i]);
-            if (res != nullptr) {
-              const T h = from_float<T>(a + to_float<T>(res[row * p.ldr + col + i]));
-              a = to_float<T>(h);
-              if (p.h != nullptr) static_cast<T*>(p.h)[row * p.ldh + col + i] = h;
-            }
-            v[c][i] = a;
-          }
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) ss = fmaf(v[c][i], v[c][i], ss);
-    }
-    ss = row_sum(ss, tpr, slots, flip);
-    flip ^= 1;
-    const float inv = 1.f / sqrtf(ss / static_cast<float>(cols) + p.eps);
-    if (live && t == 0 && p.inv != nullptr) p.inv[row] = inv;
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const int32_t col = (t + c * tpr) * 8;
-      float w[8];
-      if (col + 8 <= cols) {
-        load8_any(p.weight, col, p.w_dtype, w);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = col + i < cols ? load_any(p.weight, col + i, p.w_dtype) : 0.f;
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[c][i] = (v[c][i] * inv) * w[i];
-      if (p.y != nullptr && live) {
-        T* y = static_cast<T*>(p.y) + row * p.ldy + col;
-        if (col + 8 <= cols) {
-          store8(y, narrow<T>(v[c]));
-        } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if (col + i < cols) y[i] = from_float<T>(v[c][i]);
-        }
-      }
-      if constexpr (FMT != FMT_NONE)
-        quantise_chunk<FMT>(q, v[c], row, col, cols, tscale,
-                            live && col < q.kgroups * Fmt<FMT>::kGroup);
+    for (int i = 0; i < 4; ++i) {
+      v[i].x = col + 2 * i < cols ? load_any(w, col + 2 * i, dtype) : 0.f;
+      v[i].y = col + 2 * i + 1 < cols ? load_any(w, col + 2 * i + 1, dtype) : 0.f;
     }
   }
 }
 
-// Any alignment and any length: one value a lane, so that loads of rows that
-// start anywhere still fill whole sectors; the second pass reads the row again
-// (from L1).  A block is a warp's 32 (or half a warp's 16) lanes.
-template <typename T, int FMT>
-__global__ void norm_any_kernel(const __grid_constant__ NormParams p, int tpr) {
+// A lane's 8 values, those past the row's end set to zero.
+template <typename T>
+__device__ __forceinline__ void clear_past(Raw8<T>& r, int32_t col, int32_t cols) {
+  if (col + 8 <= cols) return;
+  T* t = reinterpret_cast<T*>(&r);
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (col + i >= cols) t[i] = from_float<T>(0.f);
+}
+
+// One tensor's rows on their way through shared memory, for one warp.  AL: every
+// row starts on a 16-byte boundary, so a lane copies and reads its own pieces
+// only; otherwise the warp does it together (rows.cuh).
+template <typename T, bool AL>
+struct RowReader {
+  const T* next;  // the next row to copy: AL this lane's chunk 0 of it, else its start
+
+  __device__ __forceinline__ void init(const void* base, int64_t ld, int64_t row, int32_t col) {
+    next = static_cast<const T*>(base) + row * ld + (AL ? col : 0);
+  }
+  // copy chunk c (`cols_over` columns after chunk 0) of that row to this warp's `dst`
+  __device__ __forceinline__ void copy(uint32_t dst, int32_t col, int32_t cols_over, int32_t cols,
+                                       bool first) const {
+    constexpr int P = WarpRow<T>::kPieces;
+    const int lane = threadIdx.x & 31;
+    if constexpr (AL) {
+      const int32_t left = (cols - col) * static_cast<int32_t>(sizeof(T));
+#pragma unroll
+      for (int j = 0; j < P; ++j) {
+        // (bytes past the row's end are zero-filled; none are read)
+        const int32_t n = min(16, max(0, left - 16 * j));
+        ptx::cp_async_16(dst + 16u * (lane * P + j), n > 0 ? next + cols_over + j * (16 / sizeof(T)) : next,
+                         static_cast<uint32_t>(n));
+      }
+    } else {
+      if (col - lane * 8 < cols) copy_row(dst, next, col - lane * 8, cols, first);
+    }
+  }
+};
+
+// A lane's 8 values of a copied chunk of the row that starts at `row`.
+template <typename T, bool AL>
+__device__ __forceinline__ Raw8<T> take_chunk(uint32_t src, const T* row, int32_t col, int32_t cols) {
+  constexpr int P = WarpRow<T>::kPieces;
+  if constexpr (AL) {
+    Raw8<T> r;
+#pragma unroll
+    for (int j = 0; j < P; ++j) r.w[j] = ptx::ld_shared_v4(src + 16u * ((threadIdx.x & 31) * P + j));
+    return r;
+  } else {
+    Raw8<T> r = take_row<T>(src, static_cast<uint32_t>(reinterpret_cast<uintptr_t>(row)) & 15u);
+    clear_past(r, col, cols);
+    return r;
+  }
+}
+
+template <typename T, bool AL>
+__device__ __forceinline__ void put_chunk(T* row, int32_t col, int32_t cols, const Raw8<T>& v) {
+  if constexpr (AL) store_row8_aligned(row, col, cols, v);
+  else store_row8(row, col, cols, v);
+}
+
+// ------------------------------------------------------------ forward
+
+// Rows in shared memory: the one at work and, where it fits, the next.
+template <typename T, int C>
+constexpr int norm_depth() {
+  return sizeof(T) == 4 && C == 2 ? 1 : 2;
+}
+
+// A row is spread over `tpr` threads; thread i holds the 8-value chunks i, i + tpr, ...
+// The block's row groups run on their own: what they share is shared memory's size.
+template <typename T, int C, int FMT, bool AL>
+__global__ void __launch_bounds__(kMaxThreads)
+    norm_kernel(const __grid_constant__ NormParams p, int tpr) {
   __shared__ float slots[64];
+  extern __shared__ uint8_t ring_raw[];
   ptx::griddep_launch_dependents();
+  constexpr int D = norm_depth<T, C>();
   const int per_block = blockDim.x / tpr;
   const int sub = threadIdx.x / tpr, t = threadIdx.x % tpr;
+  const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+  const int32_t cols = p.cols;
+  const int32_t warp_col = (t - lane) * 8;  // of chunk 0
+  // this warp's buffers: [row in flight][chunk][x, residual]
+  constexpr uint32_t kBuf = WarpRow<T>::kBytes;
+  const uint32_t ring = ptx::smem_addr(ring_raw) + (threadIdx.x >> 5) * (C * 2 * kBuf);
+  const uint32_t ring_row = warps * (C * 2 * kBuf);
+  const int64_t step = static_cast<int64_t>(gridDim.x) * per_block;
+  int64_t row = static_cast<int64_t>(blockIdx.x) * per_block + sub;
+  const bool has_res = p.residual != nullptr;
+  RowReader<T, AL> x, res;
+  x.init(p.x, p.ldx, row, t * 8);
+  res.init(p.residual, p.ldr, row, t * 8);
+  ptx::griddep_wait();
+  const float tscale = (FMT == FMT_NVFP4 && p.q.tensor_scale) ? *p.q.tensor_scale : 1.f;
+  int64_t ahead = row;
+  const auto start = [&](int slot) {
+    if (ahead < p.rows) {
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        const uint32_t dst = ring + slot * ring_row + c * 2 * kBuf;
+        x.copy(dst, (t + c * tpr) * 8, c * tpr * 8, cols, ahead == 0);
+        if (has_res) res.copy(dst + kBuf, (t + c * tpr) * 8, c * tpr * 8, cols, ahead == 0);
+      }
+      x.next += step * p.ldx;
+      res.next += step * p.ldr;
+    }
+    ahead += step;
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int s = 0; s + 1 < D; ++s) start(s);
+  const float inv_cols = 1.f / static_cast<float>(cols);
+  int slot = 0, flip = 0;
+  for (; row < p.rows; row += step) {
+    if constexpr (!AL) __syncwarp();  // (the slot was read in the iteration before)
+    start((slot + D - 1) % D);
+    cp_async_wait<D - 1>();
+    if constexpr (!AL) __syncwarp();
+    Raw8<T> h[C];
+    float2 ss = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const int32_t col = (t + c * tpr) * 8;
+      const uint32_t src = ring + slot * ring_row + c * 2 * kBuf;
+      h[c] = take_chunk<T, AL>(src, static_cast<const T*>(p.x) + row * p.ldx, col, cols);
+      if (has_res) {
+        h[c] = add8(h[c], take_chunk<T, AL>(src + kBuf, static_cast<const T*>(p.residual) + row * p.ldr, col, cols));
+        if (p.h != nullptr && warp_col + c * tpr * 8 < cols)
+          put_chunk<T, AL>(static_cast<T*>(p.h) + row * p.ldh, col, cols, h[c]);
+      }
+      float2 v[4];
+      widen(h[c], v);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) ss = __ffma2_rn(v[i], v[i], ss);
+    }
+    slot = (slot + 1) % D;
+    const float sum = row_sum(ss.x + ss.y, tpr, slots, flip, sub);
+    flip ^= 1;
+    const float inv = rsqrtf(fmaf(sum, inv_cols, p.eps));
+    if (t == 0 && p.inv != nullptr) p.inv[row] = inv;
+    uint8_t *codes = nullptr, *scales = nullptr;
+    if constexpr (FMT != FMT_NONE) {
+      codes = p.q.codes + row * p.q.ld;
+      scales = p.q.scales + scale_word(row, 0, p.q.kgroups);
+    }
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const int32_t col = (t + c * tpr) * 8;
+      if (c > 0 && warp_col + c * tpr * 8 >= cols) continue;
+      float2 v[4], w[4];
+      widen(h[c], v);
+      load_weight(p.weight, p.w_dtype, p.w_vec, col, cols, w);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = __fmul2_rn(__fmul2_rn(v[i], make_float2(inv, inv)), w[i]);
+      if (p.y != nullptr) put_chunk<T, AL>(static_cast<T*>(p.y) + row * p.ldy, col, cols, narrow<T>(v));
+      if constexpr (FMT != FMT_NONE) {
+        constexpr int B = Fmt<FMT>::kBlock;
+        const Quantised z = quantise8<FMT>(v, tscale, col >= (cols + B - 1) / B * B);
+        if (holds_word<FMT>() && col < p.q.kgroups * Fmt<FMT>::kGroup)
+          *reinterpret_cast<uint32_t*>(scales + static_cast<int64_t>(col / Fmt<FMT>::kGroup) * 512) = z.word;
+        if (col < ((cols + 31) & ~31)) store_codes<FMT>(codes + static_cast<int64_t>(col) * Fmt<FMT>::kBits / 8, z.codes);
+        if (p.q.values != nullptr) {
+          code_values<FMT>(z.codes, z.unit, tscale, v);
+          store_row8_any<AL>(p.q.values, row * p.q.ldv, p.q.v_dtype, col, cols, v);
+        }
+      }
+    }
+  }
+}
+
+// Rows too long for a block's registers: one value a lane, and a second pass that
+// reads the row again.  A scale's block is a warp's 32 (or half a warp's 16) lanes.
+template <typename T, int FMT>
+__global__ void norm_long_kernel(const __grid_constant__ NormParams p) {
+  __shared__ float slots[64];
+  ptx::griddep_launch_dependents();
+  const int per_block = 1, sub = 0, t = threadIdx.x, tpr = blockDim.x;
   const int lane = threadIdx.x & 31;
   const int32_t cols = p.cols;
   ptx::griddep_wait();
@@ -181,7 +275,7 @@ __global__ void norm_any_kernel(const __grid_constant__ NormParams p, int tpr) {
         ss = fmaf(a, a, ss);
       }
     }
-    ss = row_sum(ss, tpr, slots, flip);
+    ss = row_sum(ss, tpr, slots, flip, 0);
     flip ^= 1;
     const float inv = 1.f / sqrtf(ss / static_cast<float>(cols) + p.eps);
     if (live && t == 0 && p.inv != nullptr) p.inv[row] = inv;
@@ -202,7 +296,7 @@ __global__ void norm_any_kernel(const __grid_constant__ NormParams p, int tpr) {
         uint32_t s = block_scale<FMT>(amax, tscale, factor);
         const float unit = scale_value<FMT>(s);
         const int32_t block = col / Fmt<FMT>::kBlock;
-        const float c = scaled(a, factor);
+        const float c = a * factor;
         float back;
         if constexpr (FMT == FMT_MXFP8) {
           const uint32_t code = pack_e4m3x4(c, 0.f, 0.f, 0.f) & 0xffu;
@@ -229,41 +323,64 @@ __global__ void norm_any_kernel(const __grid_constant__ NormParams p, int tpr) {
   }
 }
 
-// Threads a row and chunks a thread for a row of `chunks` 8-value chunks.
+// Threads a row of `chunks` 8-value chunks, and chunks a thread (1 or 2).  A row
+// group has a warp, or at least 128 threads: a block of 1024 then has at most 8
+// groups with barriers (of the 15 beside barrier 0).
 struct RowShape {
   int tpr, c;
 };
-RowShape row_shape(int64_t chunks, int64_t rows, int sms) {
-  // few rows: more threads a row (latency); many: four chunks a thread, so that
-  // each thread has several loads in flight and rows a block reduce cheaply
-  const int most = rows <= 2 * sms ? 1 : 4;
+RowShape row_shape(int64_t chunks, bool one) {
   RowShape s{32, 1};
-  while (s.tpr < (most == 4 ? 512 : 1024) && static_cast<int64_t>(s.tpr) * most < chunks) s.tpr *= 2;
-  while (static_cast<int64_t>(s.tpr) * s.c < chunks) s.c *= 2;  // at most 1024 x 2 or 512 x 4
+  while (s.tpr < kMaxThreads && static_cast<int64_t>(s.tpr) * (one ? 1 : 2) < chunks) s.tpr = s.tpr == 32 ? 128 : s.tpr * 2;
+  if (s.tpr < chunks) s.c = 2;
   return s;
+}
+
+// Opt in to `smem` bytes of shared memory (a per-device attribute of the kernel).
+template <typename... A>
+cudaError_t allow_smem(void (*kern)(A...), std::atomic<size_t>* set, size_t smem) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64 || set[dev].load() < smem) {
+    RelaxedCaptureMode relaxed;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) set[dev].store(smem);
+  }
+  return cudaSuccess;
+}
+
+template <typename T, int C, int FMT, bool AL>
+cudaError_t launch_norm_c(const NormParams& p, int tpr, int sms, cudaStream_t st) {
+  static std::atomic<size_t> set[64];
+  const int block = tpr > 256 ? tpr : 256;
+  const int per = block / tpr;
+  const size_t smem = static_cast<size_t>(norm_depth<T, C>()) * (block / 32) * C * 2 * WarpRow<T>::kBytes;
+  const cudaError_t e = allow_smem(norm_kernel<T, C, FMT, AL>, set, smem);
+  if (e != cudaSuccess) return e;
+  // as many blocks as an SM holds (64 registers a thread), each with its share of the rows
+  const int64_t resident = static_cast<int64_t>(sms) * (1024 / block);
+  const int64_t want = (p.rows + per - 1) / per;
+  return launch_pdl(norm_kernel<T, C, FMT, AL>, dim3(static_cast<unsigned>(want < resident ? want : resident)),
+                    dim3(block), smem, st, p, tpr);
 }
 
 template <typename T, int FMT>
 cudaError_t launch_norm_t(const NormParams& p, int sms, cudaStream_t st) {
   const int64_t group = FMT == FMT_NONE ? 8 : Fmt<FMT == FMT_NONE ? 0 : FMT>::kGroup;
-  const int64_t chunks = (p.cols + group - 1) / group * group / 8;
-  if (p.vec && chunks <= 2 * 1024) {
-    const RowShape s = row_shape(chunks, p.rows, sms);
-    const int block = s.tpr > kBlockThreads ? s.tpr : kBlockThreads;
-    const int per = block / s.tpr;
-    const int64_t want = (p.rows + per - 1) / per;
-    const int grid = static_cast<int>(want < static_cast<int64_t>(sms) * 64 ? want : static_cast<int64_t>(sms) * 64);
-    if (s.c == 1) return launch_pdl(norm_kernel<T, 1, FMT>, dim3(grid), dim3(block), 0, st, p, s.tpr);
-    if (s.c == 2) return launch_pdl(norm_kernel<T, 2, FMT>, dim3(grid), dim3(block), 0, st, p, s.tpr);
-    return launch_pdl(norm_kernel<T, 4, FMT>, dim3(grid), dim3(block), 0, st, p, s.tpr);
+  const int64_t span = (p.cols + group - 1) / group * group;
+  if (span <= kMaxCols) {
+    // few rows: one chunk a thread (latency); many: two, so that a row's barrier costs less
+    const RowShape s = row_shape(span / 8, p.rows <= sms);
+    if (p.aligned)
+      return s.c == 1 ? launch_norm_c<T, 1, FMT, true>(p, s.tpr, sms, st)
+                      : launch_norm_c<T, 2, FMT, true>(p, s.tpr, sms, st);
+    return s.c == 1 ? launch_norm_c<T, 1, FMT, false>(p, s.tpr, sms, st)
+                    : launch_norm_c<T, 2, FMT, false>(p, s.tpr, sms, st);
   }
-  int tpr = 32;
-  while (tpr < 1024 && tpr * 16 < p.cols) tpr *= 2;
-  const int block = tpr > kBlockThreads ? tpr : kBlockThreads;
-  const int per = block / tpr;
-  const int64_t want = (p.rows + per - 1) / per;
-  const int grid = static_cast<int>(want < static_cast<int64_t>(sms) * 64 ? want : static_cast<int64_t>(sms) * 64);
-  return launch_pdl(norm_any_kernel<T, FMT>, dim3(grid), dim3(block), 0, st, p, tpr);
+  return launch_pdl(norm_long_kernel<T, FMT>,
+                    dim3(static_cast<unsigned>(p.rows < 65536 ? p.rows : 65536)), dim3(kMaxThreads), 0, st, p);
 }
 
 template <typename T>
@@ -278,87 +395,137 @@ cudaError_t launch_norm_f(const NormParams& p, int sms, cudaStream_t st) {
 
 // ----------------------------------------------------------- backward
 
-// Each block walks rows blockIdx.x, + gridDim.x, ... and keeps its share of dw
-// in registers; at its end it leaves them as one row of partial sums.
+// Rows in shared memory: what fits beside each other for 1024 threads.
 template <typename T, int C>
-__global__ void __launch_bounds__(1024) norm_bwd_kernel(const __grid_constant__ NormBwdParams p) {
+constexpr int bwd_depth() {
+  const int row = 32 * C * 3 * WarpRow<T>::kBytes;
+  return 3 * row <= 210 * 1024 ? 3 : (2 * row <= 210 * 1024 ? 2 : 1);
+}
+
+// A block of 1024 threads takes 1024 / tpr rows at a time.  Each thread keeps its
+// columns' share of dw in registers; at the end the block's row groups add theirs
+// up and leave one row of partial sums.
+template <typename T, int C, bool AL>
+__global__ void __launch_bounds__(kMaxThreads)
+    norm_bwd_kernel(const __grid_constant__ NormBwdParams p, int tpr) {
   __shared__ float slots[64];
+  extern __shared__ uint8_t ring_raw[];
   ptx::griddep_launch_dependents();
-  const int t = threadIdx.x, tpr = blockDim.x;
+  constexpr int D = bwd_depth<T, C>();
+  const int per_block = kMaxThreads / tpr;
+  const int sub = threadIdx.x / tpr, t = threadIdx.x % tpr;
+  const int lane = threadIdx.x & 31;
   const int32_t cols = p.cols;
+  const int32_t warp_col = (t - lane) * 8;
+  constexpr uint32_t kBuf = WarpRow<T>::kBytes;
+  constexpr uint32_t kRow = (kMaxThreads / 32) * C * 3 * kBuf;
+  const uint32_t ring = ptx::smem_addr(ring_raw) + (threadIdx.x >> 5) * (C * 3 * kBuf);
+  const int64_t step = static_cast<int64_t>(gridDim.x) * per_block;
+  int64_t row = static_cast<int64_t>(blockIdx.x) * per_block + sub;
+  const bool has_dh = p.dh != nullptr;
+  RowReader<T, AL> dy, h, dh;
+  dy.init(p.dy, p.lddy, row, t * 8);
+  h.init(p.h, p.ldh, row, t * 8);
+  dh.init(p.dh, p.lddh, row, t * 8);
   ptx::griddep_wait();
-  float dw[C][8];
+  float2 dw[C][4];
 #pragma unroll
   for (int c = 0; c < C; ++c)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) dw[c][i] = 0.f;
-  int flip = 0;
-  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
-    const T* dy = static_cast<const T*>(p.dy) + row * p.lddy;
-    const T* h = static_cast<const T*>(p.h) + row * p.ldh;
-    Raw8<T> dyr[C], hr[C], er[C];
+    for (int i = 0; i < 4; ++i) dw[c][i] = make_float2(0.f, 0.f);
+  float2 wk[4];  // one chunk a thread: its weights stay in registers
+  if (C == 1) load_weight(p.weight, p.w_dtype, p.w_vec, t * 8, cols, wk);
+  int64_t ahead = row;
+  const auto start = [&](int slot) {
+    if (ahead < p.rows) {
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        const uint32_t dst = ring + slot * kRow + c * 3 * kBuf;
+        const int32_t col = (t + c * tpr) * 8, over = c * tpr * 8;
+        dy.copy(dst, col, over, cols, ahead == 0);
+        h.copy(dst + kBuf, col, over, cols, ahead == 0);
+        if (has_dh) dh.copy(dst + 2 * kBuf, col, over, cols, ahead == 0);
+      }
+      dy.next += step * p.lddy;
+      h.next += step * p.ldh;
+      dh.next += step * p.lddh;
+    }
+    ahead += step;
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int s = 0; s + 1 < D; ++s) start(s);
+  const float inv_cols = 1.f / static_cast<float>(cols);
+  int slot = 0, flip = 0;
+  for (; row < p.rows; row += step) {
+    if constexpr (!AL) __syncwarp();
+    start((slot + D - 1) % D);
     const float inv = p.inv[row];
+    const float2 inv2 = make_float2(inv, inv);
+    cp_async_wait<D - 1>();
+    if constexpr (!AL) __syncwarp();
+    const uint32_t src = ring + slot * kRow;
+    Raw8<T> hr[C];
+    float2 g[C][4];
+    float2 dot = make_float2(0.f, 0.f);
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       const int32_t col = (t + c * tpr) * 8;
-      if (col < cols) {
-        dyr[c] = load8(dy + col);
-        hr[c] = load8(h + col);
-        if (p.dh != nullptr) er[c] = load8(static_cast<const T*>(p.dh) + row * p.lddh + col);
+      float2 hv[4], w[4];
+      widen(take_chunk<T, AL>(src + c * 3 * kBuf, static_cast<const T*>(p.dy) + row * p.lddy, col, cols), g[c]);
+      hr[c] = take_chunk<T, AL>(src + c * 3 * kBuf + kBuf, static_cast<const T*>(p.h) + row * p.ldh, col, cols);
+      widen(hr[c], hv);
+      if (C > 1) load_weight(p.weight, p.w_dtype, p.w_vec, col, cols, w);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        dw[c][i] = __ffma2_rn(g[c][i], __fmul2_rn(hv[i], inv2), dw[c][i]);
+        g[c][i] = __fmul2_rn(g[c][i], C > 1 ? w[i] : wk[i]);
+        dot = __ffma2_rn(g[c][i], hv[i], dot);
       }
     }
-    float dot = 0.f;
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const int32_t col = (t + c * tpr) * 8;
-      if (col < cols) {
-        float a[8], b[8], w[8];
-        widen(dyr[c], a);
-        widen(hr[c], b);
-        load8_any(p.weight, col, p.w_dtype, w);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          dw[c][i] = fmaf(a[i], b[i] * inv, dw[c][i]);
-          dot = fmaf(a[i] * w[i], b[i], dot);
-        }
-      }
-    }
-    dot = row_sum(dot, tpr, slots, flip);
+    const float sum = row_sum(dot.x + dot.y, tpr, slots, flip, sub);
     flip ^= 1;
-    const float k = dot / static_cast<float>(cols) * inv * inv;
+    const float k = -(sum * inv_cols) * inv * inv;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       const int32_t col = (t + c * tpr) * 8;
-      if (col < cols) {
-        float a[8], b[8], w[8], e[8];
-        widen(dyr[c], a);
-        widen(hr[c], b);
-        load8_any(p.weight, col, p.w_dtype, w);
-        if (p.dh != nullptr) {
-          widen(er[c], e);
-        } else {
+      if (warp_col + c * tpr * 8 >= cols) continue;
+      float2 v[4];
+      widen(hr[c], v);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) e[i] = 0.f;
-        }
+      for (int i = 0; i < 4; ++i) g[c][i] = __fmul2_rn(inv2, __ffma2_rn(v[i], make_float2(k, k), g[c][i]));
+      if (has_dh) {
+        widen(take_chunk<T, AL>(src + c * 3 * kBuf + 2 * kBuf, static_cast<const T*>(p.dh) + row * p.lddh, col, cols), v);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) a[i] = fmaf(inv, fmaf(-b[i], k, a[i] * w[i]), e[i]);
-        store8(static_cast<T*>(p.dx) + row * p.lddx + col, narrow<T>(a));
+        for (int i = 0; i < 4; ++i) g[c][i] = __fadd2_rn(g[c][i], v[i]);
       }
+      put_chunk<T, AL>(static_cast<T*>(p.dx) + row * p.lddx, col, cols, narrow<T>(g[c]));
     }
+    slot = (slot + 1) % D;
   }
-  if (p.dw != nullptr) {
+  if (p.dw == nullptr) return;
+  // the row groups' sums, added in their order
+  cp_async_wait<0>();
+  __syncthreads();
+  float* sums = reinterpret_cast<float*>(ring_raw);  // [group][column]
+  const int32_t pitch = tpr * C * 8;
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const int32_t col = (t + c * tpr) * 8;
-      if (col < cols) store8_any(p.partials, static_cast<int64_t>(blockIdx.x) * cols + col, 4, dw[c]);
-    }
+  for (int c = 0; c < C; ++c)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      *reinterpret_cast<float2*>(sums + sub * pitch + (t + c * tpr) * 8 + 2 * i) = dw[c][i];
+  __syncthreads();
+  for (int32_t col = threadIdx.x; col < cols; col += kMaxThreads) {
+    float s = 0.f;
+    for (int g = 0; g < per_block; ++g) s += sums[g * pitch + col];
+    p.partials[static_cast<int64_t>(blockIdx.x) * cols + col] = s;
   }
 }
 
-// Any alignment and any length: one value a lane, the rows read twice.  dw is
-// summed by columns in a kernel of its own (norm_bwd_dw_any_kernel).
+// Rows too long for a block's registers: one value a lane, the rows read twice.  dw
+// is summed by columns in a kernel of its own.
 template <typename T>
-__global__ void norm_bwd_any_kernel(const __grid_constant__ NormBwdParams p) {
+__global__ void norm_bwd_long_kernel(const __grid_constant__ NormBwdParams p) {
   __shared__ float slots[64];
   ptx::griddep_launch_dependents();
   const int t = threadIdx.x, tpr = blockDim.x;
@@ -373,7 +540,7 @@ __global__ void norm_bwd_any_kernel(const __grid_constant__ NormBwdParams p) {
 #pragma unroll 4
     for (int32_t col = t; col < cols; col += tpr)
       dot = fmaf(to_float<T>(dy[col]) * load_any(p.weight, col, p.w_dtype), to_float<T>(h[col]), dot);
-    dot = row_sum(dot, tpr, slots, flip);
+    dot = row_sum(dot, tpr, slots, flip, 0);
     flip ^= 1;
     const float k = dot / static_cast<float>(cols) * inv * inv;
 #pragma unroll 4
@@ -388,7 +555,7 @@ __global__ void norm_bwd_any_kernel(const __grid_constant__ NormBwdParams p) {
 
 // Partial dw of rows blockIdx.y, + gridDim.y, ... for 256 columns.
 template <typename T>
-__global__ void norm_bwd_dw_any_kernel(const __grid_constant__ NormBwdParams p) {
+__global__ void norm_bwd_long_dw_kernel(const __grid_constant__ NormBwdParams p) {
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
   const int32_t col = blockIdx.x * blockDim.x + threadIdx.x;
@@ -401,57 +568,64 @@ __global__ void norm_bwd_dw_any_kernel(const __grid_constant__ NormBwdParams p) 
   p.partials[static_cast<int64_t>(blockIdx.y) * p.cols + col] = s;
 }
 
-// dw[col] = the partial rows' sum: 32 columns a block, eight warps a column
-// share the rows, joined in a fixed order.
-__global__ void norm_bwd_dw_kernel(const float* partials, int blocks, int32_t cols, float* dw) {
-  __shared__ float part[8][33];
+// dw[col] = the partial rows' sum: 32 columns a block, and 32 warps that share
+// the rows, joined in a fixed order.
+__global__ void __launch_bounds__(1024)
+    norm_bwd_dw_kernel(const float* partials, int blocks, int32_t cols, float* dw) {
+  __shared__ float part[32][33];
   ptx::griddep_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int32_t col = blockIdx.x * 32 + lane;
   ptx::griddep_wait();
   float s = 0.f;
   if (col < cols) {
-#pragma unroll 4
-    for (int b = warp; b < blocks; b += 8) s += partials[static_cast<int64_t>(b) * cols + col];
+#pragma unroll 8
+    for (int b = warp; b < blocks; b += 32) s += partials[static_cast<int64_t>(b) * cols + col];
   }
   part[warp][lane] = s;
   __syncthreads();
-  if (warp == 0 && col < cols) {
-    float v = part[0][lane];
-#pragma unroll
-    for (int i = 1; i < 8; ++i) v += part[i][lane];
-    dw[col] = v;
-  }
+  s = warp_sum(part[lane][warp]);  // column `warp` of the block
+  if (lane == 0 && blockIdx.x * 32 + warp < cols) dw[blockIdx.x * 32 + warp] = s;
+}
+
+template <typename T, int C, bool AL>
+cudaError_t launch_norm_bwd_c(const NormBwdParams& p, int tpr, int blocks, cudaStream_t st) {
+  static std::atomic<size_t> set[64];
+  constexpr size_t smem = static_cast<size_t>(bwd_depth<T, C>()) * 32 * C * 3 * WarpRow<T>::kBytes;
+  const cudaError_t e = allow_smem(norm_bwd_kernel<T, C, AL>, set, smem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(norm_bwd_kernel<T, C, AL>, dim3(blocks), dim3(kMaxThreads), smem, st, p, tpr);
 }
 
 template <typename T>
 cudaError_t launch_norm_bwd_t(const NormBwdParams& p, int sms, cudaStream_t st) {
-  const int blocks = norm_bwd_blocks(p.rows, sms);
-  const int64_t chunks = (p.cols + 7) / 8;
+  int blocks = norm_bwd_blocks(p.rows, sms);
   cudaError_t e;
   if (p.rows == 0) {
     // no rows: dw is zero
-  } else if (p.vec && p.cols % 8 == 0 && chunks <= 2 * 1024) {
-    int c = 1, threads = 32;
-    while (threads < 1024 && static_cast<int64_t>(threads) * 2 < chunks) threads *= 2;
-    while (static_cast<int64_t>(threads) * c < chunks) c *= 2;
-    if (c == 1) e = launch_pdl(norm_bwd_kernel<T, 1>, dim3(blocks), dim3(threads), 0, st, p);
-    else e = launch_pdl(norm_bwd_kernel<T, 2>, dim3(blocks), dim3(threads), 0, st, p);
+  } else if (p.cols <= kMaxCols) {
+    const RowShape s = row_shape((p.cols + 7) / 8, true);
+    const int64_t want = (p.rows + kMaxThreads / s.tpr - 1) / (kMaxThreads / s.tpr);
+    if (want < blocks) blocks = static_cast<int>(want);
+    if (p.aligned)
+      e = s.c == 1 ? launch_norm_bwd_c<T, 1, true>(p, s.tpr, blocks, st)
+                   : launch_norm_bwd_c<T, 2, true>(p, s.tpr, blocks, st);
+    else
+      e = s.c == 1 ? launch_norm_bwd_c<T, 1, false>(p, s.tpr, blocks, st)
+                   : launch_norm_bwd_c<T, 2, false>(p, s.tpr, blocks, st);
     if (e != cudaSuccess) return e;
   } else {
-    int threads = 32;
-    while (threads < 1024 && threads * 8 < p.cols) threads *= 2;
     // dw first: dx may overwrite dy or h
     if (p.dw != nullptr) {
-      e = launch_pdl(norm_bwd_dw_any_kernel<T>, dim3((p.cols + 255) / 256, blocks), dim3(256), 0, st, p);
+      e = launch_pdl(norm_bwd_long_dw_kernel<T>, dim3((p.cols + 255) / 256, blocks), dim3(256), 0, st, p);
       if (e != cudaSuccess) return e;
     }
-    e = launch_pdl(norm_bwd_any_kernel<T>, dim3(static_cast<unsigned>(p.rows < 65536 ? p.rows : 65536)),
-                   dim3(threads), 0, st, p);
+    e = launch_pdl(norm_bwd_long_kernel<T>, dim3(static_cast<unsigned>(p.rows < 65536 ? p.rows : 65536)),
+                   dim3(kMaxThreads), 0, st, p);
     if (e != cudaSuccess) return e;
   }
   if (p.dw == nullptr) return cudaSuccess;
-  return launch_pdl(norm_bwd_dw_kernel, dim3((p.cols + 31) / 32), dim3(256), 0, st,
+  return launch_pdl(norm_bwd_dw_kernel, dim3((p.cols + 31) / 32), dim3(1024), 0, st,
                     static_cast<const float*>(p.partials), blocks, p.cols, p.dw);
 }
 
@@ -464,8 +638,7 @@ cudaError_t launch_norm(const NormParams& p, int sms, cudaStream_t st) {
 }
 
 int norm_bwd_blocks(int64_t rows, int sms) {
-  const int64_t most = 2 * static_cast<int64_t>(sms);
-  return static_cast<int>(rows < most ? rows : most);
+  return static_cast<int>(rows < sms ? rows : sms);
 }
 
 cudaError_t launch_norm_bwd(const NormBwdParams& p, int sms, cudaStream_t st) {

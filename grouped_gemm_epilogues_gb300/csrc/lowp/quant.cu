@@ -5,9 +5,8 @@
 // row-major matrix (stride_row 1), as the weight-gradient products need it: a
 // tile then goes through shared memory.  Both forms read the source once and
 // are bound by memory.
-#include "../gge_ptx.cuh"
 #include "lowp_launch.h"
-#include "mx_format.cuh"
+#include "rows.cuh"
 
 namespace gge {
 namespace lowp {
@@ -22,163 +21,344 @@ __device__ __forceinline__ QuantOut quant_out(const QuantPtrs& q, int64_t batch)
                   q.values == nullptr
                       ? nullptr
                       : static_cast<void*>(static_cast<uint8_t*>(q.values) + batch * q.values_batch_stride * vs),
-                  q.ldv, q.v_dtype, q.v_vec};
+                  q.ldv, q.v_dtype};
 }
 
-// Columns contiguous: a lane takes eight of them, and the lanes of one scale
-// word (16, or 8 for nvfp4) stay in one row; words are numbered row by row.
-template <typename T, int FMT>
-__global__ void quantize_rows_kernel(const __grid_constant__ QuantParams p) {
-  constexpr int kLanes = Fmt<FMT>::kGroup / 8;
+// A block's eight warps cover 256 columns each: `wx` of them side by side, the
+// others below, and kRowsAWarp rows a warp, whose loads are in flight together.
+constexpr int kRowsAWarp = 4;
+
+struct RowTiles {
+  int32_t wx;         // warps along the columns: 1, 2, 4 or 8
+  int32_t across;     // blocks along the columns
+};
+
+__host__ __device__ __forceinline__ int64_t rows_a_block(const RowTiles& r) { return 8 / r.wx * kRowsAWarp; }
+
+RowTiles row_tiles(int64_t span) {
+  RowTiles r{1, 1};
+  while (r.wx < 8 && r.wx * 256 < span) r.wx *= 2;
+  r.across = static_cast<int32_t>((span + r.wx * 256 - 1) / (r.wx * 256));
+  return r;
+}
+
+dim3 row_grid(const RowTiles& r, int64_t rows, int64_t batch) {
+  const int64_t down = (rows + rows_a_block(r) - 1) / rows_a_block(r);
+  return dim3(static_cast<unsigned>(down * r.across), static_cast<unsigned>(batch));
+}
+
+// This warp's first row and this lane's first column.
+__device__ __forceinline__ void warp_place(const RowTiles& r, int64_t& row, int32_t& col) {
+  const int warp = threadIdx.x >> 5;
+  const uint32_t down = blockIdx.x / static_cast<uint32_t>(r.across);
+  const uint32_t over = blockIdx.x - down * static_cast<uint32_t>(r.across);
+  row = down * rows_a_block(r) + warp / r.wx * kRowsAWarp;
+  col = (static_cast<int32_t>(over) * r.wx + warp % r.wx) * 256 + (threadIdx.x & 31) * 8;
+}
+
+// Columns contiguous.  AL: every row of the source (and of the values) starts on a
+// 16-byte boundary.
+template <typename T, int FMT, bool AL>
+__global__ void __launch_bounds__(256)
+    quantize_rows_kernel(const __grid_constant__ QuantParams p, RowTiles tiles) {
+  constexpr int B = Fmt<FMT>::kBlock;
   ptx::griddep_launch_dependents();
-  ptx::griddep_wait();
   const int64_t batch = blockIdx.y;
   const QuantOut q = quant_out(p.q, batch);
   const T* x = static_cast<const T*>(p.x) + batch * p.stride_batch;
-  const float tscale = (FMT == FMT_NVFP4 && q.tensor_scale) ? *q.tensor_scale : 1.f;
-  const int64_t words = p.rows * q.kgroups;
-  const int64_t per_block = blockDim.x / kLanes;
   const int32_t cols = static_cast<int32_t>(p.cols);
-  for (int64_t w0 = blockIdx.x * per_block; w0 < words; w0 += gridDim.x * per_block) {
-    const int64_t w = w0 + threadIdx.x / kLanes;
-    const bool live = w < words;
-    const int64_t row = live ? w / q.kgroups : 0;
-    const int32_t col = static_cast<int32_t>(live ? w - row * q.kgroups : 0) * Fmt<FMT>::kGroup +
-                        static_cast<int32_t>(threadIdx.x % kLanes) * 8;
-    float v[8];
-    const T* src = x + row * p.stride_row + col;
-    if (live && p.vec && col + 8 <= cols) {
-      widen(load8(src), v);
-    } else {
+  int64_t row0;
+  int32_t col;
+  warp_place(tiles, row0, col);
+  if (col - (threadIdx.x & 31) * 8 >= cols) return;
+  const int32_t rows = static_cast<int32_t>(min(p.rows - row0, static_cast<int64_t>(kRowsAWarp)));
+  const T* src = x + row0 * p.stride_row;
+  uint8_t* codes = q.codes + row0 * q.ld + static_cast<int64_t>(col) * Fmt<FMT>::kBits / 8;
+  // (a warp's rows share a scale tile's 32-row stretch: kRowsAWarp divides 32)
+  uint8_t* scales = q.scales + scale_word(row0, col / Fmt<FMT>::kGroup, q.kgroups);
+  const bool word = holds_word<FMT>() && col < q.kgroups * Fmt<FMT>::kGroup;
+  const bool code = col < ((cols + 31) & ~31);
+  const bool past = col >= (cols + B - 1) / B * B;
+  ptx::griddep_wait();
+  const float tscale = (FMT == FMT_NVFP4 && q.tensor_scale) ? *q.tensor_scale : 1.f;
+  Raw8<T> raw[kRowsAWarp];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = live && col + i < cols ? to_float<T>(src[i]) : 0.f;
+  for (int u = 0; u < kRowsAWarp; ++u) {
+#pragma unroll
+    for (int j = 0; j < WarpRow<T>::kPieces; ++j) raw[u].w[j] = make_uint4(0u, 0u, 0u, 0u);
+    if (u < rows && col < cols) {
+      const T* row = src + u * p.stride_row;
+      if (AL && col + 8 <= cols) raw[u] = load8(row + col);
+      else raw[u] = load_row8(row, col, cols, x);
     }
-    quantise_chunk<FMT>(q, v, row, col, cols, tscale, live);
+  }
+#pragma unroll
+  for (int u = 0; u < kRowsAWarp; ++u) {
+    if (u >= rows) break;  // (the whole warp)
+    float2 v[4];
+    widen(raw[u], v);
+    const Quantised z = quantise8<FMT>(v, tscale, past);
+    if (word) *reinterpret_cast<uint32_t*>(scales + u * 16) = z.word;
+    if (code) store_codes<FMT>(codes + u * q.ld, z.codes);
+    if (q.values != nullptr) {
+      code_values<FMT>(z.codes, z.unit, tscale, v);
+      store_row8_any<AL>(q.values, (row0 + u) * q.ldv, q.v_dtype, col, cols, v);
+    }
   }
 }
 
-// Rows contiguous (the transpose of a row-major source): a block takes 64 rows x
-// 128 columns, reads source lines of 64 values, and each thread quantises 8
-// columns of one row out of shared memory.
-constexpr int kTRows = 64, kTCols = 128;
+// Rows contiguous (the transpose of a row-major source): a block takes a tile of
+// 128 rows (64 of 32-bit values) x 128 columns through shared memory.  A thread
+// then holds 32 columns of the row pair (row) that one shared-memory word holds,
+// whole blocks, and finds their scales by itself.  A word's column is kPitch words
+// from the next, an odd number, so reads along either direction of the tile are
+// free of bank conflicts.
+constexpr int kTCols = 128, kTWords = 64, kTPitch = kTWords + 1;
 
-template <typename T, int FMT>
+// One row's 32 values v (of a part's columns), quantised: codes to w, a scale byte
+// a block to `bytes`, and the values of the codes back to v.
+template <int FMT>
+__device__ __forceinline__ void quantise32(float (&v)[32], float tscale, int32_t col, int32_t cols,
+                                           uint32_t (&w)[8], uint8_t* bytes, bool values) {
+  constexpr int B = Fmt<FMT>::kBlock;
+#pragma unroll
+  for (int k = 0; k < 32; k += B) {
+    float m = 0.f;
+#pragma unroll
+    for (int i = 0; i < B; ++i) m = max_abs(m, v[k + i]);
+    float factor;
+    const uint32_t s = block_scale<FMT>(abs_bits(m), tscale, factor);
+    const float unit = scale_value<FMT>(s);
+    bytes[k / B] = static_cast<uint8_t>(col + k < cols ? s : 0u);
+#pragma unroll
+    for (int i = k; i < k + B; i += 8) {
+      float c[8];
+#pragma unroll
+      for (int j = 0; j < 8; j += 2) {
+        const float2 f = __fmul2_rn(make_float2(v[i + j], v[i + j + 1]), make_float2(factor, factor));
+        c[j] = f.x;
+        c[j + 1] = f.y;
+      }
+      const uint2 codes = pack8<FMT>(c);
+      if constexpr (FMT == FMT_MXFP8) {
+        w[i / 4] = codes.x;
+        w[i / 4 + 1] = codes.y;
+      } else {
+        w[i / 8] = codes.x;
+      }
+      if (values) {
+        float2 f[4];
+        code_values<FMT>(codes, unit, tscale, f);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          v[i + 2 * j] = f[j].x;
+          v[i + 2 * j + 1] = f[j].y;
+        }
+      }
+    }
+  }
+}
+
+template <typename T, int FMT, bool AL>
 __global__ void __launch_bounds__(256) quantize_cols_kernel(const __grid_constant__ QuantParams p) {
-  __shared__ T tile[kTCols][kTRows + 4 / sizeof(T)];
+  constexpr int V = 4 / sizeof(T);         // rows a word holds
+  constexpr int kRows = kTWords * V;       // rows of the tile
+  constexpr int kBytes = kTCols / Fmt<FMT>::kBlock;  // scale bytes of a row of the tile
+  __shared__ uint32_t tile[kTCols * kTPitch];
+  __shared__ uint32_t words[kRows * kBytes / 4];
   ptx::griddep_launch_dependents();
-  ptx::griddep_wait();
   const int64_t batch = blockIdx.z;
   const QuantOut q = quant_out(p.q, batch);
   const T* x = static_cast<const T*>(p.x) + batch * p.stride_batch;
-  const float tscale = (FMT == FMT_NVFP4 && q.tensor_scale) ? *q.tensor_scale : 1.f;
-  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * kTRows;
-  const int32_t cols = static_cast<int32_t>(p.cols);
+  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * kRows;
+  const int32_t rows = static_cast<int32_t>(p.rows), cols = static_cast<int32_t>(p.cols);
   const int32_t col0 = blockIdx.y * kTCols;
-  const int r = threadIdx.x % kTRows;
-  for (int c = threadIdx.x / kTRows; c < kTCols; c += 256 / kTRows) {
-    const int32_t col = col0 + c;
-    T v = from_float<T>(0.f);
-    if (row0 + r < p.rows && col < cols) v = x[col * p.stride_col + row0 + r];
-    tile[c][r] = v;
+  ptx::griddep_wait();
+  const float tscale = (FMT == FMT_NVFP4 && q.tensor_scale) ? *q.tensor_scale : 1.f;
+  {
+    // 8 rows of one column a piece; kTCols * kRows / 8 pieces
+    constexpr int kAcross = kRows / 8, kDown = 256 / kAcross, kPieces = kTCols / kDown;
+    const int r = threadIdx.x % kAcross * 8, c = threadIdx.x / kAcross;
+    const int32_t row = static_cast<int32_t>(row0) + r;
+    Raw8<T> raw[kPieces];
+#pragma unroll
+    for (int u = 0; u < kPieces; ++u) {
+#pragma unroll
+      for (int j = 0; j < WarpRow<T>::kPieces; ++j) raw[u].w[j] = make_uint4(0u, 0u, 0u, 0u);
+      const int32_t col = col0 + c + kDown * u;
+      if (row < rows && col < cols) {
+        const T* line = x + col * p.stride_col;
+        if (AL && row + 8 <= rows) raw[u] = load8(line + row);
+        else raw[u] = load_row8(line, row, rows, x);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kPieces; ++u) {
+      const uint32_t* w = reinterpret_cast<const uint32_t*>(&raw[u]);
+#pragma unroll
+      for (int i = 0; i < 8 / V; ++i) tile[(c + kDown * u) * kTPitch + r / V + i] = w[i];
+    }
   }
   __syncthreads();
-  // 16 consecutive threads take the 16 chunks of a row, so that its codes are
-  // written in whole lines
-  const int chunk = threadIdx.x % 16;
-  for (int rr = threadIdx.x / 16; rr < kTRows; rr += 16) {
-    float v[8];
+  const int part = threadIdx.x / kTWords, at = threadIdx.x % kTWords;  // 32 columns a part
+  const int32_t col = col0 + part * 32;
+  uint32_t* mine = tile + part * 32 * kTPitch + at;
+  uint32_t pair[32];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = to_float<T>(tile[chunk * 8 + i][rr]);
-    const int32_t col = col0 + chunk * 8;
-    quantise_chunk<FMT>(q, v, row0 + rr, col, cols, tscale,
-                        row0 + rr < p.rows && col < q.kgroups * Fmt<FMT>::kGroup);
+  for (int i = 0; i < 32; ++i) pair[i] = mine[i * kTPitch];
+  // values of a 16-bit type, or of a source of 32 bits, go out through the tile
+  const bool staged = q.values != nullptr && (V == 1 || q.v_dtype != 4);
+#pragma unroll
+  for (int h = 0; h < V; ++h) {
+    const int64_t row = row0 + at * V + h;
+    float v[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      if constexpr (V == 1) v[i] = __uint_as_float(pair[i]);
+      else v[i] = h == 0 ? widen_pair<T>(pair[i]).x : widen_pair<T>(pair[i]).y;
+    }
+    uint32_t w[8];
+    quantise32<FMT>(v, tscale, col, cols, w,
+                    reinterpret_cast<uint8_t*>(words) + (at * V + h) * kBytes + part * (kBytes / 4),
+                    q.values != nullptr);
+    if (row < p.rows && col < ((cols + 31) & ~31)) {
+      uint4* dst = reinterpret_cast<uint4*>(q.codes + row * q.ld + static_cast<int64_t>(col) * Fmt<FMT>::kBits / 8);
+      dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+      if constexpr (FMT == FMT_MXFP8) dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+    if (staged) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        if constexpr (V == 1) {
+          pair[i] = __float_as_uint(v[i]);
+        } else {
+          const uint32_t n = q.v_dtype == 1 ? narrow_pair<__half>(make_float2(v[i], v[i]))
+                                            : narrow_pair<__nv_bfloat16>(make_float2(v[i], v[i]));
+          pair[i] = __byte_perm(pair[i], n, h == 0 ? 0x3254 : 0x5410);
+        }
+      }
+    } else if (q.values != nullptr && row < p.rows) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        if (col + i < cols) static_cast<float*>(q.values)[row * q.ldv + col + i] = v[i];
+    }
+  }
+  if (staged) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) mine[i * kTPitch] = pair[i];
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < kRows * kBytes / 4; i += 256) {
+    const int rr = i % kRows, kw = i / kRows;
+    const int64_t kg = col0 / Fmt<FMT>::kGroup + kw;
+    if (row0 + rr < p.rows && kg < q.kgroups)
+      *reinterpret_cast<uint32_t*>(q.scales + scale_word(row0 + rr, kg, q.kgroups)) = words[rr * (kBytes / 4) + kw];
+  }
+  if (!staged) return;
+  // a warp a word of rows, one column a lane: whole lines at any alignment
+  const int lane = threadIdx.x & 31;
+  for (int r = threadIdx.x >> 5; r < kTWords; r += 8) {
+    const int64_t row = row0 + r * V;
+    if (row >= p.rows) break;
+#pragma unroll
+    for (int c = lane; c < kTCols; c += 32) {
+      if (col0 + c >= cols) break;
+      const uint32_t w = tile[c * kTPitch + r];
+      const int64_t out = row * q.ldv + col0 + c;
+      if constexpr (V == 1) {
+        store_any(q.values, out, q.v_dtype, __uint_as_float(w));
+      } else {
+        static_cast<uint16_t*>(q.values)[out] = static_cast<uint16_t>(w);
+        if (row + 1 < p.rows) static_cast<uint16_t*>(q.values)[out + q.ldv] = static_cast<uint16_t>(w >> 16);
+      }
+    }
   }
 }
 
-template <typename T, int FMT>
-cudaError_t launch_quantize_t(const QuantParams& p, int sms, cudaStream_t st) {
-  if (p.stride_col == 1 || p.cols == 1) {
-    constexpr int kLanes = Fmt<FMT>::kGroup / 8;
-    const int64_t words = p.rows * p.q.kgroups;
-    const int64_t want = (words + 256 / kLanes - 1) / (256 / kLanes);
-    const int64_t most = static_cast<int64_t>(sms) * 64;
-    return launch_pdl(quantize_rows_kernel<T, FMT>,
-                      dim3(static_cast<unsigned>(want < most ? want : most), static_cast<unsigned>(p.batch)),
-                      dim3(256), 0, st, p);
-  }
+template <typename T, int FMT, bool AL>
+cudaError_t launch_quantize_t(const QuantParams& p, cudaStream_t st) {
   const int64_t span = p.q.kgroups * Fmt<FMT>::kGroup;
-  return launch_pdl(quantize_cols_kernel<T, FMT>,
-                    dim3(static_cast<unsigned>((p.rows + kTRows - 1) / kTRows),
+  if (p.stride_col == 1 || p.cols == 1) {
+    const RowTiles tiles = row_tiles(span);
+    return launch_pdl(quantize_rows_kernel<T, FMT, AL>, row_grid(tiles, p.rows, p.batch), dim3(256), 0, st,
+                      p, tiles);
+  }
+  constexpr int kRows = kTWords * (4 / sizeof(T));
+  return launch_pdl(quantize_cols_kernel<T, FMT, AL>,
+                    dim3(static_cast<unsigned>((p.rows + kRows - 1) / kRows),
                          static_cast<unsigned>((span + kTCols - 1) / kTCols),
                          static_cast<unsigned>(p.batch)),
                     dim3(256), 0, st, p);
 }
 
 template <typename T>
-cudaError_t launch_quantize_f(const QuantParams& p, int sms, cudaStream_t st) {
+cudaError_t launch_quantize_f(const QuantParams& p, cudaStream_t st) {
   switch (p.q.format) {
-    case FMT_MXFP8: return launch_quantize_t<T, FMT_MXFP8>(p, sms, st);
-    case FMT_MXFP4: return launch_quantize_t<T, FMT_MXFP4>(p, sms, st);
-    default: return launch_quantize_t<T, FMT_NVFP4>(p, sms, st);
+    case FMT_MXFP8: return p.aligned ? launch_quantize_t<T, FMT_MXFP8, true>(p, st)
+                                     : launch_quantize_t<T, FMT_MXFP8, false>(p, st);
+    case FMT_MXFP4: return p.aligned ? launch_quantize_t<T, FMT_MXFP4, true>(p, st)
+                                     : launch_quantize_t<T, FMT_MXFP4, false>(p, st);
+    default: return p.aligned ? launch_quantize_t<T, FMT_NVFP4, true>(p, st)
+                                     : launch_quantize_t<T, FMT_NVFP4, false>(p, st);
   }
 }
 
 // ------------------------------------------------------------- and back
 
-// Eight columns a thread.
-template <int FMT>
-__global__ void dequantize_kernel(const __grid_constant__ DequantParams p) {
+template <int FMT, bool AL>
+__global__ void __launch_bounds__(256)
+    dequantize_kernel(const __grid_constant__ DequantParams p, RowTiles tiles) {
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
   const int64_t batch = blockIdx.y;
   const uint8_t* codes = p.codes + batch * p.batch_stride;
   const uint8_t* scales = p.scales + batch * p.scale_batch_stride;
   const float tscale = (FMT == FMT_NVFP4 && p.tensor_scale) ? *p.tensor_scale : 1.f;
-  const int64_t chunks = (p.cols + 7) / 8;
-  const int64_t total = p.rows * chunks;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < total;
-       i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-    const int64_t row = i / chunks, col = (i - row * chunks) * 8;
-    const uint8_t* c = codes + row * p.ld + col * Fmt<FMT>::kBits / 8;
-    uint2 w = make_uint2(0u, 0u);
-    if constexpr (FMT == FMT_MXFP8) w = *reinterpret_cast<const uint2*>(c);
-    else w.x = *reinterpret_cast<const uint32_t*>(c);
+  const int32_t cols = static_cast<int32_t>(p.cols);
+  int64_t row0;
+  int32_t col;
+  warp_place(tiles, row0, col);
+  uint2 w[kRowsAWarp];
+  float unit[kRowsAWarp];
+#pragma unroll
+  for (int u = 0; u < kRowsAWarp; ++u) {
+    const int64_t row = row0 + u;
+    w[u] = make_uint2(0u, 0u);
+    unit[u] = 0.f;
+    if (row >= p.rows || col >= cols) continue;
+    const uint8_t* c = codes + row * p.ld + static_cast<int64_t>(col) * Fmt<FMT>::kBits / 8;
+    if constexpr (FMT == FMT_MXFP8) w[u] = *reinterpret_cast<const uint2*>(c);
+    else w[u].x = *reinterpret_cast<const uint32_t*>(c);
     const int64_t block = col / Fmt<FMT>::kBlock;
-    const float unit = scale_value<FMT>(scales[scale_word(row, block >> 2, p.kgroups) + (block & 3)]);
-    float v[8];
-    unpack8<FMT>(w, v);
+    unit[u] = scale_value<FMT>(scales[scale_word(row, block >> 2, p.kgroups) + (block & 3)]);
+  }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      v[j] *= unit;
-      if constexpr (FMT == FMT_NVFP4) v[j] *= tscale;
-    }
-    const int64_t at = batch * p.y_batch_stride + row * p.ldy + col;
-    if (p.vec && col + 8 <= p.cols) {
-      store8_any(p.y, at, p.dtype, v);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (col + j < p.cols) store_any(p.y, at + j, p.dtype, v[j]);
-    }
+  for (int u = 0; u < kRowsAWarp; ++u) {
+    if (row0 + u >= p.rows) break;
+    float2 v[4];
+    code_values<FMT>(w[u], unit[u], tscale, v);
+    store_row8_any<AL>(p.y, batch * p.y_batch_stride + (row0 + u) * p.ldy, p.dtype, col, cols, v);
   }
 }
 
 }  // namespace
 
-cudaError_t launch_quantize(const QuantParams& p, int sms, cudaStream_t st) {
-  if (p.dtype == 0) return launch_quantize_f<__nv_bfloat16>(p, sms, st);
-  if (p.dtype == 1) return launch_quantize_f<__half>(p, sms, st);
-  return launch_quantize_f<float>(p, sms, st);
+cudaError_t launch_quantize(const QuantParams& p, cudaStream_t st) {
+  if (p.dtype == 0) return launch_quantize_f<__nv_bfloat16>(p, st);
+  if (p.dtype == 1) return launch_quantize_f<__half>(p, st);
+  return launch_quantize_f<float>(p, st);
 }
 
-cudaError_t launch_dequantize(const DequantParams& p, int sms, cudaStream_t st) {
-  const int64_t want = (p.rows * ((p.cols + 7) / 8) + 255) / 256;
-  const int64_t most = static_cast<int64_t>(sms) * 64;
-  const dim3 grid(static_cast<unsigned>(want < most ? want : most), static_cast<unsigned>(p.batch));
+cudaError_t launch_dequantize(const DequantParams& p, cudaStream_t st) {
+  const RowTiles tiles = row_tiles(p.cols);
+  const dim3 grid = row_grid(tiles, p.rows, p.batch);
   switch (p.format) {
-    case FMT_MXFP8: return launch_pdl(dequantize_kernel<FMT_MXFP8>, grid, dim3(256), 0, st, p);
-    case FMT_MXFP4: return launch_pdl(dequantize_kernel<FMT_MXFP4>, grid, dim3(256), 0, st, p);
-    default: return launch_pdl(dequantize_kernel<FMT_NVFP4>, grid, dim3(256), 0, st, p);
+    case FMT_MXFP8: return launch_pdl(p.aligned ? dequantize_kernel<FMT_MXFP8, true> : dequantize_kernel<FMT_MXFP8, false>, grid,
+                                      dim3(256), 0, st, p, tiles);
+    case FMT_MXFP4: return launch_pdl(p.aligned ? dequantize_kernel<FMT_MXFP4, true> : dequantize_kernel<FMT_MXFP4, false>, grid,
+                                      dim3(256), 0, st, p, tiles);
+    default: return launch_pdl(p.aligned ? dequantize_kernel<FMT_NVFP4, true> : dequantize_kernel<FMT_NVFP4, false>, grid,
+                                      dim3(256), 0, st, p, tiles);
   }
 }
 

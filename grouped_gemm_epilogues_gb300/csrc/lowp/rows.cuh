@@ -1,0 +1,220 @@
+// Rows that start anywhere, read and written in 16-byte pieces.
+//
+// A warp's 32 lanes take 8 consecutive values each: 256 columns of a row.  Where
+// the row starts `b` bytes past a 16-byte boundary, the aligned pieces that
+// cover those columns are one more than a row that starts on one has.  They go
+// to shared memory by cp.async (several rows ahead, so that copies stay in
+// flight while a row is reduced and written), and each lane puts its 8 values
+// together from two neighbouring pieces.  No piece is read past the row's end
+// (cp.async takes only the bytes before it); in front of the row a piece holds
+// the end of the row before, and in front of the first row single values are
+// read.  Writing, the lanes shift their values to the row's boundaries among
+// themselves and store whole pieces; only the warp's two ends are single values.
+#pragma once
+
+#include "../gge_ptx.cuh"
+#include "mx_format.cuh"
+
+namespace gge {
+namespace lowp {
+
+using namespace mx;
+
+template <typename T>
+struct WarpRow {
+  static constexpr int kPieces = sizeof(T) / 2;                  // 16-byte pieces of 8 values
+  static constexpr int kBytes = (32 * kPieces + 1) * 16;         // of a warp's 256 columns
+};
+
+// Words w[i] of a 16-byte aligned stream, moved down by `b` bytes (a multiple of 2;
+// the same in every lane).
+template <int N>
+__device__ __forceinline__ void shift_down(uint32_t (&w)[N], uint32_t b) {
+  if (b & 8u) {
+#pragma unroll
+    for (int i = 0; i + 2 < N; ++i) w[i] = w[i + 2];
+  }
+  if (b & 4u) {
+#pragma unroll
+    for (int i = 0; i + 1 < N; ++i) w[i] = w[i + 1];
+  }
+  if (b & 2u) {
+#pragma unroll
+    for (int i = 0; i + 1 < N; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
+  }
+}
+
+// Start copying columns [col0, col0 + 256) of the row at `row` (`cols` long) to
+// `dst`.  `first`: nothing may be read in front of the row.
+template <typename T>
+__device__ __forceinline__ void copy_row(uint32_t dst, const T* row, int32_t col0, int32_t cols,
+                                         bool first) {
+  constexpr int P = WarpRow<T>::kPieces;
+  const int lane = threadIdx.x & 31;
+  const uintptr_t at = reinterpret_cast<uintptr_t>(row + col0);
+  const uint32_t b = static_cast<uint32_t>(at) & 15u;
+  const uintptr_t end = reinterpret_cast<uintptr_t>(row + cols);
+  const uintptr_t piece0 = at - b;
+#pragma unroll
+  for (int j = 0; j <= P; ++j) {
+    if (j == P && (lane != 31 || b == 0)) break;
+    const uint32_t k = static_cast<uint32_t>(lane * P + j);
+    const uintptr_t src = piece0 + 16u * k;
+    if (src >= end) continue;
+    const uint32_t bytes = static_cast<uint32_t>(min(static_cast<uintptr_t>(16), end - src));
+    if (src < reinterpret_cast<uintptr_t>(row) && first) {
+      for (uint32_t o = b; o < bytes; o += sizeof(T)) {
+        if constexpr (sizeof(T) == 2)
+          ptx::st_shared_u16(dst + 16u * k + o, *reinterpret_cast<const uint16_t*>(src + o));
+        else
+          ptx::st_shared_u32(dst + 16u * k + o, *reinterpret_cast<const uint32_t*>(src + o));
+      }
+    } else {
+      ptx::cp_async_16(dst + 16u * k, reinterpret_cast<const void*>(src), bytes);
+    }
+  }
+}
+
+// A lane's 8 values of a copied row, after the copy has landed (values past the
+// row's end are whatever the buffer held).  `b`: the row's offset from a 16-byte
+// boundary, the same for every 256 columns of it.
+template <typename T>
+__device__ __forceinline__ Raw8<T> take_row(uint32_t src, uint32_t b) {
+  constexpr int P = WarpRow<T>::kPieces;
+  const int lane = threadIdx.x & 31;
+  uint32_t w[4 * P + 4];
+#pragma unroll
+  for (int j = 0; j < P; ++j) {
+    const uint4 v = ptx::ld_shared_v4(src + 16u * (lane * P + j));
+    w[4 * j] = v.x, w[4 * j + 1] = v.y, w[4 * j + 2] = v.z, w[4 * j + 3] = v.w;
+  }
+  if (b != 0) {
+    const uint4 v = ptx::ld_shared_v4(src + 16u * (lane * P + P));
+    w[4 * P] = v.x, w[4 * P + 1] = v.y, w[4 * P + 2] = v.z, w[4 * P + 3] = v.w;
+    shift_down(w, b);
+  }
+  Raw8<T> r;
+#pragma unroll
+  for (int j = 0; j < P; ++j) r.w[j] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+  return r;
+}
+
+// The same straight from global memory, for a lane on its own: columns [col, col
+// + 8) of the row at `row`; values past its end are zero.  Reads whole pieces
+// inside [lo, row end) only.
+template <typename T>
+__device__ __forceinline__ Raw8<T> load_row8(const T* row, int32_t col, int32_t cols, const T* lo) {
+  constexpr int P = WarpRow<T>::kPieces;
+  const uintptr_t at = reinterpret_cast<uintptr_t>(row + col);
+  const uint32_t b = static_cast<uint32_t>(at) & 15u;
+  Raw8<T> r;
+  if (b == 0 && col + 8 <= cols) return load8(row + col);
+  const uintptr_t piece0 = at - b;
+  const uintptr_t end = reinterpret_cast<uintptr_t>(row + cols);
+  if (b != 0 && piece0 >= reinterpret_cast<uintptr_t>(lo) && piece0 + 16u * (P + 1) <= end) {
+    uint32_t w[4 * P + 4];
+#pragma unroll
+    for (int j = 0; j <= P; ++j) {
+      const uint4 v = *reinterpret_cast<const uint4*>(piece0 + 16u * j);
+      w[4 * j] = v.x, w[4 * j + 1] = v.y, w[4 * j + 2] = v.z, w[4 * j + 3] = v.w;
+    }
+    shift_down(w, b);
+#pragma unroll
+    for (int j = 0; j < P; ++j) r.w[j] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+    return r;
+  }
+  T* t = reinterpret_cast<T*>(&r);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) t[i] = col + i < cols ? row[col + i] : from_float<T>(0.f);
+  return r;
+}
+
+// Eight values in 16-byte pieces where the row allows it, for a lane on its own.
+template <typename T>
+__device__ __forceinline__ void store_row8_aligned(T* row, int32_t col, int32_t cols, const Raw8<T>& v) {
+  if (col + 8 <= cols) {
+    store8(row + col, v);
+  } else {
+    const T* t = reinterpret_cast<const T*>(&v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (col + i < cols) row[col + i] = t[i];
+  }
+}
+
+// Store 8 values a lane to columns [col, col + 8) of the row at `row`; columns >=
+// cols are not written.  Warp-collective.
+template <typename T>
+__device__ __forceinline__ void store_row8(T* row, int32_t col, int32_t cols, const Raw8<T>& v) {
+  constexpr int P = WarpRow<T>::kPieces;
+  const int lane = threadIdx.x & 31;
+  const T* t = reinterpret_cast<const T*>(&v);
+  const uint32_t b = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(row)) & 15u;
+  if (b == 0) {  // (col is a multiple of 8)
+    store_row8_aligned(row, col, cols, v);
+    return;
+  }
+  // Shifted by k columns, 8 values start on the boundary: the previous lane's last
+  // k and this lane's first 8 - k.
+  const int32_t k = static_cast<int32_t>(b / sizeof(T));
+  const int32_t start = col - k;
+  uint32_t w[8 * P];
+#pragma unroll
+  for (int j = 0; j < P; ++j) {
+    w[4 * P + 4 * j] = v.w[j].x, w[4 * P + 4 * j + 1] = v.w[j].y;
+    w[4 * P + 4 * j + 2] = v.w[j].z, w[4 * P + 4 * j + 3] = v.w[j].w;
+  }
+#pragma unroll
+  for (int j = 0; j < 4 * P; ++j) w[j] = __shfl_up_sync(0xffffffffu, w[4 * P + j], 1);
+  if constexpr (P == 2) {  // k <= 3 of 8 values: the previous lane's first piece is not needed
+#pragma unroll
+    for (int j = 0; j < 12; ++j) w[j] = w[j + 4];
+  }
+  shift_down(w, 16u - b);
+  if (lane > 0 && start + 8 <= cols) {
+    Raw8<T> r;
+#pragma unroll
+    for (int j = 0; j < P; ++j) r.w[j] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+    store8(row + start, r);
+  } else {
+    const T* s = reinterpret_cast<const T*>(w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int32_t c = start + i;
+      if (c < cols && (lane > 0 || c >= col)) row[c] = s[i];
+    }
+  }
+  if (lane == 31) {  // its last k values have no next lane
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int32_t c = col + i;
+      if (c >= start + 8 && c < cols) row[c] = t[i];
+    }
+  }
+}
+
+// ... of a runtime type (0 bf16, 1 f16, 4 f32: gge_dtype), at element `at` of
+// `base`; AL: the rows start on 16-byte boundaries.
+template <bool AL, typename T>
+__device__ __forceinline__ void store_row8_t(void* base, int64_t at, int32_t col, int32_t cols,
+                                             const float2 (&v)[4]) {
+  T* row = static_cast<T*>(base) + at;
+  if constexpr (AL) store_row8_aligned(row, col, cols, narrow<T>(v));
+  else store_row8(row, col, cols, narrow<T>(v));
+}
+template <bool AL>
+__device__ __forceinline__ void store_row8_any(void* base, int64_t at, int32_t dtype, int32_t col,
+                                               int32_t cols, const float2 (&v)[4]) {
+  if (dtype == 0) store_row8_t<AL, __nv_bfloat16>(base, at, col, cols, v);
+  else if (dtype == 1) store_row8_t<AL, __half>(base, at, col, cols, v);
+  else store_row8_t<AL, float>(base, at, col, cols, v);
+}
+
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+
+}  // namespace lowp
+}  // namespace gge
