@@ -111,16 +111,14 @@ struct MxPlan {
   mx::MxMaps maps;
   LaunchShape shape;
   int tile;
-  int bn, cg;
-  int64_t tiles;
-  int units;
   bool empty;
 };
 
-int tile_units(int32_t format, int tile, size_t smem) {
-  struct Entry { int dev, format, tile; size_t smem; int units; };
+// Resident CTAs (cluster 1) or clusters, cached.
+int tile_units(int32_t format, int tile, size_t smem, int cluster) {
+  struct Entry { int dev, format, tile, cluster; size_t smem; int units; };
   static std::mutex mu;
-  static Entry cache[64];
+  static Entry cache[256];
   static int n = 0;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return -1;
@@ -128,25 +126,69 @@ int tile_units(int32_t format, int tile, size_t smem) {
     std::lock_guard<std::mutex> g(mu);
     for (int i = 0; i < n; ++i)
       if (cache[i].dev == dev && cache[i].format == format && cache[i].tile == tile &&
-          cache[i].smem == smem)
+          cache[i].cluster == cluster && cache[i].smem == smem)
         return cache[i].units;
   }
   int units;
   {
     RelaxedCaptureMode relaxed;  // the first query may run inside a stream capture
-    units = format == GGE_MXFP8   ? mx::mx_units<GGE_MXFP8>(tile, smem)
-            : format == GGE_MXFP4 ? mx::mx_units<GGE_MXFP4>(tile, smem)
-                                  : mx::mx_units<GGE_NVFP4>(tile, smem);
+    units = format == GGE_MXFP8   ? mx::mx_units<GGE_MXFP8>(tile, smem, cluster)
+            : format == GGE_MXFP4 ? mx::mx_units<GGE_MXFP4>(tile, smem, cluster)
+                                  : mx::mx_units<GGE_NVFP4>(tile, smem, cluster);
   }
   if (units > 0) {
     std::lock_guard<std::mutex> g(mu);
-    if (n < 64) cache[n++] = Entry{dev, format, tile, smem, units};
+    if (n < 256) cache[n++] = Entry{dev, format, tile, cluster, smem, units};
   }
   return units;
 }
 
 constexpr int kFlagsTaken = FLAG_TEST_DROP_ACC_FULL | FLAG_DIRECT_STORES | FLAG_NO_SPLIT | FLAG_RASTER_N;
-constexpr int64_t kTicketsATile = 8 * 4;  // epilogue warps x chunks, a CTA
+
+// One way to run a product: tile shape, CTAs that share a tile's K, shared memory.
+struct MxShape {
+  int tile, bn, cg, splits, stages, stage_bytes, reduce_bytes, units;
+  size_t smem;
+  int64_t tiles_m, tiles_n, tiles;
+};
+
+// The shape `bn` (see gge_gemm_mx_args) with K over `splits` CTAs; false if it does not
+// fit or its clusters would not all run at once.
+bool mx_shape(int32_t format, int64_t M, int64_t N, int64_t L, int64_t k_tiles, int bn, int splits,
+              int out_stage, int max_stages, int sms, MxShape* s) {
+  s->bn = bn;
+  s->cg = bn == 256 ? 2 : 1;
+  s->tile = bn == 256 ? mx::TILE_PAIR_256 : (bn == 128 ? mx::TILE_128 : mx::TILE_SWAP_64);
+  s->splits = splits;
+  const int64_t rows = bn == 64 ? N : M, cols = bn == 64 ? M : N;  // (64: A and B exchanged)
+  s->tiles_m = ceil_div(rows, 128 * s->cg);
+  s->tiles_n = ceil_div(cols, bn);
+  s->tiles = s->tiles_m * s->tiles_n * L;
+  if (splits > 1 && (s->cg == 2 || splits > k_tiles || s->tiles * splits > sms)) return false;
+  const int groups = 128 * 8 / mx_bits(format) / (4 * mx_block(format));
+  // codes and scales of a stage, in whole KiB (MxCfg::kStageBytes)
+  s->stage_bytes = (128 * 128 + bn / s->cg * 128 + 512 * groups * (1 + (bn + 127) / 128) + 1023) / 1024 * 1024;
+  // the chunks (32 x 32 fp32) that the other CTAs hand over
+  s->reduce_bytes = splits > 1 ? (splits - 1) * (4 * (bn / 32) / splits) * 4096 : 0;
+  const int fixed = 1024 + kCtrlBytesHost + kEpiWarpsHost * out_stage + s->reduce_bytes;
+  s->stages = std::min(max_stages, (kMaxSmemOptin - fixed) / s->stage_bytes);
+  if (s->stages < 2) return false;
+  s->smem = static_cast<size_t>(fixed + s->stages * s->stage_bytes);
+  s->units = tile_units(format, s->tile, s->smem, s->cg * splits);
+  if (s->units <= 0) return false;
+  return splits == 1 || s->tiles <= s->units;
+}
+
+// Estimated time (ns) of a shape: rounds of tiles, each its k-tiles and an epilogue.
+// Measured a k-tile (nvfp4, mxfp8): 290 / 240 ns for 128 x 64, 430 / 280 for 128 x 128
+// and 400 / 340 for 256 x 256 on a pair, which is twice the work a CTA.
+double mx_cost(const MxShape& s, int64_t k_tiles) {
+  const double per_k = s.bn == 64 ? 260.0 : (s.bn == 128 ? 360.0 : 380.0);
+  const double tail = s.bn == 64 ? 500.0 : (s.bn == 128 ? 900.0 : 1800.0);
+  const int64_t rounds = s.splits > 1 ? 1 : ceil_div(s.tiles, s.units);
+  return static_cast<double>(rounds) * (static_cast<double>(ceil_div(k_tiles, s.splits)) * per_k + tail) +
+         (s.splits > 1 ? 1200.0 : 0.0);
+}
 
 gge_status plan_mx(const gge_gemm_mx_args* a, void* ws, size_t ws_bytes, MxPlan* out) {
   if (a == nullptr) return GGE_ERR_INVALID_ARG;
@@ -180,50 +222,59 @@ gge_status plan_mx(const gge_gemm_mx_args* a, void* ws, size_t ws_bytes, MxPlan*
   pl.empty = M == 0 || N == 0;
   if (pl.empty) return GGE_OK;
 
-  // tile shape
-  const int sms = sm_count();
-  if (sms <= 0) return GGE_ERR_CUDA;
-  int bn = cfg ? cfg->tile_n : 0;
-  if (bn == 0) {
-    const int64_t pair_tiles = ceil_div(M, 256) * ceil_div(N, 256) * L;
-    bn = M <= 64 ? 64 : (2 * pair_tiles >= sms ? 256 : 128);
-  }
-  if (bn != 256 && bn != 128 && bn != 64) return GGE_ERR_UNSUPPORTED;
-  const bool swap = bn == 64;
-  pl.tile = bn == 256 ? mx::TILE_PAIR_256 : (bn == 128 ? mx::TILE_128 : mx::TILE_SWAP_64);
-  pl.bn = bn;
-  pl.cg = bn == 256 ? 2 : 1;
-  const gge_mx_tensor& ka = swap ? a->B : a->A;  // the kernel's A and B
-  const gge_mx_tensor& kb = swap ? a->A : a->B;
-  const int64_t kM = ka.rows, kN = kb.rows;
-  const int tile_m = 128 * pl.cg;
-  const int64_t tiles_m = ceil_div(kM, tile_m), tiles_n = ceil_div(kN, bn);
-  pl.tiles = tiles_m * tiles_n * L;
-  if (pl.tiles > kMaxExtent / 8) return GGE_ERR_UNSUPPORTED;
-
-  const int bk = 128 * 8 / mx_bits(format);
-  const int groups = bk / (4 * mx_block(format));
-  const int b_tiles = static_cast<int>(ceil_div(bn, 128));
-  // (codes and scales of a stage, in whole KiB: MxCfg::kStageBytes)
-  const int stage = (128 * 128 + bn / pl.cg * 128 + 512 * groups * (1 + b_tiles) + 1023) / 1024 * 1024;
   const int out_es = std::max(a->D ? elem_bytes(a->D->dtype) : 0,
                               a->PostAct ? elem_bytes(a->PostAct->dtype) : 0);
   p.out_stage_bytes = cfg && (cfg->flags & FLAG_DIRECT_STORES) ? 0 : 32 * 32 * out_es;
-  const int fixed = 1024 + kCtrlBytesHost + kEpiWarpsHost * p.out_stage_bytes;
-  int stages = std::min(8, (kMaxSmemOptin - fixed) / stage);
-  if (cfg && cfg->stages > 0) stages = std::min(stages, cfg->stages);
-  if (stages < 2) return GGE_ERR_UNSUPPORTED;
-  pl.shape.smem = static_cast<size_t>(fixed + stages * stage);
-  pl.shape.cluster = pl.cg;
+  const int bk = 128 * 8 / mx_bits(format);
+  const int64_t k_tiles = ceil_div(K, bk);
+  const int want = cfg ? cfg->tile_n : 0;
+  if (want != 0 && want != 256 && want != 128 && want != 64) return GGE_ERR_UNSUPPORTED;
+  const int max_stages = cfg && cfg->stages > 0 ? std::min(8, static_cast<int>(cfg->stages)) : 8;
+  if (max_stages < 2) return GGE_ERR_UNSUPPORTED;
+  const int sms = sm_count();
+  if (sms <= 0) return GGE_ERR_CUDA;
+  MxShape sh{};
+  double best = -1.0;
+  for (int bn : {256, 128, 64}) {
+    if (want != 0 && bn != want) continue;
+    for (int splits = 1; splits <= 8; splits *= 2) {
+      if (splits > 1 && cfg && ((cfg->flags & FLAG_NO_SPLIT) || cfg->num_ctas > 0)) break;
+      MxShape one;
+      if (!mx_shape(format, M, N, L, k_tiles, bn, splits, p.out_stage_bytes, max_stages, sms, &one)) {
+        if (splits == 1) break;
+        continue;
+      }
+      const double cost = mx_cost(one, k_tiles);
+      if (best < 0.0 || cost < best) {
+        best = cost;
+        sh = one;
+      }
+    }
+  }
+  if (best < 0.0) return GGE_ERR_CUDA;  // (every shape fits; the device could not be asked)
+  const int bn = sh.bn;
+  const bool swap = bn == 64;
+  pl.tile = sh.tile;
+  const gge_mx_tensor& ka = swap ? a->B : a->A;  // the kernel's A and B
+  const gge_mx_tensor& kb = swap ? a->A : a->B;
+  const int64_t kM = ka.rows, kN = kb.rows;
+  const int tile_m = 128 * sh.cg;
+  if (sh.tiles > kMaxExtent / 8) return GGE_ERR_UNSUPPORTED;
+  const int groups = bk / (4 * mx_block(format));
+  const int b_tiles = static_cast<int>(ceil_div(bn, 128));
+  pl.shape.smem = sh.smem;
+  pl.shape.cluster = sh.cg * sh.splits;
+  pl.mp.splits = sh.splits;
+  pl.mp.reduce_bytes = sh.reduce_bytes;
 
   p.M = static_cast<int32_t>(kM);
   p.N = static_cast<int32_t>(kN);
   p.K = static_cast<int32_t>(K);
   p.L = static_cast<int32_t>(L);
   p.bk = bk;
-  p.k_tiles = static_cast<int32_t>(ceil_div(K, bk));
-  p.stages = stages;
-  p.tiles_n = static_cast<int32_t>(tiles_n);
+  p.k_tiles = static_cast<int32_t>(k_tiles);
+  p.stages = sh.stages;
+  p.tiles_n = static_cast<int32_t>(sh.tiles_n);
   if (a->D) {
     p.d = a->D->ptr; p.ldd = a->D->stride_row; p.sbd = a->D->stride_batch; p.d_dtype = a->D->dtype;
   }
@@ -252,37 +303,15 @@ gge_status plan_mx(const gge_gemm_mx_args* a, void* ws, size_t ws_bytes, MxPlan*
   pl.mp.tscale_a = ka.tensor_scale;
   pl.mp.tscale_b = kb.tensor_scale;
 
-  pl.units = tile_units(format, pl.tile, pl.shape.smem);
-  if (pl.units <= 0) return GGE_ERR_CUDA;
-  if (cfg && cfg->num_ctas > 0) pl.units = std::min(pl.units, std::max(1, cfg->num_ctas / pl.cg));
+  int units = sh.units;
+  if (cfg && cfg->num_ctas > 0) units = std::min(units, std::max(1, cfg->num_ctas / sh.cg));
   const bool along_n = (p.flags & FLAG_RASTER_N) != 0;
   const int band = cfg && cfg->raster_band > 0 ? cfg->raster_band
-                                               : auto_band(pl.units, tile_m, bn, along_n);
-  p.sched = PlainSchedule::create(static_cast<int32_t>(tiles_m), static_cast<int32_t>(tiles_n),
+                                               : auto_band(units, tile_m, bn, along_n);
+  p.sched = PlainSchedule::create(static_cast<int32_t>(sh.tiles_m), static_cast<int32_t>(sh.tiles_n),
                                   static_cast<int32_t>(L), band, along_n);
-  p.num_tiles = static_cast<int32_t>(pl.tiles);
-  // split the last wave along K, as far as the workspace holds the partial sums
-  if (K > 0 && !(p.flags & FLAG_NO_SPLIT) && ws != nullptr &&
-      (reinterpret_cast<uintptr_t>(ws) & 255u) == 0) {
-    TailSplit ts = plan_tail_split(pl.tiles, pl.units, p.k_tiles);
-    // only where the tiles leave units idle from the start: behind full waves the
-    // partial sums' traffic costs more than the shorter last wave saves (8192^3 nvfp4
-    // 178 us split, 172 us whole; 4096^3 mxfp8 55 and 47 us)
-    if (ts.full > 0) ts.tail = 0;
-    const int64_t blocks = static_cast<int64_t>(ts.tail) * ts.splits * pl.cg;
-    const size_t need = kTailBase + static_cast<size_t>(blocks) * 128 * bn * sizeof(float);
-    if (ts.tail > 0 && need <= ws_bytes &&
-        static_cast<size_t>(ts.tail) * pl.cg * kTicketsATile * 4 <= kTicketBytes) {
-      p.full_tiles = ts.full;
-      p.tail_tiles = ts.tail;
-      p.tail_splits = ts.splits;
-      p.num_tiles = ts.full + ts.tail * ts.splits;
-      uint8_t* base = static_cast<uint8_t*>(ws);
-      p.tail_tickets = reinterpret_cast<int32_t*>(base + kWorkspaceBytes);
-      p.partials = reinterpret_cast<float*>(base + kTailBase);
-    }
-  }
-  pl.shape.grid = pl.cg * static_cast<int>(std::min<int64_t>(p.num_tiles, pl.units));
+  p.num_tiles = static_cast<int32_t>(sh.tiles);
+  pl.shape.grid = pl.shape.cluster * static_cast<int>(std::min<int64_t>(sh.tiles, units));
   if (K == 0) return GGE_OK;  // nothing is loaded
 
   const auto codes_map = [&](CUtensorMap* m, const gge_mx_tensor& q, uint32_t box_rows) {
@@ -304,7 +333,7 @@ gge_status plan_mx(const gge_gemm_mx_args* a, void* ws, size_t ws_bytes, MxPlan*
                      false);
   };
   s = codes_map(&pl.maps.a, ka, 128);
-  if (s == GGE_OK) s = codes_map(&pl.maps.b, kb, static_cast<uint32_t>(bn / pl.cg));
+  if (s == GGE_OK) s = codes_map(&pl.maps.b, kb, static_cast<uint32_t>(bn / sh.cg));
   if (s == GGE_OK) s = scales_map(&pl.maps.sa, ka, 1, &pl.mp.sfa_batch);
   if (s == GGE_OK) s = scales_map(&pl.maps.sb, kb, static_cast<uint32_t>(b_tiles), &pl.mp.sfb_batch);
   return s;

@@ -7,8 +7,17 @@
 // K.  tcgen05.mma.block_scale multiplies codes and scales inside the tensor
 // core and accumulates in fp32, so no value is ever widened in a register.
 //
-// Roles, tile schedule, split K, epilogue and bounded waits are those of
-// gemm_kernel (gge_kernel.cuh).  What differs:
+// Roles, tile schedule, epilogue and bounded waits are those of gemm_kernel
+// (gge_kernel.cuh).  What differs:
+//   * one thread walks the producer's loop and one the MMA warp's, so a stage
+//     costs no warp votes: with 64 rows a stage's MMAs take less time than the
+//     issuing loop (16 x 8192 x 8192 nvfp4: 13.8 -> 12.4 us);
+//   * few tiles are split along K over a cluster of 2 to 8 CTAs (mx_reduce): each
+//     contracts a share of K into its own TMEM and hands the accumulator chunks it
+//     does not own to their owner's shared memory; after one cluster barrier the
+//     owners add them in rank order and run the epilogue.  (Partial sums through
+//     global memory and tickets, as gemm_kernel's split last wave has them, cost
+//     about 5 us here, more than the split saved.)
 //   * a stage also holds the scale tiles of its k-tile (512 bytes for 128 rows x
 //     4 blocks), brought by TMA like the codes;
 //   * before a stage's MMAs the issuing lane copies those tiles into TMEM
@@ -104,23 +113,23 @@ __device__ __forceinline__ uint64_t scale_desc(uint32_t addr) {
          (uint64_t(128 >> 4) << 32) | (uint64_t(1) << 46);
 }
 
-// k-tiles [k0, k1) of work item t: all, or one slice of a split tile.
+// This CTA's k-tiles [k0, k1): all of them, or its share in a cluster split along K.
 struct KSpan {
   int32_t k0, k1;
 };
-__device__ __forceinline__ KSpan k_span(const Params& p, int32_t t) {
-  if (p.tail_tiles > 0 && t >= p.full_tiles) {
-    const int32_t sl = (t - p.full_tiles) % p.tail_splits;
-    return KSpan{static_cast<int32_t>(static_cast<int64_t>(sl) * p.k_tiles / p.tail_splits),
-                 static_cast<int32_t>(static_cast<int64_t>(sl + 1) * p.k_tiles / p.tail_splits)};
-  }
-  return KSpan{0, p.k_tiles};
+__device__ __forceinline__ KSpan k_span(const MxParams& mp, uint32_t slice) {
+  const int64_t k = mp.p.k_tiles;
+  return KSpan{static_cast<int32_t>(slice * k / mp.splits),
+               static_cast<int32_t>((slice + 1) * k / mp.splits)};
 }
 
+// Run by one thread.
 template <int BN, int CG, int FMT>
-__device__ __forceinline__ void mx_mma_role(const Params& p, const Shared& sh, uint32_t stage0,
-                                            uint32_t tmem_base, int32_t unit, int32_t units) {
+__device__ __forceinline__ void mx_mma_role(const MxParams& mp, const Shared& sh, uint32_t stage0,
+                                            uint32_t tmem_base, const KSpan& ks, int32_t unit,
+                                            int32_t units) {
   using Cfg = MxCfg<BN, CG, FMT>;
+  const Params& p = mp.p;
   int stage = 0;
   uint32_t phase = 0;
   const uint32_t sfa_t = tmem_base + Cfg::kSfBase;
@@ -128,113 +137,193 @@ __device__ __forceinline__ void mx_mma_role(const Params& p, const Shared& sh, u
   int i = 0;
   for (int32_t t = unit; t < p.num_tiles; t += units, ++i) {
     // the shared columns of the tile before (and all of the one before that) are read
-    bool ok = true;
-    if (i > 0) ok = wait_phase<CG == 2>(sh.tempty, static_cast<uint32_t>(i - 1) & 1u, p, sh, 2, t);
-    if (!__all_sync(0xffffffffu, ok)) return;
+    if (i > 0 && !wait_phase<CG == 2>(sh.tempty, static_cast<uint32_t>(i - 1) & 1u, p, sh, 2, t)) return;
     ptx::tc_fence_after();
     const uint32_t acc = static_cast<uint32_t>(i) & 1u;
     const uint32_t d_tmem = tmem_base + acc * Cfg::kAcc1;
-    const KSpan ks = k_span(p, t);
     // 64-wide tiles: an odd one starts in the middle of a 128-row scale tile
     uint32_t sfb = sfb_t;
     if constexpr (BN == 64) sfb += (tile_coord<BN, Cfg::kTileM>(t, p, sh).n0 & 64) ? 2u : 0u;
     for (int32_t kt = ks.k0; kt < ks.k1; ++kt) {
-      ok = wait_phase<CG == 2>(sh.full + 8 * stage, phase, p, sh, 1, t);
-      if (!__all_sync(0xffffffffu, ok)) return;
+      if (!wait_phase<CG == 2>(sh.full + 8 * stage, phase, p, sh, 1, t)) return;
       ptx::tc_fence_after();
       const uint32_t a_addr = stage0 + stage * Cfg::kStageBytes;
       const uint32_t b_addr = a_addr + Cfg::kABytes;
       const uint32_t sfa_addr = b_addr + Cfg::kBBytes;
       const uint32_t sfb_addr = sfa_addr + Cfg::kSfaBytes;
       const int32_t nk = min(4, (p.K - kt * Cfg::kBK + Cfg::kStep - 1) / Cfg::kStep);
-      if (ptx::elect_one()) {
+      // scale words are copied just before the first MMA that uses them, so that the
+      // copies run under the MMA before (8192^3 nvfp4: 167 -> 164 us)
+      constexpr int kPerGroup = 4 / Cfg::kGroups;  // MMAs that share a scale word
 #pragma unroll
-        for (int g = 0; g < Cfg::kGroups; ++g) {
+      for (int kk = 0; kk < 4; ++kk) {
+        if (kk >= nk) break;
+        const int g = kk / kPerGroup;
+        if (kk % kPerGroup == 0) {
           ptxmx::copy_scales<CG>(sfa_t + 4 * g, scale_desc(sfa_addr + g * 512));
 #pragma unroll
           for (int j = 0; j < Cfg::kBTiles; ++j)
             ptxmx::copy_scales<CG>(sfb_t + 4 * (g * Cfg::kBTiles + j),
                                    scale_desc(sfb_addr + (j * Cfg::kGroups + g) * 512));
         }
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk) {
-          if (kk >= nk) break;
-          const uint64_t adesc = smem_desc(a_addr + kk * 32u, 16u, 1024u);
-          const uint64_t bdesc = smem_desc(b_addr + kk * 32u, 16u, 1024u);
-          // which of a scale word's bytes this MMA's blocks use
-          constexpr int kPerGroup = 4 / Cfg::kGroups;  // MMAs that share a scale word
-          const int g = kk / kPerGroup;
-          const uint32_t id = static_cast<uint32_t>(kk % kPerGroup) * (4 / kPerGroup);
-          const uint32_t idesc = p.idesc | (id << 4) | (id << 29);
-          ptxmx::mma<FMT, CG>(d_tmem, adesc, bdesc, idesc, sfa_t + 4 * g,
-                              sfb + 4 * Cfg::kBTiles * g, (kt > ks.k0 || kk > 0) ? 1u : 0u);
-        }
-        if (CG == 1) ptx::mma_commit(sh.empty + 8 * stage);
-        else ptx::mma_commit_pair(sh.empty + 8 * stage, 0x3);
+        const uint64_t adesc = smem_desc(a_addr + kk * 32u, 16u, 1024u);
+        const uint64_t bdesc = smem_desc(b_addr + kk * 32u, 16u, 1024u);
+        // which of a scale word's bytes this MMA's blocks use
+        const uint32_t id = static_cast<uint32_t>(kk % kPerGroup) * (4 / kPerGroup);
+        const uint32_t idesc = p.idesc | (id << 4) | (id << 29);
+        ptxmx::mma<FMT, CG>(d_tmem, adesc, bdesc, idesc, sfa_t + 4 * g,
+                            sfb + 4 * Cfg::kBTiles * g, (kt > ks.k0 || kk > 0) ? 1u : 0u);
       }
-      __syncwarp();
+      if (CG == 1) ptx::mma_commit(sh.empty + 8 * stage);
+      else ptx::mma_commit_pair(sh.empty + 8 * stage, 0x3);
       if (++stage == p.stages) { stage = 0; phase ^= 1u; }
     }
-    if (!(p.flags & FLAG_TEST_DROP_ACC_FULL) && ptx::elect_one()) {
+    if (!(p.flags & FLAG_TEST_DROP_ACC_FULL)) {
       if (CG == 1) ptx::mma_commit(sh.tfull + 8 * acc);
       else ptx::mma_commit_pair(sh.tfull + 8 * acc, 0x3);
     }
-    __syncwarp();
   }
 }
 
+// Run by one thread.
 template <int BN, int CG, int FMT>
 __device__ __forceinline__ void mx_load_role(const MxParams& mp, const Shared& sh,
                                              const CUtensorMap* tmA, const CUtensorMap* tmB,
                                              const CUtensorMap* tmSA, const CUtensorMap* tmSB,
-                                             uint32_t stage0, uint32_t rank, int32_t unit,
-                                             int32_t units) {
+                                             uint32_t stage0, uint32_t rank, const KSpan& ks,
+                                             int32_t unit, int32_t units) {
   using Cfg = MxCfg<BN, CG, FMT>;
   const Params& p = mp.p;
   int stage = 0;
   uint32_t phase = 0;
   for (int32_t t = unit; t < p.num_tiles; t += units) {
     const TileCoord tc = tile_coord<BN, Cfg::kTileM>(t, p, sh);
-    const KSpan ks = k_span(p, t);
     const int32_t row0 = tc.m_row0 + static_cast<int32_t>(rank) * kBM;
     const int32_t bn0 = tc.n0 + static_cast<int32_t>(rank) * Cfg::kBRows;
     const int32_t sa = tc.a_batch * mp.sfa_batch + (row0 >> 7);
     const int32_t sb = tc.b_batch * mp.sfb_batch + (tc.n0 >> 7);
     for (int32_t kt = ks.k0; kt < ks.k1; ++kt) {
-      const bool ok = wait_phase<CG == 2>(sh.empty + 8 * stage, phase ^ 1u, p, sh, 0, t);
-      if (!__all_sync(0xffffffffu, ok)) return;
-      if (ptx::elect_one()) {
-        const uint32_t full = sh.full + 8 * stage;
-        if (CG == 1) ptx::mbar_arrive_expect_tx(full, Cfg::kLoadBytes);
-        else if (rank == 0) ptx::mbar_arrive_expect_tx(full, 2 * Cfg::kLoadBytes);
-        const uint32_t bar = (CG == 1) ? full : ptx::mapa(full, 0);
-        const uint32_t a_dst = stage0 + stage * Cfg::kStageBytes;
-        const uint32_t b_dst = a_dst + Cfg::kABytes;
-        const uint32_t sfa_dst = b_dst + Cfg::kBBytes;
-        tma_load<CG>(a_dst, tmA, bar, kt * kRowBytes, row0, tc.a_batch);
-        tma_load<CG>(b_dst, tmB, bar, kt * kRowBytes, bn0, tc.b_batch);
-        tma_load<CG>(sfa_dst, tmSA, bar, 0, kt * Cfg::kGroups, sa);
-        tma_load<CG>(sfa_dst + Cfg::kSfaBytes, tmSB, bar, 0, kt * Cfg::kGroups, sb);
-      }
-      __syncwarp();
+      if (!wait_phase<CG == 2>(sh.empty + 8 * stage, phase ^ 1u, p, sh, 0, t)) return;
+      const uint32_t full = sh.full + 8 * stage;
+      if (CG == 1) ptx::mbar_arrive_expect_tx(full, Cfg::kLoadBytes);
+      else if (rank == 0) ptx::mbar_arrive_expect_tx(full, 2 * Cfg::kLoadBytes);
+      const uint32_t bar = (CG == 1) ? full : ptx::mapa(full, 0);
+      const uint32_t a_dst = stage0 + stage * Cfg::kStageBytes;
+      const uint32_t b_dst = a_dst + Cfg::kABytes;
+      const uint32_t sfa_dst = b_dst + Cfg::kBBytes;
+      tma_load<CG>(a_dst, tmA, bar, kt * kRowBytes, row0, tc.a_batch);
+      tma_load<CG>(b_dst, tmB, bar, kt * kRowBytes, bn0, tc.b_batch);
+      tma_load<CG>(sfa_dst, tmSA, bar, 0, kt * Cfg::kGroups, sa);
+      tma_load<CG>(sfa_dst + Cfg::kSfaBytes, tmSB, bar, 0, kt * Cfg::kGroups, sb);
       if (++stage == p.stages) { stage = 0; phase ^= 1u; }
     }
+  }
+}
+
+// A split tile's 32 x 32 accumulator chunks (lane quadrant x 32 columns) are dealt
+// out to the cluster's CTAs in order; chunk `n` of 4 BN / 32 belongs to rank n S /
+// (4 BN / 32).
+template <int BN>
+__device__ __forceinline__ uint32_t chunk_owner(int n, int32_t splits) {
+  return static_cast<uint32_t>(n * splits) / (4 * (BN / 32));
+}
+
+// Where rank `from` leaves chunk n in its owner's shared memory (one float4 a lane
+// and four columns, so each store instruction writes 512 contiguous bytes).
+template <int BN>
+__device__ __forceinline__ uint32_t chunk_slot(uint32_t red, int n, uint32_t owner, uint32_t from,
+                                               int32_t splits) {
+  constexpr int kChunks = 4 * (BN / 32);
+  const int mine = kChunks / splits;  // chunks an owner has (both are powers of two)
+  const uint32_t order = from < owner ? from : from - 1;
+  return red + (order * mine + n % mine) * 4096u + (threadIdx.x & 31) * 16u;
+}
+
+// Hand the chunks of this CTA's accumulator that other ranks own to them.
+template <int BN>
+__device__ __forceinline__ void mx_send(const MxParams& mp, uint32_t tbase, int32_t n0, int quad, int half,
+                                        uint32_t slice, uint32_t red) {
+#pragma unroll 1
+  for (int c = half; c < BN / 32; c += 2) {
+    if (n0 + c * 32 >= mp.p.N) break;  // (no rank computes with these columns)
+    const int n = quad * (BN / 32) + c;
+    const uint32_t owner = chunk_owner<BN>(n, mp.splits);
+    if (owner == slice) continue;
+    uint32_t v[32];
+    __syncwarp();
+    ptx::tmem_ld_32x32b_x32(tbase + c * 32, v);
+    ptx::tmem_wait_ld(v);
+    const uint32_t dst = ptx::mapa(chunk_slot<BN>(red, n, owner, slice, mp.splits), owner);
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+      asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + q * 512u), "r"(v[4 * q]),
+                   "r"(v[4 * q + 1]), "r"(v[4 * q + 2]), "r"(v[4 * q + 3])
+                   : "memory");
+  }
+}
+
+__device__ __forceinline__ float mx_alpha(const MxParams& mp) {
+  float alpha = mp.p.alpha_dev ? *mp.p.alpha_dev : mp.p.alpha;
+  if (mp.tscale_a != nullptr) alpha *= *mp.tscale_a;
+  if (mp.tscale_b != nullptr) alpha *= *mp.tscale_b;
+  return alpha;
+}
+
+// A split tile's owned chunks, after the cluster barrier: the ranks' copies added in
+// rank order, then the epilogue.  One tile a cluster.
+template <int BN, int FMT, bool TR>
+__device__ __forceinline__ void mx_reduce(const MxParams& mp, const Shared& sh, uint32_t tmem_base,
+                                          uint32_t slice, uint32_t red, uint32_t stg, int32_t t) {
+  const Params& p = mp.p;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int quad = warp & 3, half = warp >> 2;
+  const TileCoord tc = tile_coord<BN, kBM>(t, p, sh);
+  const int32_t row_base = tc.m_row0 + quad * 32;
+  const int32_t rows_valid = min(32, tc.row_limit - row_base);
+  const float alpha = mx_alpha(mp);
+  const float beta = p.beta_dev ? *p.beta_dev : p.beta;
+  const uint32_t tbase = tmem_base + (static_cast<uint32_t>(quad * 32) << 16);
+#pragma unroll 1
+  for (int c = half; c < BN / 32; c += 2) {
+    const int32_t col0 = tc.n0 + c * 32;
+    const int n = quad * (BN / 32) + c;
+    if (col0 >= p.N || rows_valid <= 0 || chunk_owner<BN>(n, mp.splits) != slice) continue;
+    CRegs creg = {};
+    if (p.c != nullptr && lane < rows_valid) load_c_chunk<TR>(p, row_base + lane, col0, tc.batch, creg);
+    uint32_t own[32];
+    __syncwarp();
+    ptx::tmem_ld_32x32b_x32(tbase + c * 32, own);
+    ptx::tmem_wait_ld(own);
+    float sum[32];
+    for (int32_t r = 0; r < mp.splits; ++r) {
+      const uint32_t src = chunk_slot<BN>(red, n, slice, static_cast<uint32_t>(r), mp.splits);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        uint4 v = make_uint4(own[4 * q], own[4 * q + 1], own[4 * q + 2], own[4 * q + 3]);
+        if (r != static_cast<int32_t>(slice)) v = ptx::ld_shared_v4(src + q * 512u);
+        const float f[4] = {__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w)};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sum[4 * q + j] = r == 0 ? f[j] : sum[4 * q + j] + f[j];
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 32; ++j) own[j] = __float_as_uint(sum[j]);
+    epilogue_chunk_t<TR>(p, own, row_base, rows_valid, col0, tc.batch, alpha, beta, creg, stg);
   }
 }
 
 template <int BN, int CG, int FMT, bool TR>
 __device__ __forceinline__ void mx_epilogue_role(const MxParams& mp, const Shared& sh,
                                                  uint32_t tmem_base, uint32_t rank, uint32_t stg,
-                                                 int32_t unit, int32_t units) {
+                                                 int32_t unit, int32_t units, uint32_t slice,
+                                                 uint32_t red) {
   using Cfg = MxCfg<BN, CG, FMT>;
   const Params& p = mp.p;
   constexpr int kMine = BN / 64;  // 32-column chunks of this warp (two warps a lane quadrant)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int quad = warp & 3, half = warp >> 2;
-  float alpha = p.alpha_dev ? *p.alpha_dev : p.alpha;
+  const float alpha = mx_alpha(mp);
   const float beta = p.beta_dev ? *p.beta_dev : p.beta;
-  if (mp.tscale_a != nullptr) alpha *= *mp.tscale_a;
-  if (mp.tscale_b != nullptr) alpha *= *mp.tscale_b;
   const bool lean = !TR && p.c == nullptr && p.post == nullptr && p.out_stage_bytes != 0 &&
                     p.d_dtype != DT_F32;
   int i = 0;
@@ -242,12 +331,6 @@ __device__ __forceinline__ void mx_epilogue_role(const MxParams& mp, const Share
     const TileCoord tc = tile_coord<BN, Cfg::kTileM>(t, p, sh);
     const uint32_t acc = static_cast<uint32_t>(i) & 1u;
     const uint32_t acc_phase = static_cast<uint32_t>(i >> 1) & 1u;
-    const bool split = p.tail_tiles > 0 && t >= p.full_tiles;
-    int32_t slice = 0, tail_r = 0;
-    if (split) {
-      tail_r = (t - p.full_tiles) / p.tail_splits;
-      slice = t - p.full_tiles - tail_r * p.tail_splits;
-    }
     const int32_t row_base = tc.m_row0 + static_cast<int32_t>(rank) * kBM + quad * 32;
     const int32_t rows_valid = min(32, tc.row_limit - row_base);
     const int32_t row = row_base + lane;
@@ -257,19 +340,24 @@ __device__ __forceinline__ void mx_epilogue_role(const MxParams& mp, const Share
     // tile's slices then rotate on, so that they finish different chunks last.
     const int first = (BN == 256 && acc == 0) ? kMine - 1 : 0;
     CRegs cnext = {};
-    if (!split && has_c && tc.n0 + (half + 2 * first) * 32 < p.N)
+    if (mp.splits == 1 && has_c && tc.n0 + (half + 2 * first) * 32 < p.N)
       load_c_chunk<TR>(p, row, tc.n0 + (half + 2 * first) * 32, tc.batch, cnext);
-    const bool ok = wait_phase<CG == 2, true>(sh.tfull + 8 * acc, acc_phase, p, sh, 3, t);
+    // (polled: the next tile's MMAs wait for this one's first chunks)
+    const bool ok = wait_phase<CG == 2>(sh.tfull + 8 * acc, acc_phase, p, sh, 3, t);
     if (!__all_sync(0xffffffffu, ok)) return;
     ptx::tc_fence_after();
     const uint32_t tbase = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + acc * Cfg::kAcc1;
+    if (CG == 1 && mp.splits > 1) {  // (one tile a cluster: mx_reduce finishes it)
+      mx_send<BN>(mp, tbase, tc.n0, quad, half, slice, red);
+      return;
+    }
 #pragma unroll 1
     for (int n = 0; n < kMine; ++n) {
       const int ci = (n + first) % kMine;
       const int c = half + 2 * ci;
       const int32_t col0 = tc.n0 + c * 32;
       const CRegs ccur = cnext;
-      if (!split && has_c && n + 1 < kMine) {
+      if (has_c && n + 1 < kMine) {
         const int32_t next = tc.n0 + (half + 2 * ((ci + 1) % kMine)) * 32;
         if (next < p.N) load_c_chunk<TR>(p, row, next, tc.batch, cnext);
       }
@@ -291,19 +379,6 @@ __device__ __forceinline__ void mx_epilogue_role(const MxParams& mp, const Share
           if (CG == 1) ptx::mbar_arrive(sh.tempty);
           else ptx::mbar_arrive_remote(ptx::mapa(sh.tempty, 0));
         }
-      }
-      if (split) {
-        tail_store(tail_chunk<BN, false, CG>(p, tail_r, slice, rank, quad, c, lane), v);
-        int32_t* ticket = p.tail_tickets +
-                          ((static_cast<int64_t>(tail_r) * CG + rank) * Cfg::kEpiWarps + warp) *
-                              kTicketsPerWarp + ci;
-        if (tail_ticket(ticket, p.tail_splits)) {
-          if (has_c && col0 < p.N) load_c_chunk<TR>(p, row, col0, tc.batch, cnext);
-          tail_sum<BN, false, CG>(p, tail_r, rank, quad, c, lane, v);
-          if (rows_valid > 0 && col0 < p.N)
-            epilogue_chunk_t<TR>(p, v, row_base, rows_valid, col0, tc.batch, alpha, beta, cnext, stg);
-        }
-        continue;
       }
       if (rows_valid > 0 && col0 < p.N) {
         if (lean) {
@@ -335,7 +410,9 @@ __global__ void __launch_bounds__(MxCfg<BN, CG, FMT>::kThreads, 1)
   uint8_t* base_ptr = smem_raw + (base - raw);
   const int S = p.stages;
   const uint32_t out_stage = base + S * Cfg::kStageBytes;
-  uint8_t* ctrl = base_ptr + S * Cfg::kStageBytes + Cfg::kEpiWarps * p.out_stage_bytes;
+  // split K: the other ranks' chunks of what this CTA owns
+  const uint32_t red = out_stage + Cfg::kEpiWarps * p.out_stage_bytes;
+  uint8_t* ctrl = base_ptr + S * Cfg::kStageBytes + Cfg::kEpiWarps * p.out_stage_bytes + mp.reduce_bytes;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(ctrl + 8 * (2 * kMaxStages + 4));
   int32_t* abort_flag = reinterpret_cast<int32_t*>(tmem_slot + 1);
 
@@ -348,9 +425,13 @@ __global__ void __launch_bounds__(MxCfg<BN, CG, FMT>::kThreads, 1)
   sh.abort = abort_flag;
 
   const int warp = threadIdx.x >> 5;
-  const uint32_t rank = (CG == 2) ? ptx::cluster_ctarank() : 0u;
-  const int32_t unit = static_cast<int32_t>(blockIdx.x) / CG;
-  const int32_t units = static_cast<int32_t>(gridDim.x) / CG;
+  const uint32_t crank = (CG == 2 || mp.splits > 1) ? ptx::cluster_ctarank() : 0u;
+  const uint32_t rank = (CG == 2) ? crank : 0u;      // in the pair
+  const uint32_t slice = (CG == 2) ? 0u : crank;     // of K
+  const int32_t ctas = CG * mp.splits;               // of the cluster
+  const int32_t unit = static_cast<int32_t>(blockIdx.x) / ctas;
+  const int32_t units = static_cast<int32_t>(gridDim.x) / ctas;
+  const KSpan ks = k_span(mp, slice);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
@@ -382,18 +463,20 @@ __global__ void __launch_bounds__(MxCfg<BN, CG, FMT>::kThreads, 1)
   }
   ptx::griddep_wait();
   __syncthreads();
-  if (CG == 2) ptx::cluster_sync();
+  if (ctas > 1) ptx::cluster_sync();
   ptx::tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
 
   if (warp < Cfg::kEpiWarps) {
     mx_epilogue_role<BN, CG, FMT, TR>(mp, sh, tmem_base, rank, out_stage + warp * p.out_stage_bytes,
-                                      unit, units);
+                                      unit, units, slice, red);
   } else if (warp == Cfg::kMmaWarp) {
-    if (rank == 0) mx_mma_role<BN, CG, FMT>(p, sh, base, tmem_base, unit, units);
+    if (rank == 0 && ptx::elect_one()) mx_mma_role<BN, CG, FMT>(mp, sh, base, tmem_base, ks, unit, units);
   } else {
-    mx_load_role<BN, CG, FMT>(mp, sh, &tmA, &tmB, &tmSA, &tmSB, base, rank, unit, units);
+    if (ptx::elect_one())
+      mx_load_role<BN, CG, FMT>(mp, sh, &tmA, &tmB, &tmSA, &tmSB, base, rank, ks, unit, units);
   }
+  __syncwarp();
 
   __syncthreads();
   // every MMA and scale copy this CTA issued has finished before TMEM is freed
@@ -406,22 +489,17 @@ __global__ void __launch_bounds__(MxCfg<BN, CG, FMT>::kThreads, 1)
     wait_phase<CG == 2>(drain_bar, 0, p, sh, 6, -1);
   }
   __syncthreads();
-  if (CG == 2) ptx::cluster_sync();
+  if (ctas > 1) ptx::cluster_sync();
+  if (CG == 1 && mp.splits > 1 && warp < Cfg::kEpiWarps && !*abort_flag) {
+    ptx::tc_fence_after();
+    mx_reduce<BN, FMT, TR>(mp, sh, tmem_base, slice, red, out_stage + warp * p.out_stage_bytes, unit);
+    ptx::tc_fence_before();
+  }
+  if (CG == 1 && mp.splits > 1) __syncthreads();
   if (*abort_flag) {
     // let copies and MMAs that were in flight land before the memory goes away
     const uint64_t t0 = ptx::globaltimer();
     while (ptx::globaltimer() - t0 < 200000ull) __nanosleep(1000);
-  }
-  // after a device error the last unit to finish clears the split tickets (as in gemm_kernel)
-  if (p.tail_tiles > 0 && rank == 0 && threadIdx.x == 0) {
-    __threadfence();
-    if (atomicAdd(p.status + 7, 1) == units - 1) {
-      atomicExch(p.status + 7, 0);
-      if (atomicAdd(p.status, 0) != 0) {
-        const int32_t n = p.tail_tiles * CG * Cfg::kEpiWarps * kTicketsPerWarp;
-        for (int32_t i = 0; i < n; ++i) atomicExch(p.tail_tickets + i, 0);
-      }
-    }
   }
   if (warp == Cfg::kMmaWarp) {
     __syncwarp();

@@ -26,7 +26,8 @@ cudaError_t mx_smem_limit(size_t smem) {
 }
 
 template <int BN, int CG, int FMT, bool TR>
-cudaLaunchConfig_t mx_config(int grid, size_t smem, cudaStream_t stream, cudaLaunchAttribute* attr) {
+cudaLaunchConfig_t mx_config(int grid, size_t smem, int cluster, cudaStream_t stream,
+                             cudaLaunchAttribute* attr) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid, 1, 1);
   cfg.blockDim = dim3(MxCfg<BN, CG, FMT>::kThreads, 1, 1);
@@ -36,9 +37,9 @@ cudaLaunchConfig_t mx_config(int grid, size_t smem, cudaStream_t stream, cudaLau
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.numAttrs = 1;
-  if (CG == 2) {
+  if (cluster > 1) {
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = CG;
+    attr[1].val.clusterDim.x = cluster;
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     cfg.numAttrs = 2;
@@ -52,14 +53,14 @@ cudaError_t mx_launch_one(const MxMaps& m, const MxParams& mp, const LaunchShape
   const cudaError_t e = mx_smem_limit<BN, CG, FMT, TR>(shape.smem);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[2];
-  const cudaLaunchConfig_t cfg = mx_config<BN, CG, FMT, TR>(shape.grid, shape.smem, stream, attr);
+  const cudaLaunchConfig_t cfg = mx_config<BN, CG, FMT, TR>(shape.grid, shape.smem, shape.cluster, stream, attr);
   return cudaLaunchKernelEx(&cfg, mx_gemm_kernel<BN, CG, FMT, TR>, m.a, m.b, m.sa, m.sb, mp);
 }
 
 template <int BN, int CG, int FMT, bool TR>
-int mx_units_one(size_t smem) {
+int mx_units_one(size_t smem, int cluster) {
   if (mx_smem_limit<BN, CG, FMT, TR>(smem) != cudaSuccess) return -1;
-  if (CG == 1) {
+  if (cluster == 1) {
     int per_sm = 0, dev = 0, sms = 0;
     if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, mx_gemm_kernel<BN, CG, FMT, TR>,
                                                       MxCfg<BN, CG, FMT>::kThreads, smem) != cudaSuccess ||
@@ -69,7 +70,7 @@ int mx_units_one(size_t smem) {
     return per_sm * sms;
   }
   cudaLaunchAttribute attr[2];
-  cudaLaunchConfig_t cfg = mx_config<BN, CG, FMT, TR>(CG * 64, smem, nullptr, attr);
+  cudaLaunchConfig_t cfg = mx_config<BN, CG, FMT, TR>(cluster * 64, smem, cluster, nullptr, attr);
   cfg.attrs = attr + 1;
   cfg.numAttrs = 1;
   int n = 0;
@@ -88,18 +89,18 @@ cudaError_t launch_mx(int tile, const MxMaps& maps, const MxParams& mp, const La
 }
 
 template <int FMT>
-int mx_units(int tile, size_t smem) {
+int mx_units(int tile, size_t smem, int cluster) {
   switch (tile) {
-    case TILE_PAIR_256: return mx_units_one<256, 2, FMT, false>(smem);
-    case TILE_128: return mx_units_one<128, 1, FMT, false>(smem);
-    default: return mx_units_one<64, 1, FMT, true>(smem);
+    case TILE_PAIR_256: return mx_units_one<256, 2, FMT, false>(smem, cluster);
+    case TILE_128: return mx_units_one<128, 1, FMT, false>(smem, cluster);
+    default: return mx_units_one<64, 1, FMT, true>(smem, cluster);
   }
 }
 
 #define GGE_MX_INSTANTIATE(FMT)                                                                    \
   template cudaError_t launch_mx<FMT>(int, const MxMaps&, const MxParams&, const LaunchShape&,   \
                                       cudaStream_t);                                              \
-  template int mx_units<FMT>(int, size_t);
+  template int mx_units<FMT>(int, size_t, int);
 
 }  // namespace mx
 }  // namespace gge

@@ -16,6 +16,8 @@ struct MxParams {
   Params p;
   const float *tscale_a, *tscale_b;  // fp32 scales of the whole operands, or NULL
   int32_t sfa_batch, sfb_batch;      // scale row tiles a batch
+  int32_t splits;                    // CTAs of a cluster that share a tile's K: 1, 2, 4 or 8
+  int32_t reduce_bytes;              // shared memory for the chunks they exchange
 };
 
 struct MxMaps {
@@ -29,9 +31,9 @@ enum MxTile { TILE_PAIR_256 = 0, TILE_128 = 1, TILE_SWAP_64 = 2 };
 template <int FMT>
 cudaError_t launch_mx(int tile, const MxMaps& maps, const MxParams& mp, const LaunchShape& shape,
                       cudaStream_t stream);
-// Resident CTAs (pairs) on the current device, or -1.
+// Resident CTAs, or clusters of `cluster` CTAs, on the current device, or -1.
 template <int FMT>
-int mx_units(int tile, size_t smem);
+int mx_units(int tile, size_t smem, int cluster);
 
 }  // namespace mx
 }  // namespace gge

@@ -88,19 +88,29 @@ struct RowReader {
   __device__ __forceinline__ void init(const void* base, int64_t ld, int64_t row, int32_t col) {
     next = static_cast<const T*>(base) + row * ld + (AL ? col : 0);
   }
-  // copy chunk c (`cols_over` columns after chunk 0) of that row to this warp's `dst`
-  __device__ __forceinline__ void copy(uint32_t dst, int32_t col, int32_t cols_over, int32_t cols,
+  // AL, once a buffer: a lane's pieces past the row's end stay zero
+  static __device__ __forceinline__ void clear(uint32_t dst, int32_t col, int32_t cols) {
+    constexpr int P = WarpRow<T>::kPieces;
+    if constexpr (AL) {
+#pragma unroll
+      for (int j = 0; j < P; ++j)
+        if (col + j * static_cast<int32_t>(16 / sizeof(T)) >= cols)
+          ptx::st_shared_v4(dst + 16u * ((threadIdx.x & 31) * P + j), make_uint4(0u, 0u, 0u, 0u));
+    }
+  }
+  // copy chunk c (`over` columns after chunk 0) of that row to this warp's `dst`
+  __device__ __forceinline__ void copy(uint32_t dst, int32_t col, int32_t over, int32_t cols,
                                        bool first) const {
     constexpr int P = WarpRow<T>::kPieces;
     const int lane = threadIdx.x & 31;
     if constexpr (AL) {
-      const int32_t left = (cols - col) * static_cast<int32_t>(sizeof(T));
 #pragma unroll
       for (int j = 0; j < P; ++j) {
         // (bytes past the row's end are zero-filled; none are read)
-        const int32_t n = min(16, max(0, left - 16 * j));
-        ptx::cp_async_16(dst + 16u * (lane * P + j), n > 0 ? next + cols_over + j * (16 / sizeof(T)) : next,
-                         static_cast<uint32_t>(n));
+        const int32_t left = (cols - col) * static_cast<int32_t>(sizeof(T)) - 16 * j;
+        if (left > 0)
+          ptx::cp_async_16(dst + 16u * (lane * P + j), next + over + j * (16 / sizeof(T)),
+                           static_cast<uint32_t>(min(16, left)));
       }
     } else {
       if (col - lane * 8 < cols) copy_row(dst, next, col - lane * 8, cols, first);
@@ -156,25 +166,29 @@ __global__ void __launch_bounds__(kMaxThreads)
   constexpr uint32_t kBuf = WarpRow<T>::kBytes;
   const uint32_t ring = ptx::smem_addr(ring_raw) + (threadIdx.x >> 5) * (C * 2 * kBuf);
   const uint32_t ring_row = warps * (C * 2 * kBuf);
-  const int64_t step = static_cast<int64_t>(gridDim.x) * per_block;
-  int64_t row = static_cast<int64_t>(blockIdx.x) * per_block + sub;
+  const uint32_t rows = static_cast<uint32_t>(p.rows);  // (below 2^31, and so is a step past them)
+  const uint32_t step = gridDim.x * per_block;
+  uint32_t row = blockIdx.x * per_block + sub;
   const bool has_res = p.residual != nullptr;
   RowReader<T, AL> x, res;
   x.init(p.x, p.ldx, row, t * 8);
   res.init(p.residual, p.ldr, row, t * 8);
   ptx::griddep_wait();
   const float tscale = (FMT == FMT_NVFP4 && p.q.tensor_scale) ? *p.q.tensor_scale : 1.f;
-  int64_t ahead = row;
+#pragma unroll
+  for (int s = 0; s < D * C * 2; ++s)
+    RowReader<T, AL>::clear(ring + s / (C * 2) * ring_row + s % (C * 2) * kBuf, (t + s % (C * 2) / 2 * tpr) * 8, cols);
+  uint32_t ahead = row;
   const auto start = [&](int slot) {
-    if (ahead < p.rows) {
+    if (ahead < rows) {
 #pragma unroll
       for (int c = 0; c < C; ++c) {
         const uint32_t dst = ring + slot * ring_row + c * 2 * kBuf;
         x.copy(dst, (t + c * tpr) * 8, c * tpr * 8, cols, ahead == 0);
         if (has_res) res.copy(dst + kBuf, (t + c * tpr) * 8, c * tpr * 8, cols, ahead == 0);
       }
-      x.next += step * p.ldx;
-      res.next += step * p.ldr;
+      x.next += static_cast<int64_t>(step) * p.ldx;
+      res.next += static_cast<int64_t>(step) * p.ldr;
     }
     ahead += step;
     cp_async_commit();
@@ -183,7 +197,7 @@ __global__ void __launch_bounds__(kMaxThreads)
   for (int s = 0; s + 1 < D; ++s) start(s);
   const float inv_cols = 1.f / static_cast<float>(cols);
   int slot = 0, flip = 0;
-  for (; row < p.rows; row += step) {
+  for (; row < rows; row += step) {
     if constexpr (!AL) __syncwarp();  // (the slot was read in the iteration before)
     start((slot + D - 1) % D);
     cp_async_wait<D - 1>();
@@ -420,8 +434,9 @@ __global__ void __launch_bounds__(kMaxThreads)
   constexpr uint32_t kBuf = WarpRow<T>::kBytes;
   constexpr uint32_t kRow = (kMaxThreads / 32) * C * 3 * kBuf;
   const uint32_t ring = ptx::smem_addr(ring_raw) + (threadIdx.x >> 5) * (C * 3 * kBuf);
-  const int64_t step = static_cast<int64_t>(gridDim.x) * per_block;
-  int64_t row = static_cast<int64_t>(blockIdx.x) * per_block + sub;
+  const uint32_t rows = static_cast<uint32_t>(p.rows);  // (below 2^31, and so is a step past them)
+  const uint32_t step = gridDim.x * per_block;
+  uint32_t row = blockIdx.x * per_block + sub;
   const bool has_dh = p.dh != nullptr;
   RowReader<T, AL> dy, h, dh;
   dy.init(p.dy, p.lddy, row, t * 8);
@@ -435,9 +450,12 @@ __global__ void __launch_bounds__(kMaxThreads)
     for (int i = 0; i < 4; ++i) dw[c][i] = make_float2(0.f, 0.f);
   float2 wk[4];  // one chunk a thread: its weights stay in registers
   if (C == 1) load_weight(p.weight, p.w_dtype, p.w_vec, t * 8, cols, wk);
-  int64_t ahead = row;
+#pragma unroll
+  for (int s = 0; s < D * C * 3; ++s)
+    RowReader<T, AL>::clear(ring + s / (C * 3) * kRow + s % (C * 3) * kBuf, (t + s % (C * 3) / 3 * tpr) * 8, cols);
+  uint32_t ahead = row;
   const auto start = [&](int slot) {
-    if (ahead < p.rows) {
+    if (ahead < rows) {
 #pragma unroll
       for (int c = 0; c < C; ++c) {
         const uint32_t dst = ring + slot * kRow + c * 3 * kBuf;
@@ -446,9 +464,9 @@ __global__ void __launch_bounds__(kMaxThreads)
         h.copy(dst + kBuf, col, over, cols, ahead == 0);
         if (has_dh) dh.copy(dst + 2 * kBuf, col, over, cols, ahead == 0);
       }
-      dy.next += step * p.lddy;
-      h.next += step * p.ldh;
-      dh.next += step * p.lddh;
+      dy.next += static_cast<int64_t>(step) * p.lddy;
+      h.next += static_cast<int64_t>(step) * p.ldh;
+      dh.next += static_cast<int64_t>(step) * p.lddh;
     }
     ahead += step;
     cp_async_commit();
@@ -457,7 +475,7 @@ __global__ void __launch_bounds__(kMaxThreads)
   for (int s = 0; s + 1 < D; ++s) start(s);
   const float inv_cols = 1.f / static_cast<float>(cols);
   int slot = 0, flip = 0;
-  for (; row < p.rows; row += step) {
+  for (; row < rows; row += step) {
     if constexpr (!AL) __syncwarp();
     start((slot + D - 1) % D);
     const float inv = p.inv[row];

@@ -160,7 +160,7 @@ __device__ __forceinline__ void quantise32(float (&v)[32], float tscale, int32_t
 }
 
 template <typename T, int FMT, bool AL>
-__global__ void __launch_bounds__(256) quantize_cols_kernel(const __grid_constant__ QuantParams p) {
+__global__ void __launch_bounds__(256, 4) quantize_cols_kernel(const __grid_constant__ QuantParams p) {
   constexpr int V = 4 / sizeof(T);         // rows a word holds
   constexpr int kRows = kTWords * V;       // rows of the tile
   constexpr int kBytes = kTCols / Fmt<FMT>::kBlock;  // scale bytes of a row of the tile
@@ -203,19 +203,17 @@ __global__ void __launch_bounds__(256) quantize_cols_kernel(const __grid_constan
   const int part = threadIdx.x / kTWords, at = threadIdx.x % kTWords;  // 32 columns a part
   const int32_t col = col0 + part * 32;
   uint32_t* mine = tile + part * 32 * kTPitch + at;
-  uint32_t pair[32];
-#pragma unroll
-  for (int i = 0; i < 32; ++i) pair[i] = mine[i * kTPitch];
-  // values of a 16-bit type, or of a source of 32 bits, go out through the tile
+  // values of a 16-bit type, or of a source of 32 bits, go out through the tile, in the
+  // place of the source's (each half of a word by the pass that read it)
   const bool staged = q.values != nullptr && (V == 1 || q.v_dtype != 4);
-#pragma unroll
+#pragma unroll 1
   for (int h = 0; h < V; ++h) {
     const int64_t row = row0 + at * V + h;
     float v[32];
 #pragma unroll
     for (int i = 0; i < 32; ++i) {
-      if constexpr (V == 1) v[i] = __uint_as_float(pair[i]);
-      else v[i] = h == 0 ? widen_pair<T>(pair[i]).x : widen_pair<T>(pair[i]).y;
+      if constexpr (V == 1) v[i] = __uint_as_float(mine[i * kTPitch]);
+      else v[i] = to_float<T>(reinterpret_cast<const T*>(mine + i * kTPitch)[h]);
     }
     uint32_t w[8];
     quantise32<FMT>(v, tscale, col, cols, w,
@@ -229,23 +227,15 @@ __global__ void __launch_bounds__(256) quantize_cols_kernel(const __grid_constan
     if (staged) {
 #pragma unroll
       for (int i = 0; i < 32; ++i) {
-        if constexpr (V == 1) {
-          pair[i] = __float_as_uint(v[i]);
-        } else {
-          const uint32_t n = q.v_dtype == 1 ? narrow_pair<__half>(make_float2(v[i], v[i]))
-                                            : narrow_pair<__nv_bfloat16>(make_float2(v[i], v[i]));
-          pair[i] = __byte_perm(pair[i], n, h == 0 ? 0x3254 : 0x5410);
-        }
+        if constexpr (V == 1) mine[i * kTPitch] = __float_as_uint(v[i]);
+        else if (q.v_dtype == 1) reinterpret_cast<__half*>(mine + i * kTPitch)[h] = __float2half_rn(v[i]);
+        else reinterpret_cast<__nv_bfloat16*>(mine + i * kTPitch)[h] = __float2bfloat16_rn(v[i]);
       }
     } else if (q.values != nullptr && row < p.rows) {
 #pragma unroll
       for (int i = 0; i < 32; ++i)
         if (col + i < cols) static_cast<float*>(q.values)[row * q.ldv + col + i] = v[i];
     }
-  }
-  if (staged) {
-#pragma unroll
-    for (int i = 0; i < 32; ++i) mine[i * kTPitch] = pair[i];
   }
   __syncthreads();
   for (int i = threadIdx.x; i < kRows * kBytes / 4; i += 256) {

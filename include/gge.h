@@ -374,8 +374,9 @@ gge_status gge_mx_dequantize(const gge_mx_tensor* q, const gge_tensor* y, gge_st
  *   (one CTA, 128 x 128) or 64 (one CTA, for few rows of A: the roles of A and B
  *   are exchanged); num_ctas, raster_band, stages, timeout_ns; of the flags
  *   those for direct stores, no split, raster along N and the test hook.
- * The workspace is gge_workspace_size's (it may be smaller, and then no tile is
- * split along K).
+ * Few tiles are split along K over a cluster of 2, 4 or 8 CTAs, which add their
+ * sums in a fixed order through shared memory.  The workspace holds the status
+ * words (at least 256 bytes; NULL: device errors go unrecorded).
  */
 typedef struct gge_gemm_mx_args {
   gge_mx_tensor A;
