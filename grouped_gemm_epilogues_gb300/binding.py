@@ -9,7 +9,9 @@ raises.
 """
 
 import ctypes
+import importlib.util
 import os
+import struct
 import threading
 
 import torch
@@ -133,6 +135,7 @@ _SIGNATURES = {
 }
 
 _lib = None
+_marshal = None
 _lock = threading.Lock()
 
 
@@ -163,6 +166,19 @@ def load(path: str = None, build_if_missing: bool = True) -> ctypes.CDLL:
             fn.argtypes = args
         _lib = lib
         return lib
+
+
+def _load_marshal():
+    """The compiled marshalling of the low-precision entry points (gge_marshal.so)."""
+    global _marshal
+    load()
+    with _lock:
+        if _marshal is None:
+            spec = importlib.util.spec_from_file_location("gge_marshal", _build.MARSHAL)
+            module = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(module)
+            _marshal = module
+    return _marshal
 
 
 # ---------------------------------------------------------------- marshalling
@@ -509,7 +525,7 @@ def _mx_scale_bytes(fmt, rows, cols):
 class MxTensor:
     """A microscaled matrix (gge_mx_tensor): codes (rows, bytes) or (batch, rows, bytes)
     uint8, scales a contiguous uint8 tensor of gge_mx_scale_bytes a batch, tensor_scale None
-    or a one-element fp32 tensor on the device (nvfp4)."""
+    or a one-element fp32 tensor on the device (nvfp4).  ``c`` holds the C struct as bytes."""
 
     __slots__ = ("format", "rows", "cols", "batch", "tensor_scale", "device", "c", "_codes",
                  "_scales", "_buffer")
@@ -531,23 +547,26 @@ class MxTensor:
         per = _mx_scale_bytes(fmt, rows, cols)
         if scales.numel() != batch * per or not scales.is_contiguous():
             raise ValueError("MxTensor: scales do not match rows, cols and format")
-        self.device = codes.device
-        t = None
+        self.device = device = codes.device
+        t = 0
         if tensor_scale is not None:
             if tensor_scale.dtype is not torch.float32 or tensor_scale.numel() != 1:
                 raise ValueError("MxTensor: tensor_scale is one fp32 value")
-            _same_device(self.device, tensor_scale)
+            if tensor_scale.device != device:
+                raise ValueError("MxTensor: tensors on different devices")
             t = tensor_scale.data_ptr()
-        _same_device(self.device, scales)
+        if scales.device != device:
+            raise ValueError("MxTensor: tensors on different devices")
         self.format, self.rows, self.cols, self.batch = format, rows, cols, batch
         self.tensor_scale, self._codes, self._scales, self._buffer = tensor_scale, codes, scales, None
-        self.c = GgeMxTensor(codes.data_ptr(), scales.data_ptr(), t, fmt, 0, rows, cols, batch,
-                             stride[-2], step, per)
+        self.c = _MX_STRUCT.pack(codes.data_ptr(), scales.data_ptr(), t, fmt, 0, rows, cols, batch,
+                                 stride[-2], step, per)
 
     @property
     def codes(self):
         if self._codes is None:   # mx_empty: a view of its one buffer, made when asked for
-            c, row = self.c, self.c.stride_row
+            c = GgeMxTensor.from_buffer_copy(self.c)
+            row = c.stride_row
             if c.stride_batch:
                 self._codes = self._buffer.as_strided((c.batch, c.rows, row), (c.stride_batch, row, 1))
             else:
@@ -557,82 +576,35 @@ class MxTensor:
     @property
     def scales(self):
         if self._scales is None:
-            c = self.c
+            c = GgeMxTensor.from_buffer_copy(self.c)
             self._scales = self._buffer.as_strided((c.batch * c.scale_stride_batch,), (1,),
                                                    c.scales - c.codes)
         return self._scales
 
 
 def mx_empty(rows, cols, format, device=None, batch=None, tensor_scale=None):
-    """An MxTensor with room for (rows, cols) or (batch, rows, cols) values: its codes and
-    scales share one allocation."""
+    """An MxTensor with room for (rows, cols) or (batch, rows, cols) values on a CUDA device:
+    its codes and scales share one allocation."""
     fmt = MX_FORMAT[format]
-    if device is None:
-        device = torch.device("cuda", torch.cuda.current_device())
+    if device is None or device.__class__ is not torch.device or device.index is None:
+        device = torch.device("cuda" if device is None else device)
+        if device.index is None:
+            device = torch.device(device.type, torch.cuda.current_device())
+    if device.type != "cuda":
+        raise ValueError("mx_empty: not a CUDA device")
     row, per = _mx_row_bytes(fmt, cols), _mx_scale_bytes(fmt, rows, cols)
     b = 1 if batch is None else batch
     start = (b * rows * row + 511) & ~511
     q = MxTensor.__new__(MxTensor)
-    q._buffer = buf = torch.empty(start + b * per, dtype=torch.uint8, device=device)
-    q.device = buf.device
-    t = None
-    if tensor_scale is not None:
-        if tensor_scale.dtype is not torch.float32 or tensor_scale.numel() != 1:
-            raise ValueError("mx_empty: tensor_scale is one fp32 value")
-        _same_device(q.device, tensor_scale)
-        t = tensor_scale.data_ptr()
-    q.format, q.rows, q.cols, q.batch, q.tensor_scale = format, rows, cols, b, tensor_scale
+    q._buffer, q.c = (_marshal or _load_marshal()).mx_alloc(
+        start + b * per, start, device.index, fmt, rows, cols, 0 if batch is None else batch, row, per,
+        tensor_scale)
+    q.device, q.format, q.rows, q.cols, q.batch, q.tensor_scale = device, format, rows, cols, b, tensor_scale
     q._codes = q._scales = None
-    ptr = buf.data_ptr()
-    q.c = GgeMxTensor(ptr, ptr + start, t, fmt, 0, rows, cols, b, row,
-                      0 if batch is None else rows * row, per)
     return q
 
 
-def _same_device(device, *tensors):
-    for t in tensors:
-        if t is not None and t.device != device:
-            raise ValueError("tensors on different devices")
-
-
-def _tensor(t, kind):
-    """The C view of a tensor, as view() makes it."""
-    shape, stride = t.shape, t.stride()
-    code = DTYPE.get(t.dtype)
-    if code is None:
-        raise TypeError(f"{kind}: unsupported dtype {t.dtype}")
-    if len(shape) == 2:
-        return GgeTensor(t.data_ptr(), code, 0, shape[0], shape[1], 1, stride[0], stride[1], 0)
-    if len(shape) == 3:
-        return GgeTensor(t.data_ptr(), code, 0, shape[1], shape[2], shape[0], stride[1], stride[2],
-                         stride[0])
-    raise ValueError(f"{kind}: expected a 2-D or 3-D tensor")
-
-
-def _output(t, kind, device):
-    """The address of an optional tensor's C view (0: none), and the view to keep."""
-    if t is None:
-        return None, None
-    if t.device != device:
-        raise ValueError(f"{kind}: tensors on different devices")
-    v = _tensor(t, kind)
-    return _address(v), v
-
-
-_address = ctypes.addressof
-
-
-def _vector(t, kind, device, n, dtype=None):
-    """The address of a contiguous vector of n values."""
-    if t.device != device:
-        raise ValueError(f"{kind}: tensors on different devices")
-    if t.numel() != n or not t.is_contiguous() or (dtype is not None and t.dtype is not dtype):
-        raise ValueError(f"{kind}: expected {n} contiguous values" + (f" of {dtype}" if dtype else ""))
-    return t.data_ptr()
-
-
-def _raw_stream(device):
-    return torch._C._cuda_getCurrentRawStream(device.index)
+_MX_STRUCT = struct.Struct("=QQQiiqqqqqq")   # gge_mx_tensor
 
 
 def _shared(device, need):
@@ -643,26 +615,24 @@ def _shared(device, need):
     return ws
 
 
+def _on(Q, device):
+    """The C struct of an MxTensor that has to be on a device."""
+    if Q.device != device:
+        raise ValueError("MxTensor: tensors on different devices")
+    return Q.c
+
+
 def gge_mx_quantize(X, Q, values=None):
     """Q (an MxTensor) = X quantised; X (rows, cols) or (batch, rows, cols), row-major or a
     transposed view.  values: optional output, the numbers that the codes stand for."""
-    dev = X.device
-    if Q.device != dev:
-        raise ValueError("Q: tensors on different devices")
-    x = _tensor(X, "X")
-    v, keep = _output(values, "values", dev)
-    code = load().gge_mx_quantize(_address(x), _address(Q.c), v, _raw_stream(dev))
+    code = (_marshal or _load_marshal()).quantize(X, _on(Q, X.device), values)
     if code:
         raise GgeError(code, "gge_mx_quantize")
 
 
 def gge_mx_dequantize(Q, Y):
     """Y (bf16, f16 or f32) = the numbers that Q's codes stand for."""
-    dev = Y.device
-    if Q.device != dev:
-        raise ValueError("Q: tensors on different devices")
-    y = _tensor(Y, "Y")
-    code = load().gge_mx_dequantize(_address(Q.c), _address(y), _raw_stream(dev))
+    code = (_marshal or _load_marshal()).dequantize(_on(Q, Y.device), Y)
     if code:
         raise GgeError(code, "gge_mx_dequantize")
 
@@ -686,18 +656,10 @@ def gge_gemm_mx(A, B, D=None, C=None, PostAct=None, act="none", alpha=1.0, beta=
     """D = alpha * A @ B^T + beta * C and / or PostAct = act(same) of MxTensors A (M, K) and
     B (N, K) (or batched), their tensor scales included."""
     dev = A.device
-    if B.device != dev:
-        raise ValueError("B: tensors on different devices")
-    d, keep_d = _output(D, "D", dev)
-    c, keep_c = _output(C, "C", dev)
-    p, keep_p = _output(PostAct, "PostAct", dev)
-    args = GgeGemmMxArgs(A.c, B.c, c, d, p, alpha, beta,
-                         _vector(alpha_dev, "alpha_dev", dev, 1, torch.float32) if alpha_dev is not None else None,
-                         _vector(beta_dev, "beta_dev", dev, 1, torch.float32) if beta_dev is not None else None,
-                         ACT[act], 0, _address(config) if config is not None else None)
-    need = _need(dev)[0]
-    ws = _shared(dev, need) if workspace is None else _ws(dev, need, workspace)
-    code = load().gge_gemm_mx(_address(args), ws.data_ptr(), ws.numel(), _raw_stream(dev))
+    ws = _shared(dev, 256) if workspace is None else _ws(dev, 256, workspace)
+    code = (_marshal or _load_marshal()).gemm_mx(
+        A.c, _on(B, dev), dev.index, D, C, PostAct, ACT[act], alpha, beta, alpha_dev, beta_dev,
+        ctypes.addressof(config) if config is not None else 0, ws)
     if code:
         raise GgeError(code, "gge_gemm_mx")
 
@@ -707,26 +669,9 @@ def gge_rmsnorm(X, weight, Y=None, residual=None, residual_out=None, Q=None, val
     """h = X + residual (rounded to X's type, written to residual_out), inv_rms = 1 / sqrt(mean
     h^2 + eps) a row, Y = h * inv_rms * weight; Q (an MxTensor) = the same quantised, values =
     the numbers that Q's codes stand for.  X (rows, cols); every output is optional."""
-    dev = X.device
-    x = _tensor(X, "X")
-    if x.batch != 1:
-        raise ValueError("X: expected a 2-D tensor")
-    w = _vector(weight, "weight", dev, x.cols)
-    w_type = DTYPE.get(weight.dtype)
-    if w_type is None:
-        raise TypeError(f"weight: unsupported dtype {weight.dtype}")
-    q = None
-    if Q is not None:
-        if Q.device != dev:
-            raise ValueError("Q: tensors on different devices")
-        q = _address(Q.c)
-    r, keep_r = _output(residual, "residual", dev)
-    h, keep_h = _output(residual_out, "residual_out", dev)
-    y, keep_y = _output(Y, "Y", dev)
-    v, keep_v = _output(values, "values", dev)
-    args = GgeRmsnormArgs(x, r, h, y, q, v, w, w_type, eps,
-                          _vector(inv_rms, "inv_rms", dev, x.rows, torch.float32) if inv_rms is not None else None)
-    code = load().gge_rmsnorm(_address(args), _raw_stream(dev))
+    code = (_marshal or _load_marshal()).rmsnorm(
+        X, weight, Y, residual, residual_out, _on(Q, X.device) if Q is not None else None, values,
+        inv_rms, eps)
     if code:
         raise GgeError(code, "gge_rmsnorm")
 
@@ -734,27 +679,13 @@ def gge_rmsnorm(X, weight, Y=None, residual=None, residual_out=None, Q=None, val
 def gge_rmsnorm_bwd(dY, H, weight, inv_rms, dX, dW=None, dH=None, workspace=None):
     """Backward of gge_rmsnorm: dX (the gradient of X and of the residual) from dY, the saved H
     (residual_out, or X) and inv_rms; dW (fp32, optional); dH the gradient reaching H directly."""
-    dev = dY.device
-    dy = _tensor(dY, "dY")
-    if dy.batch != 1:
-        raise ValueError("dY: expected a 2-D tensor")
-    if H.device != dev or dX.device != dev:
-        raise ValueError("H, dX: tensors on different devices")
-    w = _vector(weight, "weight", dev, dy.cols)
-    w_type = DTYPE.get(weight.dtype)
-    if w_type is None:
-        raise TypeError(f"weight: unsupported dtype {weight.dtype}")
-    inv = _vector(inv_rms, "inv_rms", dev, dy.rows, torch.float32)
-    dh, keep_dh = _output(dH, "dH", dev)
-    dw = ws = None
-    n = 0
-    if dW is not None:
-        dw = _vector(dW, "dW", dev, dy.cols, torch.float32)
+    if dW is None:
+        ws = None
+    else:
+        dev = dY.device
         _, fixed, a_col = _need(dev)
-        need = fixed + a_col * dy.cols
-        buf = _shared(dev, need) if workspace is None else _ws(dev, need, workspace)
-        ws, n = buf.data_ptr(), buf.numel()
-    args = GgeRmsnormBwdArgs(dy, _tensor(H, "H"), dh, _tensor(dX, "dX"), w, w_type, 0, inv, dw)
-    code = load().gge_rmsnorm_bwd(_address(args), ws, n, _raw_stream(dev))
+        need = fixed + a_col * dY.shape[-1]
+        ws = _shared(dev, need) if workspace is None else _ws(dev, need, workspace)
+    code = (_marshal or _load_marshal()).rmsnorm_bwd(dY, H, weight, inv_rms, dX, dW, dH, ws)
     if code:
         raise GgeError(code, "gge_rmsnorm_bwd")

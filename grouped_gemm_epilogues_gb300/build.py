@@ -3,6 +3,7 @@
 Each .cu under csrc/ and csrc/lowp/ is compiled in parallel into _build/, then linked into
 ``_build/libgge.so``.  ``python -m grouped_gemm_epilogues_gb300.build`` or
 ``build()`` from Python; ``-Xptxas -v`` output goes to ``_build/ptxas.log``.
+csrc/lowp/marshal.cpp becomes ``_build/gge_marshal.so``, a Python module over libgge.so.
 """
 
 import concurrent.futures as cf
@@ -11,12 +12,14 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(BUILD, "libgge.so")
+MARSHAL = os.path.join(BUILD, "gge_marshal.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xptxas", "-v",
@@ -36,7 +39,7 @@ def _sources():
 
 
 def _deps():
-    return _sources() + sorted(glob.glob(os.path.join(CSRC, "**", "*.cuh"), recursive=True) +
+    return _sources() + [os.path.join(CSRC, "lowp", "marshal.cpp")] + sorted(glob.glob(os.path.join(CSRC, "**", "*.cuh"), recursive=True) +
                                glob.glob(os.path.join(CSRC, "**", "*.h"), recursive=True) +
                                glob.glob(os.path.join(ROOT, "include", "*.h")))
 
@@ -48,10 +51,37 @@ def _compile(src: str) -> tuple:
     return obj, r.returncode, r.stdout + r.stderr, " ".join(cmd)
 
 
+def _compile_marshal(obj: str) -> tuple:
+    """The Python module's object file (torch's and CPython's headers)."""
+    import torch
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-isystem", inc, "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"),
+           "-isystem", cuda, "-isystem", sysconfig.get_paths()["include"],
+           "-c", os.path.join(CSRC, "lowp", "marshal.cpp"), "-o", obj]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    return obj, r.returncode, r.stdout + r.stderr, " ".join(cmd)
+
+
+def _link_marshal(obj: str) -> None:
+    import torch
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = MARSHAL + ".tmp"
+    cmd = ["g++", "-shared", "-o", tmp, obj, "-L", BUILD, "-L", lib, "-lgge", "-ltorch_python",
+           "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + lib]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        sys.stderr.write(r.stdout + r.stderr)
+        raise RuntimeError("link of gge_marshal failed")
+    os.replace(tmp, MARSHAL)
+
+
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(MARSHAL):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(MARSHAL))
     return all(os.path.getmtime(d) <= t for d in _deps())
 
 
@@ -60,9 +90,12 @@ def build(force: bool = False, verbose: bool = False) -> str:
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 4)) as ex:
+        marshal_obj = os.path.join(BUILD, "marshal.o")
+        marshal = ex.submit(_compile_marshal, marshal_obj)
         results = list(ex.map(_compile, _sources()))
+        marshal = marshal.result()
     log = []
-    for obj, rc, out, cmd in results:
+    for obj, rc, out, cmd in results + [marshal]:
         log.append(f"$ {cmd}\n{out}")
         if rc != 0:
             sys.stderr.write(out)
@@ -77,6 +110,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
         sys.stderr.write(r.stdout + r.stderr)
         raise RuntimeError("link failed")
     os.replace(tmp, LIB)
+    _link_marshal(marshal_obj)
     if verbose:
         print("\n".join(log))
     return LIB

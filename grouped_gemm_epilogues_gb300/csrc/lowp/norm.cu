@@ -83,10 +83,10 @@ __device__ __forceinline__ void clear_past(Raw8<T>& r, int32_t col, int32_t cols
 // only; otherwise the warp does it together (rows.cuh).
 template <typename T, bool AL>
 struct RowReader {
-  const T* next;  // the next row to copy: AL this lane's chunk 0 of it, else its start
+  const T* next;  // this lane's chunk 0 of the next row to copy
 
   __device__ __forceinline__ void init(const void* base, int64_t ld, int64_t row, int32_t col) {
-    next = static_cast<const T*>(base) + row * ld + (AL ? col : 0);
+    next = static_cast<const T*>(base) + row * ld + col;
   }
   // AL, once a buffer: a lane's pieces past the row's end stay zero
   static __device__ __forceinline__ void clear(uint32_t dst, int32_t col, int32_t cols) {
@@ -103,17 +103,17 @@ struct RowReader {
                                        bool first) const {
     constexpr int P = WarpRow<T>::kPieces;
     const int lane = threadIdx.x & 31;
+    const int32_t left = (cols - col) * static_cast<int32_t>(sizeof(T));
     if constexpr (AL) {
 #pragma unroll
       for (int j = 0; j < P; ++j) {
         // (bytes past the row's end are zero-filled; none are read)
-        const int32_t left = (cols - col) * static_cast<int32_t>(sizeof(T)) - 16 * j;
-        if (left > 0)
+        if (left > 16 * j)
           ptx::cp_async_16(dst + 16u * (lane * P + j), next + over + j * (16 / sizeof(T)),
-                           static_cast<uint32_t>(min(16, left)));
+                           static_cast<uint32_t>(min(16, left - 16 * j)));
       }
     } else {
-      if (col - lane * 8 < cols) copy_row(dst, next, col - lane * 8, cols, first);
+      copy_row(dst, next + over, left, first && col == lane * 8);
     }
   }
 };

@@ -115,51 +115,78 @@ __global__ void __launch_bounds__(256)
 // free of bank conflicts.
 constexpr int kTCols = 128, kTWords = 64, kTPitch = kTWords + 1;
 
-// One row's 32 values v (of a part's columns), quantised: codes to w, a scale byte
-// a block to `bytes`, and the values of the codes back to v.
-template <int FMT>
-__device__ __forceinline__ void quantise32(float (&v)[32], float tscale, int32_t col, int32_t cols,
-                                           uint32_t (&w)[8], uint8_t* bytes, bool values) {
-  constexpr int B = Fmt<FMT>::kBlock;
+// 32 columns of the V rows that words[0..31] hold, quantised: a row's codes to w[row],
+// a scale byte a block to bytes[row * pitch], and, where wanted, the numbers that the
+// codes stand for (rounded to O) back to the words (V = 2) or to their floats (V = 1).
+template <typename T, int FMT, typename O>
+__device__ __forceinline__ void quantise_words(uint32_t (&words)[32], float tscale, int32_t col, int32_t cols,
+                                               uint32_t (&w)[4 / sizeof(T)][8], uint8_t* bytes, int pitch,
+                                               bool values) {
+  constexpr int V = 4 / sizeof(T), B = Fmt<FMT>::kBlock;
 #pragma unroll
   for (int k = 0; k < 32; k += B) {
-    float m = 0.f;
+    float factor[V], unit[V];
+    uint32_t amax[V];
+    if constexpr (V == 2) {
+      using T2 = typename Pair<T>::type;
+      T2 m = __habs2(*reinterpret_cast<const T2*>(&words[k]));
 #pragma unroll
-    for (int i = 0; i < B; ++i) m = max_abs(m, v[k + i]);
-    float factor;
-    const uint32_t s = block_scale<FMT>(abs_bits(m), tscale, factor);
-    const float unit = scale_value<FMT>(s);
-    bytes[k / B] = static_cast<uint8_t>(col + k < cols ? s : 0u);
+      for (int i = 1; i < B; ++i) m = __hmax2_nan(m, __habs2(*reinterpret_cast<const T2*>(&words[k + i])));
+      const float2 f = widen_pair<T>(*reinterpret_cast<const uint32_t*>(&m));
+      amax[0] = abs_bits(f.x);
+      amax[1] = abs_bits(f.y);
+    } else {
+      float m = 0.f;
+#pragma unroll
+      for (int i = 0; i < B; ++i) m = max_abs(m, __uint_as_float(words[k + i]));
+      amax[0] = abs_bits(m);
+    }
+#pragma unroll
+    for (int h = 0; h < V; ++h) {
+      const uint32_t s = block_scale<FMT>(amax[h], tscale, factor[h]);
+      unit[h] = scale_value<FMT>(s);
+      bytes[h * pitch + k / B] = static_cast<uint8_t>(col + k < cols ? s : 0u);
+    }
 #pragma unroll
     for (int i = k; i < k + B; i += 8) {
-      float c[8];
+      float2 back[V][4];
 #pragma unroll
-      for (int j = 0; j < 8; j += 2) {
-        const float2 f = __fmul2_rn(make_float2(v[i + j], v[i + j + 1]), make_float2(factor, factor));
-        c[j] = f.x;
-        c[j + 1] = f.y;
-      }
-      const uint2 codes = pack8<FMT>(c);
-      if constexpr (FMT == FMT_MXFP8) {
-        w[i / 4] = codes.x;
-        w[i / 4 + 1] = codes.y;
-      } else {
-        w[i / 8] = codes.x;
+      for (int h = 0; h < V; ++h) {
+        float c[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          float x;
+          if constexpr (V == 1) x = __uint_as_float(words[i + j]);
+          else x = h == 0 ? widen_pair<T>(words[i + j]).x : widen_pair<T>(words[i + j]).y;
+          c[j] = x * factor[h];
+        }
+        const uint2 codes = pack8<FMT>(c);
+        if constexpr (FMT == FMT_MXFP8) {
+          w[h][i / 4] = codes.x;
+          w[h][i / 4 + 1] = codes.y;
+        } else {
+          w[h][i / 8] = codes.x;
+        }
+        if (values) code_values<FMT>(codes, unit[h], tscale, back[h]);
       }
       if (values) {
-        float2 f[4];
-        code_values<FMT>(codes, unit, tscale, f);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          v[i + 2 * j] = f[j].x;
-          v[i + 2 * j + 1] = f[j].y;
+          if constexpr (V == 1) {
+            words[i + 2 * j] = __float_as_uint(back[0][j].x);
+            words[i + 2 * j + 1] = __float_as_uint(back[0][j].y);
+          } else {
+            words[i + 2 * j] = narrow_pair<O>(make_float2(back[0][j].x, back[1][j].x));
+            words[i + 2 * j + 1] = narrow_pair<O>(make_float2(back[0][j].y, back[1][j].y));
+          }
         }
       }
     }
   }
 }
 
-template <typename T, int FMT, bool AL>
+// O: the type of the values (what a 16-bit source's words take; bf16 where none).
+template <typename T, int FMT, bool AL, typename O>
 __global__ void __launch_bounds__(256, 4) quantize_cols_kernel(const __grid_constant__ QuantParams p) {
   constexpr int V = 4 / sizeof(T);         // rows a word holds
   constexpr int kRows = kTWords * V;       // rows of the tile
@@ -203,39 +230,25 @@ __global__ void __launch_bounds__(256, 4) quantize_cols_kernel(const __grid_cons
   const int part = threadIdx.x / kTWords, at = threadIdx.x % kTWords;  // 32 columns a part
   const int32_t col = col0 + part * 32;
   uint32_t* mine = tile + part * 32 * kTPitch + at;
-  // values of a 16-bit type, or of a source of 32 bits, go out through the tile, in the
-  // place of the source's (each half of a word by the pass that read it)
-  const bool staged = q.values != nullptr && (V == 1 || q.v_dtype != 4);
-#pragma unroll 1
+  uint32_t held[32];
+#pragma unroll
+  for (int i = 0; i < 32; ++i) held[i] = mine[i * kTPitch];
+  uint32_t w[V][8];
+  quantise_words<T, FMT, O>(held, tscale, col, cols, w,
+                            reinterpret_cast<uint8_t*>(words) + at * V * kBytes + part * (kBytes / 4), kBytes,
+                            q.values != nullptr);
+#pragma unroll
   for (int h = 0; h < V; ++h) {
     const int64_t row = row0 + at * V + h;
-    float v[32];
-#pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      if constexpr (V == 1) v[i] = __uint_as_float(mine[i * kTPitch]);
-      else v[i] = to_float<T>(reinterpret_cast<const T*>(mine + i * kTPitch)[h]);
-    }
-    uint32_t w[8];
-    quantise32<FMT>(v, tscale, col, cols, w,
-                    reinterpret_cast<uint8_t*>(words) + (at * V + h) * kBytes + part * (kBytes / 4),
-                    q.values != nullptr);
     if (row < p.rows && col < ((cols + 31) & ~31)) {
       uint4* dst = reinterpret_cast<uint4*>(q.codes + row * q.ld + static_cast<int64_t>(col) * Fmt<FMT>::kBits / 8);
-      dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
-      if constexpr (FMT == FMT_MXFP8) dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+      dst[0] = make_uint4(w[h][0], w[h][1], w[h][2], w[h][3]);
+      if constexpr (FMT == FMT_MXFP8) dst[1] = make_uint4(w[h][4], w[h][5], w[h][6], w[h][7]);
     }
-    if (staged) {
+  }
+  if (q.values != nullptr) {  // the values take the source's place in the tile
 #pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        if constexpr (V == 1) mine[i * kTPitch] = __float_as_uint(v[i]);
-        else if (q.v_dtype == 1) reinterpret_cast<__half*>(mine + i * kTPitch)[h] = __float2half_rn(v[i]);
-        else reinterpret_cast<__nv_bfloat16*>(mine + i * kTPitch)[h] = __float2bfloat16_rn(v[i]);
-      }
-    } else if (q.values != nullptr && row < p.rows) {
-#pragma unroll
-      for (int i = 0; i < 32; ++i)
-        if (col + i < cols) static_cast<float*>(q.values)[row * q.ldv + col + i] = v[i];
-    }
+    for (int i = 0; i < 32; ++i) mine[i * kTPitch] = held[i];
   }
   __syncthreads();
   for (int i = threadIdx.x; i < kRows * kBytes / 4; i += 256) {
@@ -244,7 +257,7 @@ __global__ void __launch_bounds__(256, 4) quantize_cols_kernel(const __grid_cons
     if (row0 + rr < p.rows && kg < q.kgroups)
       *reinterpret_cast<uint32_t*>(q.scales + scale_word(row0 + rr, kg, q.kgroups)) = words[rr * (kBytes / 4) + kw];
   }
-  if (!staged) return;
+  if (q.values == nullptr) return;
   // a warp a word of rows, one column a lane: whole lines at any alignment
   const int lane = threadIdx.x & 31;
   for (int r = threadIdx.x >> 5; r < kTWords; r += 8) {
@@ -274,7 +287,9 @@ cudaError_t launch_quantize_t(const QuantParams& p, cudaStream_t st) {
                       p, tiles);
   }
   constexpr int kRows = kTWords * (4 / sizeof(T));
-  return launch_pdl(quantize_cols_kernel<T, FMT, AL>,
+  const bool half = p.q.values != nullptr && p.q.v_dtype == 1;
+  return launch_pdl(half ? quantize_cols_kernel<T, FMT, AL, __half>
+                         : quantize_cols_kernel<T, FMT, AL, __nv_bfloat16>,
                     dim3(static_cast<unsigned>((p.rows + kRows - 1) / kRows),
                          static_cast<unsigned>((span + kTCols - 1) / kTCols),
                          static_cast<unsigned>(p.batch)),
@@ -334,6 +349,24 @@ __global__ void __launch_bounds__(256)
 }  // namespace
 
 cudaError_t launch_quantize(const QuantParams& p, cudaStream_t st) {
+  if (p.dtype != 4 && p.q.values != nullptr && p.q.v_dtype == 4 && p.stride_col != 1 && p.cols != 1) {
+    // the transposing kernel passes a 16-bit source's values on in 16 bits: 32-bit ones
+    // are read back from the codes
+    QuantParams codes = p;
+    codes.q.values = nullptr;
+    const cudaError_t e = launch_quantize(codes, st);
+    if (e != cudaSuccess) return e;
+    DequantParams d{};
+    d.rows = p.rows, d.cols = p.cols, d.batch = p.batch;
+    d.format = p.q.format;
+    d.codes = p.q.codes, d.scales = p.q.scales;
+    d.ld = p.q.ld, d.batch_stride = p.q.batch_stride;
+    d.kgroups = p.q.kgroups, d.scale_batch_stride = p.q.scale_batch_stride;
+    d.tensor_scale = p.q.tensor_scale;
+    d.y = p.q.values, d.ldy = p.q.ldv, d.y_batch_stride = p.q.values_batch_stride;
+    d.dtype = 4;
+    return launch_dequantize(d, st);  // (any alignment)
+  }
   if (p.dtype == 0) return launch_quantize_f<__nv_bfloat16>(p, st);
   if (p.dtype == 1) return launch_quantize_f<__half>(p, st);
   return launch_quantize_f<float>(p, st);

@@ -26,53 +26,46 @@ struct WarpRow {
   static constexpr int kBytes = (32 * kPieces + 1) * 16;         // of a warp's 256 columns
 };
 
-// Words w[i] of a 16-byte aligned stream, moved down by `b` bytes (a multiple of 2;
-// the same in every lane).
+// N words of a stream, from `b` bytes on (a multiple of 2 below 16).
 template <int N>
-__device__ __forceinline__ void shift_down(uint32_t (&w)[N], uint32_t b) {
-  if (b & 8u) {
+__device__ __forceinline__ void pick(const uint32_t (&w)[N + 4], uint32_t b, uint32_t (&o)[N]) {
+  const bool two = (b & 8u) != 0, one = (b & 4u) != 0;
+  const uint32_t half = (b & 2u) * 8;
+  uint32_t a[N + 2], c[N + 1];
 #pragma unroll
-    for (int i = 0; i + 2 < N; ++i) w[i] = w[i + 2];
-  }
-  if (b & 4u) {
+  for (int i = 0; i < N + 2; ++i) a[i] = two ? w[i + 2] : w[i];
 #pragma unroll
-    for (int i = 0; i + 1 < N; ++i) w[i] = w[i + 1];
-  }
-  if (b & 2u) {
+  for (int i = 0; i < N + 1; ++i) c[i] = one ? a[i + 1] : a[i];
 #pragma unroll
-    for (int i = 0; i + 1 < N; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
-  }
+  for (int i = 0; i < N; ++i) o[i] = __funnelshift_r(c[i], c[i + 1], half);
 }
 
-// Start copying columns [col0, col0 + 256) of the row at `row` (`cols` long) to
-// `dst`.  `first`: nothing may be read in front of the row.
+// Start copying this warp's 256 columns of a row to `dst`.  `at`: this lane's first
+// value, `left`: bytes from there to the row's end (it may be negative).  `first`:
+// nothing may be read in front of the row, which starts at this warp's lane 0.
 template <typename T>
-__device__ __forceinline__ void copy_row(uint32_t dst, const T* row, int32_t col0, int32_t cols,
-                                         bool first) {
+__device__ __forceinline__ void copy_row(uint32_t dst, const T* at, int32_t left, bool first) {
   constexpr int P = WarpRow<T>::kPieces;
   const int lane = threadIdx.x & 31;
-  const uintptr_t at = reinterpret_cast<uintptr_t>(row + col0);
-  const uint32_t b = static_cast<uint32_t>(at) & 15u;
-  const uintptr_t end = reinterpret_cast<uintptr_t>(row + cols);
-  const uintptr_t piece0 = at - b;
+  const uint32_t b = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(at)) & 15u;
+  const uint8_t* src = reinterpret_cast<const uint8_t*>(at) - b;  // of the lane's first piece
+  left += static_cast<int32_t>(b);
+  dst += 16u * P * lane;
 #pragma unroll
-  for (int j = 0; j <= P; ++j) {
-    if (j == P && (lane != 31 || b == 0)) break;
-    const uint32_t k = static_cast<uint32_t>(lane * P + j);
-    const uintptr_t src = piece0 + 16u * k;
-    if (src >= end) continue;
-    const uint32_t bytes = static_cast<uint32_t>(min(static_cast<uintptr_t>(16), end - src));
-    if (src < reinterpret_cast<uintptr_t>(row) && first) {
-      for (uint32_t o = b; o < bytes; o += sizeof(T)) {
+  for (int j = 0; j < P; ++j) {
+    if (j == 0 && first && b != 0 && lane == 0) {
+      for (int32_t o = b; o < min(16, left); o += sizeof(T)) {
         if constexpr (sizeof(T) == 2)
-          ptx::st_shared_u16(dst + 16u * k + o, *reinterpret_cast<const uint16_t*>(src + o));
+          ptx::st_shared_u16(dst + o, *reinterpret_cast<const uint16_t*>(src + o));
         else
-          ptx::st_shared_u32(dst + 16u * k + o, *reinterpret_cast<const uint32_t*>(src + o));
+          ptx::st_shared_u32(dst + o, *reinterpret_cast<const uint32_t*>(src + o));
       }
-    } else {
-      ptx::cp_async_16(dst + 16u * k, reinterpret_cast<const void*>(src), bytes);
+    } else if (left > 16 * j) {
+      ptx::cp_async_16(dst + 16 * j, src + 16 * j, static_cast<uint32_t>(min(16, left - 16 * j)));
     }
   }
+  if (lane == 31 && b != 0 && left > 16 * P)
+    ptx::cp_async_16(dst + 16 * P, src + 16 * P, static_cast<uint32_t>(min(16, left - 16 * P)));
 }
 
 // A lane's 8 values of a copied row, after the copy has landed (values past the
@@ -84,18 +77,15 @@ __device__ __forceinline__ Raw8<T> take_row(uint32_t src, uint32_t b) {
   const int lane = threadIdx.x & 31;
   uint32_t w[4 * P + 4];
 #pragma unroll
-  for (int j = 0; j < P; ++j) {
+  for (int j = 0; j <= P; ++j) {
     const uint4 v = ptx::ld_shared_v4(src + 16u * (lane * P + j));
     w[4 * j] = v.x, w[4 * j + 1] = v.y, w[4 * j + 2] = v.z, w[4 * j + 3] = v.w;
   }
-  if (b != 0) {
-    const uint4 v = ptx::ld_shared_v4(src + 16u * (lane * P + P));
-    w[4 * P] = v.x, w[4 * P + 1] = v.y, w[4 * P + 2] = v.z, w[4 * P + 3] = v.w;
-    shift_down(w, b);
-  }
+  uint32_t o[4 * P];
+  pick(w, b, o);
   Raw8<T> r;
 #pragma unroll
-  for (int j = 0; j < P; ++j) r.w[j] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+  for (int j = 0; j < P; ++j) r.w[j] = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
   return r;
 }
 
@@ -118,9 +108,10 @@ __device__ __forceinline__ Raw8<T> load_row8(const T* row, int32_t col, int32_t 
       const uint4 v = *reinterpret_cast<const uint4*>(piece0 + 16u * j);
       w[4 * j] = v.x, w[4 * j + 1] = v.y, w[4 * j + 2] = v.z, w[4 * j + 3] = v.w;
     }
-    shift_down(w, b);
+    uint32_t o[4 * P];
+    pick(w, b, o);
 #pragma unroll
-    for (int j = 0; j < P; ++j) r.w[j] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+    for (int j = 0; j < P; ++j) r.w[j] = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
     return r;
   }
   T* t = reinterpret_cast<T*>(&r);
@@ -148,48 +139,48 @@ template <typename T>
 __device__ __forceinline__ void store_row8(T* row, int32_t col, int32_t cols, const Raw8<T>& v) {
   constexpr int P = WarpRow<T>::kPieces;
   const int lane = threadIdx.x & 31;
-  const T* t = reinterpret_cast<const T*>(&v);
   const uint32_t b = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(row)) & 15u;
   if (b == 0) {  // (col is a multiple of 8)
     store_row8_aligned(row, col, cols, v);
     return;
   }
   // Shifted by k columns, 8 values start on the boundary: the previous lane's last
-  // k and this lane's first 8 - k.
+  // k and this lane's first 8 - k.  The warp's first 8 - k and last k are left over.
   const int32_t k = static_cast<int32_t>(b / sizeof(T));
   const int32_t start = col - k;
-  uint32_t w[8 * P];
+  uint32_t w[4 * P + 4], o[4 * P];
 #pragma unroll
-  for (int j = 0; j < P; ++j) {
-    w[4 * P + 4 * j] = v.w[j].x, w[4 * P + 4 * j + 1] = v.w[j].y;
-    w[4 * P + 4 * j + 2] = v.w[j].z, w[4 * P + 4 * j + 3] = v.w[j].w;
-  }
+  for (int j = 0; j < P; ++j)
+    w[4 + 4 * j] = v.w[j].x, w[5 + 4 * j] = v.w[j].y, w[6 + 4 * j] = v.w[j].z, w[7 + 4 * j] = v.w[j].w;
 #pragma unroll
-  for (int j = 0; j < 4 * P; ++j) w[j] = __shfl_up_sync(0xffffffffu, w[4 * P + j], 1);
-  if constexpr (P == 2) {  // k <= 3 of 8 values: the previous lane's first piece is not needed
-#pragma unroll
-    for (int j = 0; j < 12; ++j) w[j] = w[j + 4];
-  }
-  shift_down(w, 16u - b);
+  for (int j = 0; j < 4; ++j) w[j] = __shfl_up_sync(0xffffffffu, w[4 * P + j], 1);  // its last piece
+  pick(w, 16u - b, o);
   if (lane > 0 && start + 8 <= cols) {
     Raw8<T> r;
 #pragma unroll
-    for (int j = 0; j < P; ++j) r.w[j] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+    for (int j = 0; j < P; ++j) r.w[j] = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
     store8(row + start, r);
-  } else {
-    const T* s = reinterpret_cast<const T*>(w);
+  } else if (lane > 0) {  // the row's end
+    const T* s = reinterpret_cast<const T*>(o);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int32_t c = start + i;
-      if (c < cols && (lane > 0 || c >= col)) row[c] = s[i];
-    }
+    for (int i = 0; i < 8; ++i)
+      if (start + i < cols) row[start + i] = s[i];
   }
-  if (lane == 31) {  // its last k values have no next lane
+  // lanes 0-7 store the left-over values, one each
+  const int i = lane & 7;
+  const bool front = i < 8 - k;
+  uint32_t left = 0u;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int32_t c = col + i;
-      if (c >= start + 8 && c < cols) row[c] = t[i];
-    }
+  for (int j = 0; j < 4 * P; ++j) {
+    const uint32_t x = __shfl_sync(0xffffffffu, w[4 + j], front ? 0 : 31);
+    if ((P == 1 ? i >> 1 : i) == j) left = x;
+  }
+  const int32_t c = col - lane * 8 + (front ? 0 : 31 * 8) + i;
+  if (lane < 8 && c < cols) {
+    if constexpr (P == 1)
+      reinterpret_cast<uint16_t*>(row)[c] = static_cast<uint16_t>((i & 1) ? left >> 16 : left);
+    else
+      reinterpret_cast<uint32_t*>(row)[c] = left;
   }
 }
 
