@@ -128,6 +128,8 @@ _SIGNATURES = {
                                 ctypes.c_void_p]),
     "gge_mx_dequantize": (c_i32, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
     "gge_gemm_mx": (c_i32, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    "gge_gemm_mx_dact": (c_i32, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t,
+                                 ctypes.c_void_p]),
     "gge_rmsnorm": (c_i32, [ctypes.c_void_p, ctypes.c_void_p]),
     "gge_workspace_size_rmsnorm_bwd": (ctypes.c_size_t, [c_i64]),
     "gge_rmsnorm_bwd": (c_i32, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t,
@@ -659,9 +661,21 @@ def gge_gemm_mx(A, B, D=None, C=None, PostAct=None, act="none", alpha=1.0, beta=
     ws = _shared(dev, 256) if workspace is None else _ws(dev, 256, workspace)
     code = (_marshal or _load_marshal()).gemm_mx(
         A.c, _on(B, dev), dev.index, D, C, PostAct, ACT[act], alpha, beta, alpha_dev, beta_dev,
-        ctypes.addressof(config) if config is not None else 0, ws)
+        ctypes.addressof(config) if config is not None else 0, ws, False)
     if code:
         raise GgeError(code, "gge_gemm_mx")
+
+
+def gge_gemm_mx_dact(A, B, PreAct, D, act, PostAct=None, config=None, workspace=None):
+    """Backward activation epilogue on MxTensors: D = act'(PreAct) * (A @ B^T), PostAct =
+    act(PreAct)."""
+    dev = A.device
+    ws = _shared(dev, 256) if workspace is None else _ws(dev, 256, workspace)
+    code = (_marshal or _load_marshal()).gemm_mx(
+        A.c, _on(B, dev), dev.index, D, PreAct, PostAct, ACT[act], 1.0, 1.0, None, None,
+        ctypes.addressof(config) if config is not None else 0, ws, True)
+    if code:
+        raise GgeError(code, "gge_gemm_mx_dact")
 
 
 def gge_rmsnorm(X, weight, Y=None, residual=None, residual_out=None, Q=None, values=None,

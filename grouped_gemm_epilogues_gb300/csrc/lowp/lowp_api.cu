@@ -190,7 +190,7 @@ double mx_cost(const MxShape& s, int64_t k_tiles) {
          (s.splits > 1 ? 1200.0 : 0.0);
 }
 
-gge_status plan_mx(const gge_gemm_mx_args* a, void* ws, size_t ws_bytes, MxPlan* out) {
+gge_status plan_mx(const gge_gemm_mx_args* a, bool dact, void* ws, size_t ws_bytes, MxPlan* out) {
   if (a == nullptr) return GGE_ERR_INVALID_ARG;
   MxPlan& pl = *out;
   std::memset(&pl, 0, sizeof(pl));
@@ -200,7 +200,11 @@ gge_status plan_mx(const gge_gemm_mx_args* a, void* ws, size_t ws_bytes, MxPlan*
   if (cfg && (cfg->flags & ~kFlagsTaken)) return GGE_ERR_UNSUPPORTED;
   if (cfg && (cfg->batch_idx_permute != nullptr || cfg->cta_group != 0)) return GGE_ERR_UNSUPPORTED;
   if (a->D == nullptr && a->PostAct == nullptr) return GGE_ERR_INVALID_ARG;
-  if (a->PostAct == nullptr && a->act != GGE_ACT_NONE) return GGE_ERR_INVALID_ARG;
+  if (dact) {
+    if (a->C == nullptr || a->D == nullptr || a->act == GGE_ACT_NONE) return GGE_ERR_INVALID_ARG;
+  } else if (a->PostAct == nullptr && a->act != GGE_ACT_NONE) {
+    return GGE_ERR_INVALID_ARG;
+  }
   gge_status s = check_mx(a->A);
   if (s != GGE_OK) return s;
   s = check_mx(a->B);
@@ -286,6 +290,7 @@ gge_status plan_mx(const gge_gemm_mx_args* a, void* ws, size_t ws_bytes, MxPlan*
     p.c = a->C->ptr; p.ldc = a->C->stride_row; p.sbc = a->C->stride_batch; p.c_dtype = a->C->dtype;
   }
   p.act = a->act;
+  p.dact = dact ? 1 : 0;
   p.out_trans = swap ? 1 : 0;
   p.alpha = a->alpha;
   p.beta = a->beta;
@@ -337,6 +342,17 @@ gge_status plan_mx(const gge_gemm_mx_args* a, void* ws, size_t ws_bytes, MxPlan*
   if (s == GGE_OK) s = scales_map(&pl.maps.sa, ka, 1, &pl.mp.sfa_batch);
   if (s == GGE_OK) s = scales_map(&pl.maps.sb, kb, static_cast<uint32_t>(b_tiles), &pl.mp.sfb_batch);
   return s;
+}
+
+gge_status run_mx(const gge_gemm_mx_args* args, bool dact, void* ws, size_t ws_bytes, gge_stream_t stream) {
+  MxPlan pl;
+  const gge_status s = plan_mx(args, dact, ws, ws_bytes, &pl);
+  if (s != GGE_OK || pl.empty) return s;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const int32_t format = args->A.format;
+  return launched(format == GGE_MXFP8   ? mx::launch_mx<GGE_MXFP8>(pl.tile, pl.maps, pl.mp, pl.shape, st)
+                  : format == GGE_MXFP4 ? mx::launch_mx<GGE_MXFP4>(pl.tile, pl.maps, pl.mp, pl.shape, st)
+                                        : mx::launch_mx<GGE_NVFP4>(pl.tile, pl.maps, pl.mp, pl.shape, st));
 }
 
 }  // namespace
@@ -414,16 +430,11 @@ gge_status gge_mx_dequantize(const gge_mx_tensor* q, const gge_tensor* y, gge_st
 }
 
 gge_status gge_gemm_mx(const gge_gemm_mx_args* args, void* ws, size_t ws_bytes, gge_stream_t stream) {
-  MxPlan pl;
-  const gge_status s = plan_mx(args, ws, ws_bytes, &pl);
-  if (s != GGE_OK || pl.empty) return s;
-  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const int32_t format = args->A.format;
-  const cudaError_t e =
-      format == GGE_MXFP8   ? mx::launch_mx<GGE_MXFP8>(pl.tile, pl.maps, pl.mp, pl.shape, st)
-      : format == GGE_MXFP4 ? mx::launch_mx<GGE_MXFP4>(pl.tile, pl.maps, pl.mp, pl.shape, st)
-                            : mx::launch_mx<GGE_NVFP4>(pl.tile, pl.maps, pl.mp, pl.shape, st);
-  return launched(e);
+  return run_mx(args, false, ws, ws_bytes, stream);
+}
+
+gge_status gge_gemm_mx_dact(const gge_gemm_mx_args* args, void* ws, size_t ws_bytes, gge_stream_t stream) {
+  return run_mx(args, true, ws, ws_bytes, stream);
 }
 
 gge_status gge_rmsnorm(const gge_rmsnorm_args* a, gge_stream_t stream) {

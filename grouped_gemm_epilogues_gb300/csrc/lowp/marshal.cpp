@@ -178,10 +178,11 @@ PyObject* dequantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
-// gemm_mx(A, B, device, D, C, PostAct, act, alpha, beta, alpha_dev, beta_dev, config address or 0, workspace)
+// gemm_mx(A, B, device, D, C, PostAct, act, alpha, beta, alpha_dev, beta_dev, config address or 0, workspace,
+// backward epilogue)
 PyObject* gemm_mx(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
-  if (!count(n, 13)) return nullptr;
+  if (!count(n, 14)) return nullptr;
   const gge_mx_tensor* A = mx(a[0], false);
   if (A == nullptr) return nullptr;
   const gge_mx_tensor* B = mx(a[1], false);
@@ -217,7 +218,8 @@ PyObject* gemm_mx(PyObject*, PyObject* const* a, Py_ssize_t n) {
   void* wp = ws->data_ptr();
   const size_t wn = static_cast<size_t>(ws->numel());
   gge_stream_t st = stream(dev);
-  GGE_CALL(gge_gemm_mx(&g, wp, wn, st));
+  const bool dact = PyObject_IsTrue(a[13]) == 1;
+  GGE_CALL(dact ? gge_gemm_mx_dact(&g, wp, wn, st) : gge_gemm_mx(&g, wp, wn, st));
   END_HANDLE_TH_ERRORS
 }
 

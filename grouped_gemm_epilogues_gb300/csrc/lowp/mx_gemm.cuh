@@ -263,7 +263,7 @@ __device__ __forceinline__ void mx_send(const MxParams& mp, uint32_t tbase, int3
 }
 
 __device__ __forceinline__ float mx_alpha(const MxParams& mp) {
-  float alpha = mp.p.alpha_dev ? *mp.p.alpha_dev : mp.p.alpha;
+  float alpha = mp.p.dact ? 1.f : (mp.p.alpha_dev ? *mp.p.alpha_dev : mp.p.alpha);
   if (mp.tscale_a != nullptr) alpha *= *mp.tscale_a;
   if (mp.tscale_b != nullptr) alpha *= *mp.tscale_b;
   return alpha;
@@ -306,8 +306,10 @@ __device__ __forceinline__ void mx_reduce(const MxParams& mp, const Shared& sh, 
         for (int j = 0; j < 4; ++j) sum[4 * q + j] = r == 0 ? f[j] : sum[4 * q + j] + f[j];
       }
     }
+    // (the backward epilogue takes the accumulator as it is)
+    const float scale = p.dact ? alpha : 1.f;
 #pragma unroll
-    for (int j = 0; j < 32; ++j) own[j] = __float_as_uint(sum[j]);
+    for (int j = 0; j < 32; ++j) own[j] = __float_as_uint(sum[j] * scale);
     epilogue_chunk_t<TR>(p, own, row_base, rows_valid, col0, tc.batch, alpha, beta, creg, stg);
   }
 }
@@ -389,6 +391,10 @@ __device__ __forceinline__ void mx_epilogue_role(const MxParams& mp, const Share
                              out_ptr(p.d, p.ldd, p.sbd, p.d_dtype, row_base, col0, tc.batch, p),
                              2 * p.ldd, rows_valid, min(32, p.N - col0), false);
         } else {
+          if (p.dact) {  // (it takes the accumulator as it is)
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * alpha);
+          }
           epilogue_chunk_t<TR>(p, v, row_base, rows_valid, col0, tc.batch, alpha, beta, ccur, stg);
         }
       }

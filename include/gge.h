@@ -395,6 +395,13 @@ typedef struct gge_gemm_mx_args {
 gge_status gge_gemm_mx(const gge_gemm_mx_args* args, void* workspace, size_t workspace_bytes,
                        gge_stream_t stream);
 
+/* The backward activation epilogue on microscaled operands (as gge_gemm_dact):
+ * with S = tA * tB * sum_k (a_k sa_k) (b_k sb_k) the incoming gradient and C
+ * (required) the pre-activation x, D = act'(x) * S (required) and PostAct =
+ * act(x) (optional); act is not NONE, alpha and beta are not used. */
+gge_status gge_gemm_mx_dact(const gge_gemm_mx_args* args, void* workspace, size_t workspace_bytes,
+                            gge_stream_t stream);
+
 /*
  * RMS norm with the residual's addition:
  *   h = round(x + residual)  (h = x without one)

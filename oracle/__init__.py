@@ -30,10 +30,13 @@ Modules:
   fastdivmod  -- FastDivmod exactly as ``quack/fast_math.py`` builds it, in
                  Python integers.
   tiles       -- the set of output tiles a schedule must cover exactly once.
+  lowp        -- microscaled formats (quantisation, layout, decoding), RMS norm
+                 and its backward.
 
-Every function is pinned by ``tests/test_oracle_pins.py`` against values fixed
+Every function is pinned by ``tests/test_oracle_pins.py`` (lowp:
+``tests/test_lowp_oracle.py``) against values fixed
 by mathematics or by independent libraries.  No function here is
 "parity unpinned".
 """
 
-from . import formats, activations, gemm, fastdivmod, tiles  # noqa: F401
+from . import formats, activations, gemm, fastdivmod, tiles, lowp  # noqa: F401
