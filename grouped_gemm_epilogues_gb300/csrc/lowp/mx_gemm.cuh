@@ -97,9 +97,10 @@ struct MxCfg {
   static constexpr int kThreads = 10 * 32;
   // TMEM columns: the scales at the end, the second accumulator as far up as it goes
   static constexpr int kSfCols = 4 * kGroups * (1 + kBTiles);
-  static constexpr int kTmemCols = BN == 256 ? 512 : (BN == 128 ? 512 : 256);
+  static constexpr int kTmemCols = BN == 64 ? 256 : 512;
   static constexpr int kSfBase = kTmemCols - 48;
-  static constexpr int kAcc1 = BN == 256 ? 208 : BN;
+  static constexpr bool kOverlap = BN == 256;  // the accumulators share columns
+  static constexpr int kAcc1 = kOverlap ? 208 : BN;
   static_assert(kSfCols <= 48 && kAcc1 + BN <= kSfBase, "TMEM columns");
   static_assert(BN == 256 || BN == 128 || BN == 64, "tile widths");
 };
@@ -136,10 +137,16 @@ __device__ __forceinline__ void mx_mma_role(const MxParams& mp, const Shared& sh
   const uint32_t sfb_t = sfa_t + 4 * Cfg::kGroups;
   int i = 0;
   for (int32_t t = unit; t < p.num_tiles; t += units, ++i) {
-    // the shared columns of the tile before (and all of the one before that) are read
-    if (i > 0 && !wait_phase<CG == 2>(sh.tempty, static_cast<uint32_t>(i - 1) & 1u, p, sh, 2, t)) return;
-    ptx::tc_fence_after();
     const uint32_t acc = static_cast<uint32_t>(i) & 1u;
+    if (Cfg::kOverlap) {
+      // the columns shared with the tile before are read (and all of the one before that)
+      if (i > 0 && !wait_phase<CG == 2>(sh.tempty, static_cast<uint32_t>(i - 1) & 1u, p, sh, 2, t)) return;
+    } else if (i > 1) {
+      // the accumulator's last tile is read.  (A barrier each: a warp may read the next
+      // tile, in the other accumulator, before its neighbours have read this one.)
+      if (!wait_phase<CG == 2>(sh.tempty + 8 * acc, static_cast<uint32_t>((i >> 1) - 1) & 1u, p, sh, 2, t)) return;
+    }
+    ptx::tc_fence_after();
     const uint32_t d_tmem = tmem_base + acc * Cfg::kAcc1;
     // 64-wide tiles: an odd one starts in the middle of a 128-row scale tile
     uint32_t sfb = sfb_t;
@@ -340,7 +347,7 @@ __device__ __forceinline__ void mx_epilogue_role(const MxParams& mp, const Share
     // this warp's chunks are half, half + 2, ...; the first accumulator's walk starts at
     // its last pair, the second one's at its first: the columns both own.  A split
     // tile's slices then rotate on, so that they finish different chunks last.
-    const int first = (BN == 256 && acc == 0) ? kMine - 1 : 0;
+    const int first = (Cfg::kOverlap && acc == 0) ? kMine - 1 : 0;
     CRegs cnext = {};
     if (mp.splits == 1 && has_c && tc.n0 + (half + 2 * first) * 32 < p.N)
       load_c_chunk<TR>(p, row, tc.n0 + (half + 2 * first) * 32, tc.batch, cnext);
@@ -372,14 +379,16 @@ __device__ __forceinline__ void mx_epilogue_role(const MxParams& mp, const Share
 #pragma unroll
         for (int j = 0; j < 32; ++j) v[j] = 0u;
       }
-      if (n == 0) {
+      if (n == (Cfg::kOverlap ? 0 : kMine - 1)) {
         // the columns the next tile's accumulator shares are read (and, in program
-        // order, all of the tile before this one): its MMAs may start
+        // order, all of the tile before this one): its MMAs may start.  Without shared
+        // columns: this accumulator is read
         ptx::tc_fence_before();
         __syncwarp();
+        const uint32_t bar = sh.tempty + (Cfg::kOverlap ? 0u : 8u * acc);
         if (lane == 0) {
-          if (CG == 1) ptx::mbar_arrive(sh.tempty);
-          else ptx::mbar_arrive_remote(ptx::mapa(sh.tempty, 0));
+          if (CG == 1) ptx::mbar_arrive(bar);
+          else ptx::mbar_arrive_remote(ptx::mapa(bar, 0));
         }
       }
       if (rows_valid > 0 && col0 < p.N) {
@@ -419,7 +428,7 @@ __global__ void __launch_bounds__(MxCfg<BN, CG, FMT>::kThreads, 1)
   // split K: the other ranks' chunks of what this CTA owns
   const uint32_t red = out_stage + Cfg::kEpiWarps * p.out_stage_bytes;
   uint8_t* ctrl = base_ptr + S * Cfg::kStageBytes + Cfg::kEpiWarps * p.out_stage_bytes + mp.reduce_bytes;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(ctrl + 8 * (2 * kMaxStages + 4));
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(ctrl + 8 * (2 * kMaxStages + 5));
   int32_t* abort_flag = reinterpret_cast<int32_t*>(tmem_slot + 1);
 
   Shared sh = {};
@@ -427,7 +436,7 @@ __global__ void __launch_bounds__(MxCfg<BN, CG, FMT>::kThreads, 1)
   sh.empty = sh.full + 8 * kMaxStages;
   sh.tfull = sh.empty + 8 * kMaxStages;
   sh.tempty = sh.tfull + 16;
-  const uint32_t drain_bar = sh.tempty + 8;
+  const uint32_t drain_bar = sh.tempty + 16;
   sh.abort = abort_flag;
 
   const int warp = threadIdx.x >> 5;
@@ -447,6 +456,7 @@ __global__ void __launch_bounds__(MxCfg<BN, CG, FMT>::kThreads, 1)
     ptx::mbar_init(sh.tfull, 1);
     ptx::mbar_init(sh.tfull + 8, 1);
     ptx::mbar_init(sh.tempty, Cfg::kEpiWarps * CG);
+    ptx::mbar_init(sh.tempty + 8, Cfg::kEpiWarps * CG);
     ptx::mbar_init(drain_bar, 1);
     *abort_flag = 0;
     ptx::fence_barrier_init();

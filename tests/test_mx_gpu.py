@@ -378,3 +378,19 @@ def test_python_refusals():
         gge.mx_empty(4, 4, "fp6", device=DEV)
     with pytest.raises(ValueError, match="fp32"):
         gge.MxTensor(q.codes, q.scales, "mxfp4", 64, 128, tensor_scale=torch.ones(2, device=DEV))
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("tile_n", [256, 128, 64])
+@pytest.mark.parametrize("k", [64, 500, 1300])
+def test_many_short_tiles_a_cta(fmt, tile_n, k):
+    """Many tiles of a short K on few CTAs, so that every wait between the accumulators is
+    the one that decides: the outputs equal those of one tile a CTA bit for bit."""
+    (A, _), (B, _) = _operands(500, 1496, k, fmt, 31)
+    one = torch.empty(500, 1496, dtype=torch.bfloat16, device=DEV)
+    gge.gge_gemm_mx(A, B, D=one, config=gge.make_config(tile_n=tile_n, flags=32))
+    for ctas in (2, 4, 10):
+        for _ in range(4):
+            D = torch.full_like(one, float("nan"))
+            gge.gge_gemm_mx(A, B, D=D, config=gge.make_config(tile_n=tile_n, num_ctas=ctas))
+            assert torch.equal(D, one)
