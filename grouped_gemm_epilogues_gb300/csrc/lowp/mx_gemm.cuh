@@ -227,6 +227,10 @@ __device__ __forceinline__ void mx_load_role(const MxParams& mp, const Shared& s
   }
 }
 
+// The two halves of a cluster barrier.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
+
 // A split tile's 32 x 32 accumulator chunks (lane quadrant x 32 columns) are dealt
 // out to the cluster's CTAs in order; chunk `n` of 4 BN / 32 belongs to rank n S /
 // (4 BN / 32).
@@ -353,10 +357,14 @@ __device__ __forceinline__ void mx_epilogue_role(const MxParams& mp, const Share
       load_c_chunk<TR>(p, row, tc.n0 + (half + 2 * first) * 32, tc.batch, cnext);
     // (polled: the next tile's MMAs wait for this one's first chunks)
     const bool ok = wait_phase<CG == 2>(sh.tfull + 8 * acc, acc_phase, p, sh, 3, t);
-    if (!__all_sync(0xffffffffu, ok)) return;
+    if (!__all_sync(0xffffffffu, ok)) {
+      if (CG == 1 && mp.splits > 1) cluster_wait();
+      return;
+    }
     ptx::tc_fence_after();
     const uint32_t tbase = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + acc * Cfg::kAcc1;
     if (CG == 1 && mp.splits > 1) {  // (one tile a cluster: mx_reduce finishes it)
+      cluster_wait();  // every CTA of the cluster runs: their shared memory may be written
       mx_send<BN>(mp, tbase, tc.n0, quad, half, slice, red);
       return;
     }
@@ -479,7 +487,8 @@ __global__ void __launch_bounds__(MxCfg<BN, CG, FMT>::kThreads, 1)
   }
   ptx::griddep_wait();
   __syncthreads();
-  if (ctas > 1) ptx::cluster_sync();
+  if (CG == 2) ptx::cluster_sync();
+  if (CG == 1 && mp.splits > 1) cluster_arrive();  // (waited for before the first remote store)
   ptx::tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
 
@@ -493,6 +502,16 @@ __global__ void __launch_bounds__(MxCfg<BN, CG, FMT>::kThreads, 1)
       mx_load_role<BN, CG, FMT>(mp, sh, &tmA, &tmB, &tmSA, &tmSB, base, rank, ks, unit, units);
   }
   __syncwarp();
+  if (CG == 1 && mp.splits > 1) {
+    if (warp >= Cfg::kEpiWarps) cluster_wait();
+    cluster_arrive();
+    cluster_wait();  // every rank's chunks are where they belong
+    if (warp < Cfg::kEpiWarps && !*abort_flag) {
+      ptx::tc_fence_after();
+      mx_reduce<BN, FMT, TR>(mp, sh, tmem_base, slice, red, out_stage + warp * p.out_stage_bytes, unit);
+      ptx::tc_fence_before();
+    }
+  }
 
   __syncthreads();
   // every MMA and scale copy this CTA issued has finished before TMEM is freed
@@ -505,13 +524,7 @@ __global__ void __launch_bounds__(MxCfg<BN, CG, FMT>::kThreads, 1)
     wait_phase<CG == 2>(drain_bar, 0, p, sh, 6, -1);
   }
   __syncthreads();
-  if (ctas > 1) ptx::cluster_sync();
-  if (CG == 1 && mp.splits > 1 && warp < Cfg::kEpiWarps && !*abort_flag) {
-    ptx::tc_fence_after();
-    mx_reduce<BN, FMT, TR>(mp, sh, tmem_base, slice, red, out_stage + warp * p.out_stage_bytes, unit);
-    ptx::tc_fence_before();
-  }
-  if (CG == 1 && mp.splits > 1) __syncthreads();
+  if (CG == 2) ptx::cluster_sync();
   if (*abort_flag) {
     // let copies and MMAs that were in flight land before the memory goes away
     const uint64_t t0 = ptx::globaltimer();

@@ -475,10 +475,12 @@ __global__ void __launch_bounds__(kMaxThreads)
   for (int s = 0; s + 1 < D; ++s) start(s);
   const float inv_cols = 1.f / static_cast<float>(cols);
   int slot = 0, flip = 0;
+  float inv_next = row < rows ? p.inv[row] : 0.f;
   for (; row < rows; row += step) {
     if constexpr (!AL) __syncwarp();
     start((slot + D - 1) % D);
-    const float inv = p.inv[row];
+    const float inv = inv_next;
+    if (row + step < rows) inv_next = p.inv[row + step];
     const float2 inv2 = make_float2(inv, inv);
     cp_async_wait<D - 1>();
     if constexpr (!AL) __syncwarp();
