@@ -399,8 +399,8 @@ gge_status gge_mx_quantize(const gge_tensor* x, const gge_mx_tensor* q, const gg
                   ? rows_aligned(*x) && (values == nullptr || rows_aligned(*values))
                   : aligned16(x->ptr) && x->stride_col * elem_bytes(x->dtype) % 16 == 0 &&
                         (x->batch <= 1 || x->stride_batch * elem_bytes(x->dtype) % 16 == 0);
-  // (a transposed view takes the columns' tiles as a second grid dimension)
-  if (x->cols != 1 && x->stride_col != 1 && x->cols > 65535 * int64_t(128)) return GGE_ERR_UNSUPPORTED;
+  // (a transposed view takes the rows' tiles as a second grid dimension)
+  if (x->cols != 1 && x->stride_col != 1 && x->rows > 65535 * int64_t(64)) return GGE_ERR_UNSUPPORTED;
   return launched(lowp::launch_quantize(p, reinterpret_cast<cudaStream_t>(stream)));
 }
 

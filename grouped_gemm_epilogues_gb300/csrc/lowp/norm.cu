@@ -15,7 +15,6 @@
 // registers and written, so every value is read once.
 #include <atomic>
 
-#include "../gge_launch.h"
 #include "lowp_launch.h"
 #include "rows.cuh"
 
@@ -348,21 +347,6 @@ RowShape row_shape(int64_t chunks, bool one) {
   while (s.tpr < kMaxThreads && static_cast<int64_t>(s.tpr) * (one ? 1 : 2) < chunks) s.tpr = s.tpr == 32 ? 128 : s.tpr * 2;
   if (s.tpr < chunks) s.c = 2;
   return s;
-}
-
-// Opt in to `smem` bytes of shared memory (a per-device attribute of the kernel).
-template <typename... A>
-cudaError_t allow_smem(void (*kern)(A...), std::atomic<size_t>* set, size_t smem) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= 64 || set[dev].load() < smem) {
-    RelaxedCaptureMode relaxed;
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-    if (e != cudaSuccess) return e;
-    if (dev >= 0 && dev < 64) set[dev].store(smem);
-  }
-  return cudaSuccess;
 }
 
 template <typename T, int C, int FMT, bool AL>

@@ -5,6 +5,8 @@
 // row-major matrix (stride_row 1), as the weight-gradient products need it: a
 // tile then goes through shared memory.  Both forms read the source once and
 // are bound by memory.
+#include <atomic>
+
 #include "lowp_launch.h"
 #include "rows.cuh"
 
@@ -25,18 +27,25 @@ __device__ __forceinline__ QuantOut quant_out(const QuantPtrs& q, int64_t batch)
 }
 
 // A block's eight warps cover 256 columns each: `wx` of them side by side, the
-// others below, and kRowsAWarp rows a warp, whose loads are in flight together.
-constexpr int kRowsAWarp = 4;
+// others below, and U rows a warp, whose loads are in flight together.  Four rows
+// where they start on 16-byte boundaries (8192 x 8192 to nvfp4 54 us; 60 with two, 77
+// with one), two elsewhere, where a row takes more registers (4000 x 4001 25.7 us; 29.7
+// with four, 27.3 with one).
+template <bool AL>
+constexpr int rows_a_warp() {
+  return AL ? 4 : 2;
+}
 
 struct RowTiles {
   int32_t wx;         // warps along the columns: 1, 2, 4 or 8
   int32_t across;     // blocks along the columns
+  int32_t rows;       // rows a warp
 };
 
-__host__ __device__ __forceinline__ int64_t rows_a_block(const RowTiles& r) { return 8 / r.wx * kRowsAWarp; }
+__host__ __device__ __forceinline__ int64_t rows_a_block(const RowTiles& r) { return 8 / r.wx * r.rows; }
 
-RowTiles row_tiles(int64_t span) {
-  RowTiles r{1, 1};
+RowTiles row_tiles(int64_t span, bool aligned) {
+  RowTiles r{1, 1, aligned ? rows_a_warp<true>() : rows_a_warp<false>()};
   while (r.wx < 8 && r.wx * 256 < span) r.wx *= 2;
   r.across = static_cast<int32_t>((span + r.wx * 256 - 1) / (r.wx * 256));
   return r;
@@ -52,7 +61,7 @@ __device__ __forceinline__ void warp_place(const RowTiles& r, int64_t& row, int3
   const int warp = threadIdx.x >> 5;
   const uint32_t down = blockIdx.x / static_cast<uint32_t>(r.across);
   const uint32_t over = blockIdx.x - down * static_cast<uint32_t>(r.across);
-  row = down * rows_a_block(r) + warp / r.wx * kRowsAWarp;
+  row = down * rows_a_block(r) + warp / r.wx * r.rows;
   col = (static_cast<int32_t>(over) * r.wx + warp % r.wx) * 256 + (threadIdx.x & 31) * 8;
 }
 
@@ -61,7 +70,7 @@ __device__ __forceinline__ void warp_place(const RowTiles& r, int64_t& row, int3
 template <typename T, int FMT, bool AL>
 __global__ void __launch_bounds__(256)
     quantize_rows_kernel(const __grid_constant__ QuantParams p, RowTiles tiles) {
-  constexpr int B = Fmt<FMT>::kBlock;
+  constexpr int B = Fmt<FMT>::kBlock, U = rows_a_warp<AL>();
   ptx::griddep_launch_dependents();
   const int64_t batch = blockIdx.y;
   const QuantOut q = quant_out(p.q, batch);
@@ -71,19 +80,19 @@ __global__ void __launch_bounds__(256)
   int32_t col;
   warp_place(tiles, row0, col);
   if (col - (threadIdx.x & 31) * 8 >= cols) return;
-  const int32_t rows = static_cast<int32_t>(min(p.rows - row0, static_cast<int64_t>(kRowsAWarp)));
+  const int32_t rows = static_cast<int32_t>(min(p.rows - row0, static_cast<int64_t>(U)));
   const T* src = x + row0 * p.stride_row;
   uint8_t* codes = q.codes + row0 * q.ld + static_cast<int64_t>(col) * Fmt<FMT>::kBits / 8;
-  // (a warp's rows share a scale tile's 32-row stretch: kRowsAWarp divides 32)
+  // (a warp's rows share a scale tile's 32-row stretch: U divides 32)
   uint8_t* scales = q.scales + scale_word(row0, col / Fmt<FMT>::kGroup, q.kgroups);
   const bool word = holds_word<FMT>() && col < q.kgroups * Fmt<FMT>::kGroup;
   const bool code = col < ((cols + 31) & ~31);
   const bool past = col >= (cols + B - 1) / B * B;
   ptx::griddep_wait();
   const float tscale = (FMT == FMT_NVFP4 && q.tensor_scale) ? *q.tensor_scale : 1.f;
-  Raw8<T> raw[kRowsAWarp];
+  Raw8<T> raw[U];
 #pragma unroll
-  for (int u = 0; u < kRowsAWarp; ++u) {
+  for (int u = 0; u < U; ++u) {
 #pragma unroll
     for (int j = 0; j < WarpRow<T>::kPieces; ++j) raw[u].w[j] = make_uint4(0u, 0u, 0u, 0u);
     if (u < rows && col < cols) {
@@ -93,7 +102,7 @@ __global__ void __launch_bounds__(256)
     }
   }
 #pragma unroll
-  for (int u = 0; u < kRowsAWarp; ++u) {
+  for (int u = 0; u < U; ++u) {
     if (u >= rows) break;  // (the whole warp)
     float2 v[4];
     widen(raw[u], v);
@@ -191,15 +200,19 @@ __global__ void __launch_bounds__(256, 4) quantize_cols_kernel(const __grid_cons
   constexpr int V = 4 / sizeof(T);         // rows a word holds
   constexpr int kRows = kTWords * V;       // rows of the tile
   constexpr int kBytes = kTCols / Fmt<FMT>::kBlock;  // scale bytes of a row of the tile
-  __shared__ uint32_t tile[kTCols * kTPitch];
-  __shared__ uint32_t words[kRows * kBytes / 4];
+  constexpr int kCodes = kTCols * Fmt<FMT>::kBits / 8;  // bytes of codes of a row of the tile
+  constexpr int kPiecesARow = kCodes / 16;
+  extern __shared__ __align__(16) uint8_t shared[];
+  uint32_t* tile = reinterpret_cast<uint32_t*>(shared);                    // [column][word]
+  uint32_t* words = tile + kTCols * kTPitch;                               // scale bytes
+  uint4* pieces = reinterpret_cast<uint4*>(words + kRows * kBytes / 4);    // codes, [row][kPiecesARow + 1]
   ptx::griddep_launch_dependents();
   const int64_t batch = blockIdx.z;
   const QuantOut q = quant_out(p.q, batch);
   const T* x = static_cast<const T*>(p.x) + batch * p.stride_batch;
-  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * kRows;
+  const int64_t row0 = static_cast<int64_t>(blockIdx.y) * kRows;
   const int32_t rows = static_cast<int32_t>(p.rows), cols = static_cast<int32_t>(p.cols);
-  const int32_t col0 = blockIdx.y * kTCols;
+  const int32_t col0 = blockIdx.x * kTCols;
   ptx::griddep_wait();
   const float tscale = (FMT == FMT_NVFP4 && q.tensor_scale) ? *q.tensor_scale : 1.f;
   {
@@ -239,12 +252,9 @@ __global__ void __launch_bounds__(256, 4) quantize_cols_kernel(const __grid_cons
                             q.values != nullptr);
 #pragma unroll
   for (int h = 0; h < V; ++h) {
-    const int64_t row = row0 + at * V + h;
-    if (row < p.rows && col < ((cols + 31) & ~31)) {
-      uint4* dst = reinterpret_cast<uint4*>(q.codes + row * q.ld + static_cast<int64_t>(col) * Fmt<FMT>::kBits / 8);
-      dst[0] = make_uint4(w[h][0], w[h][1], w[h][2], w[h][3]);
-      if constexpr (FMT == FMT_MXFP8) dst[1] = make_uint4(w[h][4], w[h][5], w[h][6], w[h][7]);
-    }
+    uint4* dst = pieces + (at * V + h) * (kPiecesARow + 1) + part * (kPiecesARow / 4);
+    dst[0] = make_uint4(w[h][0], w[h][1], w[h][2], w[h][3]);
+    if constexpr (FMT == FMT_MXFP8) dst[1] = make_uint4(w[h][4], w[h][5], w[h][6], w[h][7]);
   }
   if (q.values != nullptr) {  // the values take the source's place in the tile
 #pragma unroll
@@ -257,9 +267,39 @@ __global__ void __launch_bounds__(256, 4) quantize_cols_kernel(const __grid_cons
     if (row0 + rr < p.rows && kg < q.kgroups)
       *reinterpret_cast<uint32_t*>(q.scales + scale_word(row0 + rr, kg, q.kgroups)) = words[rr * (kBytes / 4) + kw];
   }
+  // whole lines of codes
+  for (int i = threadIdx.x; i < kRows * kPiecesARow; i += 256) {
+    const int rr = i / kPiecesARow, piece = i % kPiecesARow;
+    const int32_t c = col0 + piece * (128 / Fmt<FMT>::kBits);
+    if (row0 + rr < p.rows && c < ((cols + 31) & ~31))
+      *reinterpret_cast<uint4*>(q.codes + (row0 + rr) * q.ld + static_cast<int64_t>(c) * Fmt<FMT>::kBits / 8) =
+          pieces[rr * (kPiecesARow + 1) + piece];
+  }
   if (q.values == nullptr) return;
-  // a warp a word of rows, one column a lane: whole lines at any alignment
+  // values: a warp a word of rows.  Two columns a lane where a row's pairs start on four
+  // bytes, else one: whole lines at any alignment
   const int lane = threadIdx.x & 31;
+  if (V == 2 && q.ldv % 2 == 0 && (reinterpret_cast<uintptr_t>(q.values) & 3u) == 0) {
+    uint16_t* values = static_cast<uint16_t*>(q.values);
+    for (int r = threadIdx.x >> 5; r < kTWords; r += 8) {
+      const int64_t row = row0 + r * V;
+      if (row >= p.rows) break;
+#pragma unroll
+      for (int c = lane * 2; c < kTCols; c += 64) {
+        if (col0 + c >= cols) break;
+        const uint32_t a = tile[c * kTPitch + r], b = tile[(c + 1) * kTPitch + r];
+        uint16_t* out = values + row * q.ldv + col0 + c;
+        if (col0 + c + 1 < cols) {
+          *reinterpret_cast<uint32_t*>(out) = __byte_perm(a, b, 0x5410);
+          if (row + 1 < p.rows) *reinterpret_cast<uint32_t*>(out + q.ldv) = __byte_perm(a, b, 0x7632);
+        } else {
+          out[0] = static_cast<uint16_t>(a);
+          if (row + 1 < p.rows) out[q.ldv] = static_cast<uint16_t>(a >> 16);
+        }
+      }
+    }
+    return;
+  }
   for (int r = threadIdx.x >> 5; r < kTWords; r += 8) {
     const int64_t row = row0 + r * V;
     if (row >= p.rows) break;
@@ -282,18 +322,23 @@ template <typename T, int FMT, bool AL>
 cudaError_t launch_quantize_t(const QuantParams& p, cudaStream_t st) {
   const int64_t span = p.q.kgroups * Fmt<FMT>::kGroup;
   if (p.stride_col == 1 || p.cols == 1) {
-    const RowTiles tiles = row_tiles(span);
+    const RowTiles tiles = row_tiles(span, AL);
     return launch_pdl(quantize_rows_kernel<T, FMT, AL>, row_grid(tiles, p.rows, p.batch), dim3(256), 0, st,
                       p, tiles);
   }
   constexpr int kRows = kTWords * (4 / sizeof(T));
+  constexpr size_t smem = kTCols * kTPitch * 4 + kRows * (kTCols / Fmt<FMT>::kBlock) +
+                          kRows * (kTCols * Fmt<FMT>::kBits / 8 + 16);
+  static std::atomic<size_t> set[2][64];
   const bool half = p.q.values != nullptr && p.q.v_dtype == 1;
-  return launch_pdl(half ? quantize_cols_kernel<T, FMT, AL, __half>
-                         : quantize_cols_kernel<T, FMT, AL, __nv_bfloat16>,
-                    dim3(static_cast<unsigned>((p.rows + kRows - 1) / kRows),
-                         static_cast<unsigned>((span + kTCols - 1) / kTCols),
+  const auto kern = half ? quantize_cols_kernel<T, FMT, AL, __half> : quantize_cols_kernel<T, FMT, AL, __nv_bfloat16>;
+  const cudaError_t e = allow_smem(kern, set[half], smem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kern,
+                    dim3(static_cast<unsigned>((span + kTCols - 1) / kTCols),
+                         static_cast<unsigned>((p.rows + kRows - 1) / kRows),
                          static_cast<unsigned>(p.batch)),
-                    dim3(256), 0, st, p);
+                    dim3(256), smem, st, p);
 }
 
 template <typename T>
@@ -323,10 +368,11 @@ __global__ void __launch_bounds__(256)
   int64_t row0;
   int32_t col;
   warp_place(tiles, row0, col);
-  uint2 w[kRowsAWarp];
-  float unit[kRowsAWarp];
+  constexpr int U = rows_a_warp<AL>();
+  uint2 w[U];
+  float unit[U];
 #pragma unroll
-  for (int u = 0; u < kRowsAWarp; ++u) {
+  for (int u = 0; u < U; ++u) {
     const int64_t row = row0 + u;
     w[u] = make_uint2(0u, 0u);
     unit[u] = 0.f;
@@ -338,7 +384,7 @@ __global__ void __launch_bounds__(256)
     unit[u] = scale_value<FMT>(scales[scale_word(row, block >> 2, p.kgroups) + (block & 3)]);
   }
 #pragma unroll
-  for (int u = 0; u < kRowsAWarp; ++u) {
+  for (int u = 0; u < U; ++u) {
     if (row0 + u >= p.rows) break;
     float2 v[4];
     code_values<FMT>(w[u], unit[u], tscale, v);
@@ -373,7 +419,7 @@ cudaError_t launch_quantize(const QuantParams& p, cudaStream_t st) {
 }
 
 cudaError_t launch_dequantize(const DequantParams& p, cudaStream_t st) {
-  const RowTiles tiles = row_tiles(p.cols);
+  const RowTiles tiles = row_tiles(p.cols, p.aligned != 0);
   const dim3 grid = row_grid(tiles, p.rows, p.batch);
   switch (p.format) {
     case FMT_MXFP8: return launch_pdl(p.aligned ? dequantize_kernel<FMT_MXFP8, true> : dequantize_kernel<FMT_MXFP8, false>, grid,
