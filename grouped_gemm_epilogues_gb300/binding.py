@@ -11,7 +11,6 @@ raises.
 import ctypes
 import importlib.util
 import os
-import struct
 import threading
 
 import torch
@@ -527,47 +526,37 @@ def _mx_scale_bytes(fmt, rows, cols):
 class MxTensor:
     """A microscaled matrix (gge_mx_tensor): codes (rows, bytes) or (batch, rows, bytes)
     uint8, scales a contiguous uint8 tensor of gge_mx_scale_bytes a batch, tensor_scale None
-    or a one-element fp32 tensor on the device (nvfp4).  ``c`` holds the C struct as bytes."""
+    or a one-element fp32 tensor (nvfp4), all on one CUDA device.  ``c`` holds the C struct
+    as bytes."""
 
-    __slots__ = ("format", "rows", "cols", "batch", "tensor_scale", "device", "c", "_codes",
-                 "_scales", "_buffer")
+    __slots__ = ("format", "tensor_scale", "device", "c", "_codes", "_scales", "_buffer")
 
     def __init__(self, codes, scales, format, rows, cols, tensor_scale=None):
-        fmt = MX_FORMAT[format]
-        shape, stride = codes.shape, codes.stride()
-        if len(shape) == 2:
-            batch, step = 1, 0
-        elif len(shape) == 3:
-            batch, step = shape[0], stride[0]
-        else:
-            raise ValueError("MxTensor: codes are 2-D or 3-D (batch first)")
-        if codes.dtype is not torch.uint8 or scales.dtype is not torch.uint8:
-            raise TypeError("MxTensor: codes and scales are uint8 tensors")
-        if shape[-2] != rows or shape[-1] != _mx_row_bytes(fmt, cols) or \
-                (stride[-1] != 1 and codes.numel() > 0):
-            raise ValueError("MxTensor: codes do not match rows, cols and format")
-        per = _mx_scale_bytes(fmt, rows, cols)
-        if scales.numel() != batch * per or not scales.is_contiguous():
-            raise ValueError("MxTensor: scales do not match rows, cols and format")
-        self.device = device = codes.device
-        t = 0
-        if tensor_scale is not None:
-            if tensor_scale.dtype is not torch.float32 or tensor_scale.numel() != 1:
-                raise ValueError("MxTensor: tensor_scale is one fp32 value")
-            if tensor_scale.device != device:
-                raise ValueError("MxTensor: tensors on different devices")
-            t = tensor_scale.data_ptr()
-        if scales.device != device:
-            raise ValueError("MxTensor: tensors on different devices")
-        self.format, self.rows, self.cols, self.batch = format, rows, cols, batch
-        self.tensor_scale, self._codes, self._scales, self._buffer = tensor_scale, codes, scales, None
-        self.c = _MX_STRUCT.pack(codes.data_ptr(), scales.data_ptr(), t, fmt, 0, rows, cols, batch,
-                                 stride[-2], step, per)
+        self.c = (_marshal or _load_marshal()).mx_wrap(codes, scales, MX_FORMAT[format], rows, cols,
+                                                       tensor_scale)
+        self.device = codes.device
+        self.format, self.tensor_scale = format, tensor_scale
+        self._codes, self._scales = codes, scales
+
+    def _struct(self):
+        return GgeMxTensor.from_buffer_copy(self.c)
+
+    @property
+    def rows(self):
+        return self._struct().rows
+
+    @property
+    def cols(self):
+        return self._struct().cols
+
+    @property
+    def batch(self):
+        return self._struct().batch
 
     @property
     def codes(self):
         if self._codes is None:   # mx_empty: a view of its one buffer, made when asked for
-            c = GgeMxTensor.from_buffer_copy(self.c)
+            c = self._struct()
             row = c.stride_row
             if c.stride_batch:
                 self._codes = self._buffer.as_strided((c.batch, c.rows, row), (c.stride_batch, row, 1))
@@ -578,7 +567,7 @@ class MxTensor:
     @property
     def scales(self):
         if self._scales is None:
-            c = GgeMxTensor.from_buffer_copy(self.c)
+            c = self._struct()
             self._scales = self._buffer.as_strided((c.batch * c.scale_stride_batch,), (1,),
                                                    c.scales - c.codes)
         return self._scales
@@ -601,12 +590,9 @@ def mx_empty(rows, cols, format, device=None, batch=None, tensor_scale=None):
     q._buffer, q.c = (_marshal or _load_marshal()).mx_alloc(
         start + b * per, start, device.index, fmt, rows, cols, 0 if batch is None else batch, row, per,
         tensor_scale)
-    q.device, q.format, q.rows, q.cols, q.batch, q.tensor_scale = device, format, rows, cols, b, tensor_scale
+    q.device, q.format, q.tensor_scale = device, format, tensor_scale
     q._codes = q._scales = None
     return q
-
-
-_MX_STRUCT = struct.Struct("=QQQiiqqqqqq")   # gge_mx_tensor
 
 
 def _shared(device, need):

@@ -150,6 +150,47 @@ PyObject* mx_alloc(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+// mx_wrap(codes, scales, format, rows, cols, tensor_scale) -> struct bytes
+PyObject* mx_wrap(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (!count(n, 6)) return nullptr;
+  const at::Tensor* codes = tensor(a[0], "codes", -1);
+  if (codes == nullptr) return nullptr;
+  const int dev = static_cast<int>(codes->get_device());
+  const at::Tensor* scales = tensor(a[1], "scales", dev);
+  if (scales == nullptr) return nullptr;
+  const int format = static_cast<int>(PyLong_AsLong(a[2]));
+  const int64_t rows = PyLong_AsLongLong(a[3]), cols = PyLong_AsLongLong(a[4]);
+  if (PyErr_Occurred()) return nullptr;
+  void* scale = nullptr;
+  if (vector(a[5], "tensor_scale", dev, true, 1, at::kFloat, &scale) < 0) return nullptr;
+  if (codes->scalar_type() != at::kByte || scales->scalar_type() != at::kByte) {
+    PyErr_SetString(PyExc_TypeError, "MxTensor: codes and scales are uint8 tensors");
+    return nullptr;
+  }
+  const int64_t dim = codes->dim();
+  if (dim != 2 && dim != 3) {
+    PyErr_SetString(PyExc_ValueError, "MxTensor: codes are 2-D or 3-D (batch first)");
+    return nullptr;
+  }
+  const int b = dim == 3 ? 1 : 0;
+  const int64_t batch = b ? codes->size(0) : 1;
+  const int64_t per = static_cast<int64_t>(gge_mx_scale_bytes(format, rows, cols));
+  if (codes->size(b) != rows || codes->size(b + 1) != static_cast<int64_t>(gge_mx_row_bytes(format, cols)) ||
+      (codes->stride(b + 1) != 1 && codes->numel() > 0)) {
+    PyErr_SetString(PyExc_ValueError, "MxTensor: codes do not match rows, cols and format");
+    return nullptr;
+  }
+  if (scales->numel() != batch * per || !scales->is_contiguous()) {
+    PyErr_SetString(PyExc_ValueError, "MxTensor: scales do not match rows, cols and format");
+    return nullptr;
+  }
+  const gge_mx_tensor m{codes->data_ptr(), scales->data_ptr(), static_cast<const float*>(scale), format, 0,
+                        rows, cols, batch, codes->stride(b), b ? codes->stride(0) : 0, per};
+  return PyBytes_FromStringAndSize(reinterpret_cast<const char*>(&m), sizeof(m));
+  END_HANDLE_TH_ERRORS
+}
+
 // quantize(X, Q, values)
 PyObject* quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
@@ -302,7 +343,7 @@ PyMethodDef method(const char* name) {
   return PyMethodDef{name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(F)), METH_FASTCALL, nullptr};
 }
 
-PyMethodDef kMethods[] = {method<mx_alloc>("mx_alloc"), method<quantize>("quantize"),
+PyMethodDef kMethods[] = {method<mx_alloc>("mx_alloc"), method<mx_wrap>("mx_wrap"), method<quantize>("quantize"),
                           method<dequantize>("dequantize"), method<gemm_mx>("gemm_mx"),
                           method<rmsnorm>("rmsnorm"), method<rmsnorm_bwd>("rmsnorm_bwd"),
                           {nullptr, nullptr, 0, nullptr}};
