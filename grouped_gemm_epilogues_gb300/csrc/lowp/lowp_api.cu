@@ -182,14 +182,15 @@ bool mx_shape(int32_t format, int64_t M, int64_t N, int64_t L, int64_t k_tiles, 
 // Estimated time (ns) of a shape: rounds of tiles, each its k-tiles and an epilogue.
 // Measured a k-tile (nvfp4, mxfp8): 295 / 240 ns for 128 x 64, 365 / 275 for 128 x 128
 // and 380 / 330 for 256 x 256 on a pair, which is twice the work a CTA.  A split saves
-// the k-tiles but costs the exchange: 16 x 8192 x 4096 nvfp4 7.5 us whole, 7.7 split by
-// two; x 8192 12.7 and 11.2; 128 x 128 tiles exchange twice the chunks (256 x 4096 x
-// 4096 8.4 and 9.4 us, 8.4 -> 7.8 as 128 x 64 tiles).
+// the k-tiles but costs the exchange, about 1.9 us (16 x 8192 nvfp4, whole and split by
+// two: K 512 3.6 and 5.3 us, 4096 7.5 and 7.6, 8192 12.5 and 11.1; 16 x 2048 x 8192,
+// by four: 11.6 and 7.2); 128 x 128 tiles exchange twice the chunks (128 x 8192: K 512
+// 4.3 and 7.2 us, 8192 15.1 and 14.1).
 double mx_cost(const MxShape& s, int64_t k_tiles) {
   const double per_k = s.bn == 64 ? 290.0 : (s.bn == 128 ? 370.0 : 380.0);
   const double tail = s.bn == 64 ? 500.0 : (s.bn == 128 ? 900.0 : 1800.0);
   const int64_t rounds = s.splits > 1 ? 1 : ceil_div(s.tiles, s.units);
-  const double exchange = s.splits == 1 ? 0.0 : (s.bn == 64 ? 2400.0 : 3800.0);
+  const double exchange = s.splits == 1 ? 0.0 : (s.bn == 64 ? 2000.0 : 3300.0);
   return static_cast<double>(rounds) * (static_cast<double>(ceil_div(k_tiles, s.splits)) * per_k + tail) +
          exchange;
 }
