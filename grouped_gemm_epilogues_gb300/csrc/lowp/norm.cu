@@ -53,9 +53,8 @@ __device__ __forceinline__ float row_sum(float v, int tpr, float* slots, int fli
   // (a barrier of its own for each row group: the groups do not run in step, and
   // barrier 0 is the whole block's)
   asm volatile("bar.sync %0, %1;" ::"r"(sub + 1), "r"(tpr) : "memory");
-  const float* mine = s + warp / per * per;
   const int lane = threadIdx.x & 31;
-  return warp_sum(lane < per ? mine[lane] : 0.f);
+  return warp_sum(lane < per ? s[sub * per + lane] : 0.f);
 }
 
 // Eight weights from column col on (zeros past the last one).

@@ -47,25 +47,28 @@ template <typename T>
 __device__ __forceinline__ void copy_row(uint32_t dst, const T* at, int32_t left, bool first) {
   constexpr int P = WarpRow<T>::kPieces;
   const int lane = threadIdx.x & 31;
-  const uint32_t b = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(at)) & 15u;
+  const int32_t b = static_cast<int32_t>(reinterpret_cast<uintptr_t>(at)) & 15;
   const uint8_t* src = reinterpret_cast<const uint8_t*>(at) - b;  // of the lane's first piece
-  left += static_cast<int32_t>(b);
+  left += b;
   dst += 16u * P * lane;
-#pragma unroll
-  for (int j = 0; j < P; ++j) {
-    if (j == 0 && first && b != 0 && lane == 0) {
+  if (first && b != 0) {  // (the whole warp: one row of a matrix at most)
+    if (lane == 0) {
       for (int32_t o = b; o < min(16, left); o += sizeof(T)) {
         if constexpr (sizeof(T) == 2)
           ptx::st_shared_u16(dst + o, *reinterpret_cast<const uint16_t*>(src + o));
         else
           ptx::st_shared_u32(dst + o, *reinterpret_cast<const uint32_t*>(src + o));
       }
-    } else if (left > 16 * j) {
-      ptx::cp_async_16(dst + 16 * j, src + 16 * j, static_cast<uint32_t>(min(16, left - 16 * j)));
+    } else if (left > 0) {
+      ptx::cp_async_16(dst, src, static_cast<uint32_t>(min(16, left)));
     }
+  } else if (left > 0) {
+    ptx::cp_async_16(dst, src, static_cast<uint32_t>(min(16, left)));
   }
-  if (lane == 31 && b != 0 && left > 16 * P)
-    ptx::cp_async_16(dst + 16 * P, src + 16 * P, static_cast<uint32_t>(min(16, left - 16 * P)));
+#pragma unroll
+  for (int j = 1; j <= P; ++j)
+    if ((j < P || lane == 31) && left > 16 * j)
+      ptx::cp_async_16(dst + 16 * j, src + 16 * j, static_cast<uint32_t>(min(16, left - 16 * j)));
 }
 
 // A lane's 8 values of a copied row, after the copy has landed (values past the
