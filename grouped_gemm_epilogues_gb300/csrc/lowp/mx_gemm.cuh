@@ -292,15 +292,14 @@ __device__ __forceinline__ float mx_alpha(const MxParams& mp) {
 // rank order, then the epilogue.  One tile a cluster.
 template <int BN, int FMT, bool TR>
 __device__ __forceinline__ void mx_reduce(const MxParams& mp, const Shared& sh, uint32_t tmem_base,
-                                          uint32_t slice, uint32_t red, uint32_t stg, int32_t t) {
+                                          uint32_t slice, uint32_t red, uint32_t stg, int32_t t,
+                                          float alpha, float beta) {
   const Params& p = mp.p;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int quad = warp & 3, half = warp >> 2;
   const TileCoord tc = tile_coord<BN, kBM>(t, p, sh);
   const int32_t row_base = tc.m_row0 + quad * 32;
   const int32_t rows_valid = min(32, tc.row_limit - row_base);
-  const float alpha = mx_alpha(mp);
-  const float beta = p.beta_dev ? *p.beta_dev : p.beta;
   const uint32_t tbase = tmem_base + (static_cast<uint32_t>(quad * 32) << 16);
 #pragma unroll 1
   for (int c = half; c < BN / 32; c += 2) {
@@ -337,14 +336,12 @@ template <int BN, int CG, int FMT, bool TR>
 __device__ __forceinline__ void mx_epilogue_role(const MxParams& mp, const Shared& sh,
                                                  uint32_t tmem_base, uint32_t rank, uint32_t stg,
                                                  int32_t unit, int32_t units, uint32_t slice,
-                                                 uint32_t red) {
+                                                 uint32_t red, float alpha, float beta) {
   using Cfg = MxCfg<BN, CG, FMT>;
   const Params& p = mp.p;
   constexpr int kMine = BN / 64;  // 32-column chunks of this warp (two warps a lane quadrant)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int quad = warp & 3, half = warp >> 2;
-  const float alpha = mx_alpha(mp);
-  const float beta = p.beta_dev ? *p.beta_dev : p.beta;
   const bool lean = !TR && p.c == nullptr && p.post == nullptr && p.out_stage_bytes != 0 &&
                     p.d_dtype != DT_F32;
   int i = 0;
@@ -500,9 +497,13 @@ __global__ void __launch_bounds__(MxCfg<BN, CG, FMT>::kThreads, 1)
   ptx::tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
 
+  // (read before the main loop: they would cost the split's last step two loads' latency)
+  float alpha = 1.f, beta = 0.f;
   if (warp < Cfg::kEpiWarps) {
+    alpha = mx_alpha(mp);
+    beta = p.beta_dev ? *p.beta_dev : p.beta;
     mx_epilogue_role<BN, CG, FMT, TR>(mp, sh, tmem_base, rank, out_stage + warp * p.out_stage_bytes,
-                                      unit, units, slice, red);
+                                      unit, units, slice, red, alpha, beta);
   } else if (warp == Cfg::kMmaWarp) {
     if (rank == 0 && ptx::elect_one()) mx_mma_role<BN, CG, FMT>(mp, sh, base, tmem_base, ks, unit, units);
   } else {
@@ -516,14 +517,16 @@ __global__ void __launch_bounds__(MxCfg<BN, CG, FMT>::kThreads, 1)
     cluster_wait();  // every rank's chunks are where they belong
     if (warp < Cfg::kEpiWarps && !*abort_flag) {
       ptx::tc_fence_after();
-      mx_reduce<BN, FMT, TR>(mp, sh, tmem_base, slice, red, out_stage + warp * p.out_stage_bytes, unit);
+      mx_reduce<BN, FMT, TR>(mp, sh, tmem_base, slice, red, out_stage + warp * p.out_stage_bytes, unit, alpha,
+                             beta);
       ptx::tc_fence_before();
     }
   }
 
   __syncthreads();
-  // every MMA and scale copy this CTA issued has finished before TMEM is freed
-  if (warp == Cfg::kMmaWarp && rank == 0) {
+  // Every MMA and scale copy this CTA issued has finished before TMEM is freed: its
+  // epilogue has waited for the last tile's, unless a wait ran out.
+  if (*abort_flag && warp == Cfg::kMmaWarp && rank == 0) {
     if (ptx::elect_one()) {
       if (CG == 1) ptx::mma_commit(drain_bar);
       else ptx::mma_commit_pair(drain_bar, 0x1);
