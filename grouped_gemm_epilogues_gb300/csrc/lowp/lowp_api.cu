@@ -77,6 +77,13 @@ bool rows_aligned(const gge_tensor& t) {
          (t.batch <= 1 || t.stride_batch * es % 16 == 0);
 }
 
+// Every row of `t` starts as far past a 16-byte boundary as the same row of `x`.
+bool rows_alike(const gge_tensor& t, const gge_tensor& x) {
+  const int64_t es = elem_bytes(x.dtype);
+  return ((reinterpret_cast<uintptr_t>(t.ptr) ^ reinterpret_cast<uintptr_t>(x.ptr)) & 15u) == 0 &&
+         (t.rows <= 1 || (t.stride_row - x.stride_row) * es % 16 == 0);
+}
+
 // A quantised output (and its values) as the kernels take it.
 gge_status quant_ptrs(const gge_mx_tensor& q, const gge_tensor* values, QuantPtrs* out) {
   gge_status s = check_mx(q);
@@ -182,10 +189,10 @@ bool mx_shape(int32_t format, int64_t M, int64_t N, int64_t L, int64_t k_tiles, 
 // Estimated time (ns) of a shape: rounds of tiles, each its k-tiles and an epilogue.
 // Measured a k-tile (nvfp4, mxfp8): 295 / 240 ns for 128 x 64, 365 / 275 for 128 x 128
 // and 380 / 330 for 256 x 256 on a pair, which is twice the work a CTA.  A split saves
-// the k-tiles but costs the exchange, about 1.9 us (16 x 8192 nvfp4, whole and split by
-// two: K 512 3.6 and 5.3 us, 4096 7.5 and 7.6, 8192 12.5 and 11.1; 16 x 2048 x 8192,
-// by four: 11.6 and 7.2); 128 x 128 tiles exchange twice the chunks (128 x 8192: K 512
-// 4.3 and 7.2 us, 8192 15.1 and 14.1).
+// the k-tiles but costs the exchange, about 1.7 us (16 x 8192 nvfp4, whole and split by
+// two: K 512 3.5 and 5.1 us, 4096 7.4 and 7.4, 8192 12.5 and 11.0; 16 x 2048 x 8192,
+// by four: 11.6 and 7.1); 128 x 128 tiles exchange twice the chunks (128 x 8192: K 512
+// 4.3 and 6.9 us, 4096 8.5 and 9.2, 8192 15.1 and 14.0).
 double mx_cost(const MxShape& s, int64_t k_tiles) {
   const double per_k = s.bn == 64 ? 290.0 : (s.bn == 128 ? 370.0 : 380.0);
   const double tail = s.bn == 64 ? 500.0 : (s.bn == 128 ? 900.0 : 1800.0);
@@ -453,6 +460,7 @@ gge_status gge_rmsnorm(const gge_rmsnorm_args* a, gge_stream_t stream) {
   std::memset(&p, 0, sizeof(p));
   p.q.format = 3;  // no quantised output
   bool aligned = rows_aligned(x) && (a->values == nullptr || rows_aligned(*a->values));
+  bool alike = a->q == nullptr;
   const auto take = [&](const gge_tensor* t, bool output) {
     if (t == nullptr) return GGE_OK;
     const gge_status r = check_values(*t, false);
@@ -460,6 +468,7 @@ gge_status gge_rmsnorm(const gge_rmsnorm_args* a, gge_stream_t stream) {
     if (t->dtype != x.dtype) return GGE_ERR_UNSUPPORTED;
     if (!same_shape(*t, x.rows, x.cols, 1) || (output && !rows_apart(*t))) return GGE_ERR_INVALID_ARG;
     aligned = aligned && rows_aligned(*t);
+    alike = alike && rows_alike(*t, x);
     return GGE_OK;
   };
   if ((s = take(a->residual, false)) != GGE_OK) return s;
@@ -490,7 +499,7 @@ gge_status gge_rmsnorm(const gge_rmsnorm_args* a, gge_stream_t stream) {
   p.eps = a->eps;
   p.inv = a->inv_rms;
   p.w_vec = aligned16(a->weight) ? 1 : 0;
-  p.aligned = aligned ? 1 : 0;
+  p.rows_lie = aligned ? lowp::ROWS_ALIGNED : (alike ? lowp::ROWS_ALIKE : lowp::ROWS_ANY);
   const int sms = sm_count();
   if (sms <= 0) return GGE_ERR_CUDA;
   return launched(lowp::launch_norm(p, sms, reinterpret_cast<cudaStream_t>(stream)));
@@ -511,7 +520,7 @@ gge_status gge_rmsnorm_bwd(const gge_rmsnorm_bwd_args* a, void* ws, size_t ws_by
   if (s != GGE_OK) return s;
   if (dy.batch != 1) return GGE_ERR_UNSUPPORTED;
   if (!is_value_type(a->weight_dtype)) return GGE_ERR_UNSUPPORTED;
-  bool aligned = rows_aligned(dy);
+  bool aligned = rows_aligned(dy), alike = true;
   for (const gge_tensor* t : {&a->h, a->dh, &a->dx}) {
     if (t == nullptr) continue;
     s = check_values(*t, false);
@@ -519,6 +528,7 @@ gge_status gge_rmsnorm_bwd(const gge_rmsnorm_bwd_args* a, void* ws, size_t ws_by
     if (t->dtype != dy.dtype) return GGE_ERR_UNSUPPORTED;
     if (!same_shape(*t, dy.rows, dy.cols, 1)) return GGE_ERR_INVALID_ARG;
     aligned = aligned && rows_aligned(*t);
+    alike = alike && rows_alike(*t, dy);
   }
   if (!rows_apart(a->dx)) return GGE_ERR_INVALID_ARG;
   if (dy.cols == 0 || (dy.rows == 0 && a->dweight == nullptr)) return GGE_OK;
@@ -544,7 +554,7 @@ gge_status gge_rmsnorm_bwd(const gge_rmsnorm_bwd_args* a, void* ws, size_t ws_by
   p.inv = a->inv_rms;
   p.dw = a->dweight;
   p.w_vec = aligned16(a->weight) ? 1 : 0;
-  p.aligned = aligned ? 1 : 0;
+  p.rows_lie = aligned ? lowp::ROWS_ALIGNED : (alike ? lowp::ROWS_ALIKE : lowp::ROWS_ANY);
   const int sms = sm_count();
   if (sms <= 0) return GGE_ERR_CUDA;
   if (a->dweight != nullptr) {

@@ -25,6 +25,18 @@ struct QuantPtrs {
   int32_t v_dtype;
 };
 
+// How the rows of a norm's tensors lie in memory.
+//   ALIGNED  every row of every tensor starts on a 16-byte boundary;
+//   ALIKE    a row starts equally far (`skew` values) past one in every tensor.  The
+//            chunks then start on the boundary before the row, chunk 0 with `skew`
+//            values that are not the row's.  A row group takes every 8th row (or every
+//            16th ...), so that its skew stays the same: the weights' place and dw's
+//            are fixed in registers, and nothing is shifted;
+//   ANY      chunks start with the row, and rows.cuh shifts what is read and written.
+// Codes with scales want chunks that start with the row (their blocks do), so ALIKE is
+// for outputs in values only.
+enum Rows { ROWS_ANY = 0, ROWS_ALIGNED = 1, ROWS_ALIKE = 2 };
+
 struct NormParams {
   int64_t rows;
   int32_t cols;
@@ -37,8 +49,8 @@ struct NormParams {
   float eps;
   float* inv;  // NULL: not wanted
   QuantPtrs q;
-  int32_t w_vec;    // the weight starts on a 16-byte boundary
-  int32_t aligned;  // and so does every row of every tensor
+  int32_t w_vec;     // the weight starts on a 16-byte boundary
+  int32_t rows_lie;  // Rows
 };
 
 struct NormBwdParams {
@@ -53,7 +65,7 @@ struct NormBwdParams {
   const float* inv;
   float* dw;        // NULL: not wanted
   float* partials;  // [grid][cols] sums of the blocks' rows
-  int32_t w_vec, aligned;
+  int32_t w_vec, rows_lie;
 };
 
 struct QuantParams {

@@ -21,6 +21,7 @@
 // issue.  Two chunks a thread against one: 47 and 58 us for 16000 x 1999; four 50.
 // Backward 16384 x 4096 with dh 92 us (5.8 TB/s, 87 %).
 #include <atomic>
+#include <numeric>
 
 #include "lowp_launch.h"
 #include "rows.cuh"
@@ -57,7 +58,7 @@ __device__ __forceinline__ float row_sum(float v, int tpr, float* slots, int fli
   return warp_sum(lane < per ? s[sub * per + lane] : 0.f);
 }
 
-// Eight weights from column col on (zeros past the last one).
+// Eight weights from column col on (zeros outside the row).
 __device__ __forceinline__ void load_weight(const void* w, int32_t dtype, int32_t vec, int32_t col,
                                             int32_t cols, float2 (&v)[4]) {
   if (vec && col + 8 <= cols) {
@@ -67,8 +68,9 @@ __device__ __forceinline__ void load_weight(const void* w, int32_t dtype, int32_
   } else {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      v[i].x = col + 2 * i < cols ? load_any(w, col + 2 * i, dtype) : 0.f;
-      v[i].y = col + 2 * i + 1 < cols ? load_any(w, col + 2 * i + 1, dtype) : 0.f;
+      const int32_t a = col + 2 * i, b = a + 1;
+      v[i].x = a >= 0 && a < cols ? load_any(w, a, dtype) : 0.f;
+      v[i].y = b >= 0 && b < cols ? load_any(w, b, dtype) : 0.f;
     }
   }
 }
@@ -83,35 +85,61 @@ __device__ __forceinline__ void clear_past(Raw8<T>& r, int32_t col, int32_t cols
     if (col + i >= cols) t[i] = from_float<T>(0.f);
 }
 
-// One tensor's rows on their way through shared memory, for one warp.  AL: every
-// row starts on a 16-byte boundary, so a lane copies and reads its own pieces
-// only; otherwise the warp does it together (rows.cuh).
-template <typename T, bool AL>
+template <typename T>
+__device__ __forceinline__ int32_t row_skew(const void* row) {
+  return static_cast<int32_t>((reinterpret_cast<uintptr_t>(row) & 15u) / sizeof(T));
+}
+
+// The first k (0 to 7) set to zero.
+template <typename T>
+__device__ __forceinline__ void clear_front(Raw8<T>& r, int32_t k) {
+  uint32_t* w = reinterpret_cast<uint32_t*>(&r);
+#pragma unroll
+  for (int j = 0; j < 2 * static_cast<int>(sizeof(T)); ++j) {
+    const int32_t bits = 8 * static_cast<int>(sizeof(T)) * k - 32 * j;  // of word j
+    w[j] &= __funnelshift_lc(0u, 0xffffffffu, static_cast<uint32_t>(max(bits, 0)));
+  }
+}
+
+// One tensor's rows on their way through shared memory, for one warp: in ANY the
+// warp does it together, otherwise a lane copies and reads its own pieces only.
+template <typename T, int R>
 struct RowReader {
   const T* next;  // this lane's chunk 0 of the next row to copy
 
   __device__ __forceinline__ void init(const void* base, int64_t ld, int64_t row, int32_t col) {
     next = static_cast<const T*>(base) + row * ld + col;
   }
-  // AL, once a buffer: a lane's pieces past the row's end stay zero
+  // Once a buffer (not ANY): a lane's pieces past the row's end stay zero.
   static __device__ __forceinline__ void clear(uint32_t dst, int32_t col, int32_t cols) {
     constexpr int P = WarpRow<T>::kPieces;
-    if constexpr (AL) {
+    if constexpr (R != ROWS_ANY) {
 #pragma unroll
       for (int j = 0; j < P; ++j)
         if (col + j * static_cast<int32_t>(16 / sizeof(T)) >= cols)
           ptx::st_shared_v4(dst + 16u * ((threadIdx.x & 31) * P + j), make_uint4(0u, 0u, 0u, 0u));
     }
   }
-  // copy chunk c (`over` columns after chunk 0) of that row to this warp's `dst`
+  // Copy chunk c (`over` columns after chunk 0) of that row to this warp's `dst`.
+  // `first`: nothing may be read in front of the row.
   __device__ __forceinline__ void copy(uint32_t dst, int32_t col, int32_t over, int32_t cols,
                                        bool first) const {
     constexpr int P = WarpRow<T>::kPieces;
     const int lane = threadIdx.x & 31;
     const int32_t left = (cols - col) * static_cast<int32_t>(sizeof(T));
-    if constexpr (AL) {
+    if constexpr (R != ROWS_ANY) {
+      if (R == ROWS_ALIKE && first && col < 0) {  // (one thread of the launch's first rows)
+        const T* at = next + over;
+        for (int32_t i = -col; i < min(static_cast<int32_t>(16 / sizeof(T)), cols - col); ++i) {
+          if constexpr (sizeof(T) == 2)
+            ptx::st_shared_u16(dst + 16u * (lane * P) + 2 * i, *reinterpret_cast<const uint16_t*>(at + i));
+          else
+            ptx::st_shared_u32(dst + 16u * (lane * P) + 4 * i, *reinterpret_cast<const uint32_t*>(at + i));
+        }
+      }
 #pragma unroll
       for (int j = 0; j < P; ++j) {
+        if (R == ROWS_ALIKE && j == 0 && first && col < 0) continue;
         // (bytes past the row's end are zero-filled; none are read)
         if (left > 16 * j)
           ptx::cp_async_16(dst + 16u * (lane * P + j), next + over + j * (16 / sizeof(T)),
@@ -123,14 +151,19 @@ struct RowReader {
   }
 };
 
-// A lane's 8 values of a copied chunk of the row that starts at `row`.
-template <typename T, bool AL>
+// A lane's 8 values of a copied chunk of the row that starts at `row`; zeros where the
+// chunk leaves the row.
+template <typename T, int R>
 __device__ __forceinline__ Raw8<T> take_chunk(uint32_t src, const T* row, int32_t col, int32_t cols) {
   constexpr int P = WarpRow<T>::kPieces;
-  if constexpr (AL) {
+  if constexpr (R != ROWS_ANY) {
     Raw8<T> r;
 #pragma unroll
     for (int j = 0; j < P; ++j) r.w[j] = ptx::ld_shared_v4(src + 16u * ((threadIdx.x & 31) * P + j));
+    if (R == ROWS_ALIKE && col < 0) {
+      clear_front(r, -col);
+      clear_past(r, col, cols);
+    }
     return r;
   } else {
     Raw8<T> r = take_row<T>(src, static_cast<uint32_t>(reinterpret_cast<uintptr_t>(row)) & 15u);
@@ -139,10 +172,30 @@ __device__ __forceinline__ Raw8<T> take_chunk(uint32_t src, const T* row, int32_
   }
 }
 
-template <typename T, bool AL>
+template <typename T, int R>
 __device__ __forceinline__ void put_chunk(T* row, int32_t col, int32_t cols, const Raw8<T>& v) {
-  if constexpr (AL) store_row8_aligned(row, col, cols, v);
-  else store_row8(row, col, cols, v);
+  if (R == ROWS_ALIKE && col < 0) {
+    if (col + 8 <= cols) {
+      store_from(row + col, -col, v);
+    } else {  // (a row shorter than 8)
+      const T* t = reinterpret_cast<const T*>(&v);
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i >= -col && col + i < cols) row[col + i] = t[i];
+    }
+  } else if constexpr (R != ROWS_ANY) {
+    store_row8_aligned(row, col, cols, v);
+  } else {
+    store_row8(row, col, cols, v);
+  }
+}
+
+// A launch's blocks such that a row group's rows are a multiple of 8 apart (of which
+// every skew has an equal), if it takes more than one; 0 if there are too few.
+int alike_blocks(int64_t rows, int per_block, int64_t blocks) {
+  if (rows <= blocks * per_block) return static_cast<int>(blocks);
+  const int unit = 8 / std::gcd(8, per_block);
+  return static_cast<int>(blocks / unit * unit);
 }
 
 // ------------------------------------------------------------ forward
@@ -155,7 +208,7 @@ constexpr int norm_depth() {
 
 // A row is spread over `tpr` threads; thread i holds the 8-value chunks i, i + tpr, ...
 // The block's row groups run on their own: what they share is shared memory's size.
-template <typename T, int C, int FMT, bool AL>
+template <typename T, int C, int FMT, int R>
 __global__ void __launch_bounds__(kMaxThreads)
     norm_kernel(const __grid_constant__ NormParams p, int tpr) {
   __shared__ float slots[64];
@@ -166,7 +219,6 @@ __global__ void __launch_bounds__(kMaxThreads)
   const int sub = threadIdx.x / tpr, t = threadIdx.x % tpr;
   const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   const int32_t cols = p.cols;
-  const int32_t warp_col = (t - lane) * 8;  // of chunk 0
   // this warp's buffers: [row in flight][chunk][x, residual]
   constexpr uint32_t kBuf = WarpRow<T>::kBytes;
   const uint32_t ring = ptx::smem_addr(ring_raw) + (threadIdx.x >> 5) * (C * 2 * kBuf);
@@ -175,22 +227,31 @@ __global__ void __launch_bounds__(kMaxThreads)
   const uint32_t step = gridDim.x * per_block;
   uint32_t row = blockIdx.x * per_block + sub;
   const bool has_res = p.residual != nullptr;
-  RowReader<T, AL> x, res;
-  x.init(p.x, p.ldx, row, t * 8);
-  res.init(p.residual, p.ldr, row, t * 8);
+  RowReader<T, R> x, res;
+  const int32_t skew = R == ROWS_ALIKE ? row_skew<T>(static_cast<const T*>(p.x) + row * p.ldx) : 0;
+  const int32_t col0 = t * 8 - skew;         // chunk 0's first column
+  const int32_t warp_col = col0 - lane * 8;  // and its warp's
+  x.init(p.x, p.ldx, row, col0);
+  res.init(p.residual, p.ldr, row, col0);
   ptx::griddep_wait();
   const float tscale = (FMT == FMT_NVFP4 && p.q.tensor_scale) ? *p.q.tensor_scale : 1.f;
 #pragma unroll
   for (int s = 0; s < D * C * 2; ++s)
-    RowReader<T, AL>::clear(ring + s / (C * 2) * ring_row + s % (C * 2) * kBuf, (t + s % (C * 2) / 2 * tpr) * 8, cols);
+    RowReader<T, R>::clear(ring + s / (C * 2) * ring_row + s % (C * 2) * kBuf, col0 + s % (C * 2) / 2 * tpr * 8, cols);
+  float2 wk[C][4];  // ALIKE: the weights stay in registers
+  if constexpr (R == ROWS_ALIKE) {
+#pragma unroll
+    for (int c = 0; c < C; ++c) load_weight(p.weight, p.w_dtype, 0, col0 + c * tpr * 8, cols, wk[c]);
+  }
   uint32_t ahead = row;
   const auto start = [&](int slot) {
     if (ahead < rows) {
 #pragma unroll
       for (int c = 0; c < C; ++c) {
         const uint32_t dst = ring + slot * ring_row + c * 2 * kBuf;
-        x.copy(dst, (t + c * tpr) * 8, c * tpr * 8, cols, ahead == 0);
-        if (has_res) res.copy(dst + kBuf, (t + c * tpr) * 8, c * tpr * 8, cols, ahead == 0);
+        const int32_t over = c * tpr * 8;
+        x.copy(dst, col0 + over, over, cols, ahead * p.ldx < 8);
+        if (has_res) res.copy(dst + kBuf, col0 + over, over, cols, ahead * p.ldr < 8);
       }
       x.next += static_cast<int64_t>(step) * p.ldx;
       res.next += static_cast<int64_t>(step) * p.ldr;
@@ -203,21 +264,21 @@ __global__ void __launch_bounds__(kMaxThreads)
   const float inv_cols = 1.f / static_cast<float>(cols);
   int slot = 0, flip = 0;
   for (; row < rows; row += step) {
-    if constexpr (!AL) __syncwarp();  // (the slot was read in the iteration before)
+    if constexpr (R == ROWS_ANY) __syncwarp();  // (the slot was read in the iteration before)
     start((slot + D - 1) % D);
     cp_async_wait<D - 1>();
-    if constexpr (!AL) __syncwarp();
+    if constexpr (R == ROWS_ANY) __syncwarp();
     Raw8<T> h[C];
     float2 ss = make_float2(0.f, 0.f);
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      const int32_t col = (t + c * tpr) * 8;
+      const int32_t col = col0 + c * tpr * 8;
       const uint32_t src = ring + slot * ring_row + c * 2 * kBuf;
-      h[c] = take_chunk<T, AL>(src, static_cast<const T*>(p.x) + row * p.ldx, col, cols);
+      h[c] = take_chunk<T, R>(src, static_cast<const T*>(p.x) + row * p.ldx, col, cols);
       if (has_res) {
-        h[c] = add8(h[c], take_chunk<T, AL>(src + kBuf, static_cast<const T*>(p.residual) + row * p.ldr, col, cols));
+        h[c] = add8(h[c], take_chunk<T, R>(src + kBuf, static_cast<const T*>(p.residual) + row * p.ldr, col, cols));
         if (p.h != nullptr && warp_col + c * tpr * 8 < cols)
-          put_chunk<T, AL>(static_cast<T*>(p.h) + row * p.ldh, col, cols, h[c]);
+          put_chunk<T, R>(static_cast<T*>(p.h) + row * p.ldh, col, cols, h[c]);
       }
       float2 v[4];
       widen(h[c], v);
@@ -237,14 +298,15 @@ __global__ void __launch_bounds__(kMaxThreads)
     }
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      const int32_t col = (t + c * tpr) * 8;
+      const int32_t col = col0 + c * tpr * 8;
       if (c > 0 && warp_col + c * tpr * 8 >= cols) continue;
       float2 v[4], w[4];
       widen(h[c], v);
-      load_weight(p.weight, p.w_dtype, p.w_vec, col, cols, w);
+      if constexpr (R != ROWS_ALIKE) load_weight(p.weight, p.w_dtype, p.w_vec, col, cols, w);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = __fmul2_rn(__fmul2_rn(v[i], make_float2(inv, inv)), w[i]);
-      if (p.y != nullptr) put_chunk<T, AL>(static_cast<T*>(p.y) + row * p.ldy, col, cols, narrow<T>(v));
+      for (int i = 0; i < 4; ++i)
+        v[i] = __fmul2_rn(__fmul2_rn(v[i], make_float2(inv, inv)), R == ROWS_ALIKE ? wk[c][i] : w[i]);
+      if (p.y != nullptr) put_chunk<T, R>(static_cast<T*>(p.y) + row * p.ldy, col, cols, narrow<T>(v));
       if constexpr (FMT != FMT_NONE) {
         constexpr int B = Fmt<FMT>::kBlock;
         const Quantised z = quantise8<FMT>(v, tscale, col >= (cols + B - 1) / B * B);
@@ -253,7 +315,7 @@ __global__ void __launch_bounds__(kMaxThreads)
         if (col < ((cols + 31) & ~31)) store_codes<FMT>(codes + static_cast<int64_t>(col) * Fmt<FMT>::kBits / 8, z.codes);
         if (p.q.values != nullptr) {
           code_values<FMT>(z.codes, z.unit, tscale, v);
-          store_row8_any<AL>(p.q.values, row * p.q.ldv, p.q.v_dtype, col, cols, v);
+          store_row8_any<R == ROWS_ALIGNED>(p.q.values, row * p.q.ldv, p.q.v_dtype, col, cols, v);
         }
       }
     }
@@ -343,32 +405,53 @@ __global__ void norm_long_kernel(const __grid_constant__ NormParams p) {
   }
 }
 
-// Threads a row of `chunks` 8-value chunks, and chunks a thread (1 or 2).  A row
-// group has a warp, or at least 128 threads: a block of 1024 then has at most 8
-// groups with barriers (of the 15 beside barrier 0).
+// Threads a row of `chunks` 8-value chunks (whole warps), and chunks a thread (1 or 2).
 struct RowShape {
   int tpr, c;
 };
-RowShape row_shape(int64_t chunks, bool one) {
-  RowShape s{32, 1};
-  while (s.tpr < kMaxThreads && static_cast<int64_t>(s.tpr) * (one ? 1 : 2) < chunks) s.tpr = s.tpr == 32 ? 128 : s.tpr * 2;
-  if (s.tpr < chunks) s.c = 2;
-  return s;
+RowShape row_shape(int64_t chunks, bool few) {
+  const int c = chunks > (few ? kMaxThreads : 32) ? 2 : 1;
+  const int tpr = static_cast<int>((chunks + 32 * c - 1) / (32 * c) * 32);
+  return {tpr, c};
 }
 
-template <typename T, int C, int FMT, bool AL>
+// Rows a block, and blocks an SM, such that as many rows as possible are at work: an
+// SM has four quarters of 8 warps of 64 registers a thread, and a block's warps go
+// round them.  Row groups of several warps have a barrier each, of the 15 beside the
+// block's.  (1536 columns, 96 threads a row: 5 rows a block, twice, 34 us for 48 M
+// values; 2 rows a block, which leaves room for four blocks, 46.)
+struct BlockShape {
+  int per, blocks;
+};
+BlockShape block_shape(int tpr) {
+  BlockShape best{0, 0};
+  for (int per = 1; per * tpr <= kMaxThreads && (tpr == 32 || per <= 15); ++per) {
+    const int warps = per * tpr / 32;
+    const int blocks = 8 / ((warps + 3) / 4);
+    // (blocks below 256 threads were slower at the same number of rows; above, alike)
+    const bool more = per * blocks > best.per * best.blocks;
+    if (more || (per * blocks == best.per * best.blocks && best.per * tpr < 256)) best = {per, blocks};
+  }
+  return best;
+}
+
+// Chunks of a row of `cols` values that starts at any skew.
+int64_t alike_chunks(int64_t cols, int value_bytes) { return (cols + 16 / value_bytes - 1 + 7) / 8; }
+
+template <typename T, int C, int FMT, int R>
 cudaError_t launch_norm_c(const NormParams& p, int tpr, int sms, cudaStream_t st) {
   static std::atomic<size_t> set[64];
-  const int block = tpr > 256 ? tpr : 256;
-  const int per = block / tpr;
+  const BlockShape shape = block_shape(tpr);
+  const int per = shape.per, block = per * tpr;
   const size_t smem = static_cast<size_t>(norm_depth<T, C>()) * (block / 32) * C * 2 * WarpRow<T>::kBytes;
-  const cudaError_t e = allow_smem(norm_kernel<T, C, FMT, AL>, set, smem);
+  const cudaError_t e = allow_smem(norm_kernel<T, C, FMT, R>, set, smem);
   if (e != cudaSuccess) return e;
-  // as many blocks as an SM holds (64 registers a thread), each with its share of the rows
-  const int64_t resident = static_cast<int64_t>(sms) * (1024 / block);
+  // as many blocks as an SM holds, each with its share of the rows
+  const int64_t resident = static_cast<int64_t>(sms) * shape.blocks;
   const int64_t want = (p.rows + per - 1) / per;
-  return launch_pdl(norm_kernel<T, C, FMT, AL>, dim3(static_cast<unsigned>(want < resident ? want : resident)),
-                    dim3(block), smem, st, p, tpr);
+  int blocks = static_cast<int>(want < resident ? want : resident);
+  if (R == ROWS_ALIKE) blocks = alike_blocks(p.rows, per, blocks);
+  return launch_pdl(norm_kernel<T, C, FMT, R>, dim3(blocks), dim3(block), smem, st, p, tpr);
 }
 
 template <typename T, int FMT>
@@ -378,11 +461,19 @@ cudaError_t launch_norm_t(const NormParams& p, int sms, cudaStream_t st) {
   if (span <= kMaxCols) {
     // few rows: one chunk a thread (latency); many: two, so that a row's barrier costs less
     const RowShape s = row_shape(span / 8, p.rows <= sms);
-    if (p.aligned)
-      return s.c == 1 ? launch_norm_c<T, 1, FMT, true>(p, s.tpr, sms, st)
-                      : launch_norm_c<T, 2, FMT, true>(p, s.tpr, sms, st);
-    return s.c == 1 ? launch_norm_c<T, 1, FMT, false>(p, s.tpr, sms, st)
-                    : launch_norm_c<T, 2, FMT, false>(p, s.tpr, sms, st);
+    if (p.rows_lie == ROWS_ALIGNED)
+      return s.c == 1 ? launch_norm_c<T, 1, FMT, ROWS_ALIGNED>(p, s.tpr, sms, st)
+                      : launch_norm_c<T, 2, FMT, ROWS_ALIGNED>(p, s.tpr, sms, st);
+    if constexpr (FMT == FMT_NONE) {
+      const int64_t chunks = alike_chunks(p.cols, sizeof(T));
+      if (p.rows_lie == ROWS_ALIKE && chunks * 8 <= kMaxCols && sms >= 8) {
+        const RowShape a = row_shape(chunks, p.rows <= sms);
+        return a.c == 1 ? launch_norm_c<T, 1, FMT, ROWS_ALIKE>(p, a.tpr, sms, st)
+                        : launch_norm_c<T, 2, FMT, ROWS_ALIKE>(p, a.tpr, sms, st);
+      }
+    }
+    return s.c == 1 ? launch_norm_c<T, 1, FMT, ROWS_ANY>(p, s.tpr, sms, st)
+                    : launch_norm_c<T, 2, FMT, ROWS_ANY>(p, s.tpr, sms, st);
   }
   return launch_pdl(norm_long_kernel<T, FMT>,
                     dim3(static_cast<unsigned>(p.rows < 65536 ? p.rows : 65536)), dim3(kMaxThreads), 0, st, p);
@@ -400,60 +491,70 @@ cudaError_t launch_norm_f(const NormParams& p, int sms, cudaStream_t st) {
 
 // ----------------------------------------------------------- backward
 
-// Rows in shared memory: what fits beside each other for 1024 threads.
+// dw, the weights and a row stay in registers over the row's sum, so a block has few
+// threads with many registers, and up to four chunks a thread.
+constexpr int kBwdThreads = 512;
+
+// Rows in shared memory: what fits beside each other for a whole block.
 template <typename T, int C>
 constexpr int bwd_depth() {
-  const int row = 32 * C * 3 * WarpRow<T>::kBytes;
+  const int row = kBwdThreads / 32 * C * 3 * WarpRow<T>::kBytes;
   return 3 * row <= 210 * 1024 ? 3 : (2 * row <= 210 * 1024 ? 2 : 1);
 }
 
-// A block of 1024 threads takes 1024 / tpr rows at a time.  Each thread keeps its
+// A block takes as many rows at a time as its threads hold.  Each thread keeps its
 // columns' share of dw in registers; at the end the block's row groups add theirs
 // up and leave one row of partial sums.
-template <typename T, int C, bool AL>
-__global__ void __launch_bounds__(kMaxThreads)
+template <typename T, int C, int R>
+__global__ void __launch_bounds__(kBwdThreads)
     norm_bwd_kernel(const __grid_constant__ NormBwdParams p, int tpr) {
   __shared__ float slots[64];
   extern __shared__ uint8_t ring_raw[];
   ptx::griddep_launch_dependents();
   constexpr int D = bwd_depth<T, C>();
-  const int per_block = kMaxThreads / tpr;
+  // g and h stay in registers over the row's sum, or are made again from shared memory
+  constexpr bool kKeep = C < 4;
+  const int per_block = blockDim.x / tpr;
   const int sub = threadIdx.x / tpr, t = threadIdx.x % tpr;
   const int lane = threadIdx.x & 31;
   const int32_t cols = p.cols;
-  const int32_t warp_col = (t - lane) * 8;
   constexpr uint32_t kBuf = WarpRow<T>::kBytes;
-  constexpr uint32_t kRow = (kMaxThreads / 32) * C * 3 * kBuf;
+  const uint32_t ring_row = (blockDim.x >> 5) * (C * 3 * kBuf);
   const uint32_t ring = ptx::smem_addr(ring_raw) + (threadIdx.x >> 5) * (C * 3 * kBuf);
   const uint32_t rows = static_cast<uint32_t>(p.rows);  // (below 2^31, and so is a step past them)
   const uint32_t step = gridDim.x * per_block;
   uint32_t row = blockIdx.x * per_block + sub;
   const bool has_dh = p.dh != nullptr;
-  RowReader<T, AL> dy, h, dh;
-  dy.init(p.dy, p.lddy, row, t * 8);
-  h.init(p.h, p.ldh, row, t * 8);
-  dh.init(p.dh, p.lddh, row, t * 8);
+  RowReader<T, R> dy, h, dh;
+  const int32_t skew = R == ROWS_ALIKE ? row_skew<T>(static_cast<const T*>(p.h) + row * p.ldh) : 0;
+  const int32_t col0 = t * 8 - skew;         // chunk 0's first column
+  const int32_t warp_col = col0 - lane * 8;  // and its warp's
+  dy.init(p.dy, p.lddy, row, col0);
+  h.init(p.h, p.ldh, row, col0);
+  dh.init(p.dh, p.lddh, row, col0);
   ptx::griddep_wait();
   float2 dw[C][4];
 #pragma unroll
   for (int c = 0; c < C; ++c)
 #pragma unroll
     for (int i = 0; i < 4; ++i) dw[c][i] = make_float2(0.f, 0.f);
-  float2 wk[4];  // one chunk a thread: its weights stay in registers
-  if (C == 1) load_weight(p.weight, p.w_dtype, p.w_vec, t * 8, cols, wk);
+  float2 w[C][4];
+#pragma unroll
+  for (int c = 0; c < C; ++c)
+    load_weight(p.weight, p.w_dtype, R == ROWS_ALIKE ? 0 : p.w_vec, col0 + c * tpr * 8, cols, w[c]);
 #pragma unroll
   for (int s = 0; s < D * C * 3; ++s)
-    RowReader<T, AL>::clear(ring + s / (C * 3) * kRow + s % (C * 3) * kBuf, (t + s % (C * 3) / 3 * tpr) * 8, cols);
+    RowReader<T, R>::clear(ring + s / (C * 3) * ring_row + s % (C * 3) * kBuf, col0 + s % (C * 3) / 3 * tpr * 8, cols);
   uint32_t ahead = row;
   const auto start = [&](int slot) {
     if (ahead < rows) {
 #pragma unroll
       for (int c = 0; c < C; ++c) {
-        const uint32_t dst = ring + slot * kRow + c * 3 * kBuf;
-        const int32_t col = (t + c * tpr) * 8, over = c * tpr * 8;
-        dy.copy(dst, col, over, cols, ahead == 0);
-        h.copy(dst + kBuf, col, over, cols, ahead == 0);
-        if (has_dh) dh.copy(dst + 2 * kBuf, col, over, cols, ahead == 0);
+        const uint32_t dst = ring + slot * ring_row + c * 3 * kBuf;
+        const int32_t over = c * tpr * 8, col = col0 + over;
+        dy.copy(dst, col, over, cols, ahead * p.lddy < 8);
+        h.copy(dst + kBuf, col, over, cols, ahead * p.ldh < 8);
+        if (has_dh) dh.copy(dst + 2 * kBuf, col, over, cols, ahead * p.lddh < 8);
       }
       dy.next += static_cast<int64_t>(step) * p.lddy;
       h.next += static_cast<int64_t>(step) * p.ldh;
@@ -468,30 +569,31 @@ __global__ void __launch_bounds__(kMaxThreads)
   int slot = 0, flip = 0;
   float inv_next = row < rows ? p.inv[row] : 0.f;
   for (; row < rows; row += step) {
-    if constexpr (!AL) __syncwarp();
+    if constexpr (R == ROWS_ANY) __syncwarp();
     start((slot + D - 1) % D);
     const float inv = inv_next;
     if (row + step < rows) inv_next = p.inv[row + step];
     const float2 inv2 = make_float2(inv, inv);
     cp_async_wait<D - 1>();
-    if constexpr (!AL) __syncwarp();
-    const uint32_t src = ring + slot * kRow;
-    Raw8<T> hr[C];
-    float2 g[C][4];
+    if constexpr (R == ROWS_ANY) __syncwarp();
+    const uint32_t src = ring + slot * ring_row;
+    Raw8<T> hr[kKeep ? C : 1];
+    float2 g[kKeep ? C : 1][4];
     float2 dot = make_float2(0.f, 0.f);
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      const int32_t col = (t + c * tpr) * 8;
-      float2 hv[4], w[4];
-      widen(take_chunk<T, AL>(src + c * 3 * kBuf, static_cast<const T*>(p.dy) + row * p.lddy, col, cols), g[c]);
-      hr[c] = take_chunk<T, AL>(src + c * 3 * kBuf + kBuf, static_cast<const T*>(p.h) + row * p.ldh, col, cols);
-      widen(hr[c], hv);
-      if (C > 1) load_weight(p.weight, p.w_dtype, p.w_vec, col, cols, w);
+      const int32_t col = col0 + c * tpr * 8;
+      float2 hv[4];
+      float2(&z)[4] = g[kKeep ? c : 0];
+      widen(take_chunk<T, R>(src + c * 3 * kBuf, static_cast<const T*>(p.dy) + row * p.lddy, col, cols), z);
+      Raw8<T>& raw = hr[kKeep ? c : 0];
+      raw = take_chunk<T, R>(src + c * 3 * kBuf + kBuf, static_cast<const T*>(p.h) + row * p.ldh, col, cols);
+      widen(raw, hv);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        dw[c][i] = __ffma2_rn(g[c][i], __fmul2_rn(hv[i], inv2), dw[c][i]);
-        g[c][i] = __fmul2_rn(g[c][i], C > 1 ? w[i] : wk[i]);
-        dot = __ffma2_rn(g[c][i], hv[i], dot);
+        dw[c][i] = __ffma2_rn(z[i], __fmul2_rn(hv[i], inv2), dw[c][i]);
+        z[i] = __fmul2_rn(z[i], w[c][i]);
+        dot = __ffma2_rn(z[i], hv[i], dot);
       }
     }
     const float sum = row_sum(dot.x + dot.y, tpr, slots, flip, sub);
@@ -499,18 +601,25 @@ __global__ void __launch_bounds__(kMaxThreads)
     const float k = -(sum * inv_cols) * inv * inv;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      const int32_t col = (t + c * tpr) * 8;
+      const int32_t col = col0 + c * tpr * 8;
       if (warp_col + c * tpr * 8 >= cols) continue;
       float2 v[4];
-      widen(hr[c], v);
+      float2(&z)[4] = g[kKeep ? c : 0];
+      if constexpr (!kKeep) {
+        hr[0] = take_chunk<T, R>(src + c * 3 * kBuf + kBuf, static_cast<const T*>(p.h) + row * p.ldh, col, cols);
+        widen(take_chunk<T, R>(src + c * 3 * kBuf, static_cast<const T*>(p.dy) + row * p.lddy, col, cols), z);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) g[c][i] = __fmul2_rn(inv2, __ffma2_rn(v[i], make_float2(k, k), g[c][i]));
-      if (has_dh) {
-        widen(take_chunk<T, AL>(src + c * 3 * kBuf + 2 * kBuf, static_cast<const T*>(p.dh) + row * p.lddh, col, cols), v);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) g[c][i] = __fadd2_rn(g[c][i], v[i]);
+        for (int i = 0; i < 4; ++i) z[i] = __fmul2_rn(z[i], w[c][i]);
       }
-      put_chunk<T, AL>(static_cast<T*>(p.dx) + row * p.lddx, col, cols, narrow<T>(g[c]));
+      widen(hr[kKeep ? c : 0], v);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) z[i] = __fmul2_rn(inv2, __ffma2_rn(v[i], make_float2(k, k), z[i]));
+      if (has_dh) {
+        widen(take_chunk<T, R>(src + c * 3 * kBuf + 2 * kBuf, static_cast<const T*>(p.dh) + row * p.lddh, col, cols), v);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) z[i] = __fadd2_rn(z[i], v[i]);
+      }
+      put_chunk<T, R>(static_cast<T*>(p.dx) + row * p.lddx, col, cols, narrow<T>(z));
     }
     slot = (slot + 1) % D;
   }
@@ -518,17 +627,20 @@ __global__ void __launch_bounds__(kMaxThreads)
   // the row groups' sums, added in their order
   cp_async_wait<0>();
   __syncthreads();
-  float* sums = reinterpret_cast<float*>(ring_raw);  // [group][column]
-  const int32_t pitch = tpr * C * 8;
+  float* sums = reinterpret_cast<float*>(ring_raw);  // [group][8 + column]
+  const int32_t pitch = tpr * C * 8 + 8;
 #pragma unroll
   for (int c = 0; c < C; ++c)
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      *reinterpret_cast<float2*>(sums + sub * pitch + (t + c * tpr) * 8 + 2 * i) = dw[c][i];
+    for (int i = 0; i < 4; ++i) {
+      float* at = sums + sub * pitch + 8 + col0 + c * tpr * 8 + 2 * i;
+      if constexpr (R == ROWS_ALIKE) at[0] = dw[c][i].x, at[1] = dw[c][i].y;
+      else *reinterpret_cast<float2*>(at) = dw[c][i];
+    }
   __syncthreads();
-  for (int32_t col = threadIdx.x; col < cols; col += kMaxThreads) {
+  for (int32_t col = threadIdx.x; col < cols; col += blockDim.x) {
     float s = 0.f;
-    for (int g = 0; g < per_block; ++g) s += sums[g * pitch + col];
+    for (int g = 0; g < per_block; ++g) s += sums[g * pitch + 8 + col];
     p.partials[static_cast<int64_t>(blockIdx.x) * cols + col] = s;
   }
 }
@@ -599,13 +711,24 @@ __global__ void __launch_bounds__(1024)
   if (lane == 0 && blockIdx.x * 32 + warp < cols) dw[blockIdx.x * 32 + warp] = s;
 }
 
-template <typename T, int C, bool AL>
-cudaError_t launch_norm_bwd_c(const NormBwdParams& p, int tpr, int blocks, cudaStream_t st) {
+// Rows a block: row groups of several warps have a barrier each, of the 15 beside the
+// block's (64 threads a row or more leave 8 of them at most).
+int bwd_rows(int tpr) { return kBwdThreads / tpr; }
+
+template <typename T, int C, int R>
+cudaError_t launch_norm_bwd_r(const NormBwdParams& p, int tpr, int blocks, cudaStream_t st) {
   static std::atomic<size_t> set[64];
-  constexpr size_t smem = static_cast<size_t>(bwd_depth<T, C>()) * 32 * C * 3 * WarpRow<T>::kBytes;
-  const cudaError_t e = allow_smem(norm_bwd_kernel<T, C, AL>, set, smem);
+  constexpr size_t smem = static_cast<size_t>(bwd_depth<T, C>()) * (kBwdThreads / 32) * C * 3 * WarpRow<T>::kBytes;
+  const cudaError_t e = allow_smem(norm_bwd_kernel<T, C, R>, set, smem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(norm_bwd_kernel<T, C, AL>, dim3(blocks), dim3(kMaxThreads), smem, st, p, tpr);
+  return launch_pdl(norm_bwd_kernel<T, C, R>, dim3(blocks), dim3(bwd_rows(tpr) * tpr), smem, st, p, tpr);
+}
+
+template <typename T, int C>
+cudaError_t launch_norm_bwd_c(const NormBwdParams& p, int lie, int tpr, int blocks, cudaStream_t st) {
+  if (lie == ROWS_ALIGNED) return launch_norm_bwd_r<T, C, ROWS_ALIGNED>(p, tpr, blocks, st);
+  if (lie == ROWS_ALIKE) return launch_norm_bwd_r<T, C, ROWS_ALIKE>(p, tpr, blocks, st);
+  return launch_norm_bwd_r<T, C, ROWS_ANY>(p, tpr, blocks, st);
 }
 
 template <typename T>
@@ -615,15 +738,22 @@ cudaError_t launch_norm_bwd_t(const NormBwdParams& p, int sms, cudaStream_t st) 
   if (p.rows == 0) {
     // no rows: dw is zero
   } else if (p.cols <= kMaxCols) {
-    const RowShape s = row_shape((p.cols + 7) / 8, true);
-    const int64_t want = (p.rows + kMaxThreads / s.tpr - 1) / (kMaxThreads / s.tpr);
+    int lie = p.rows_lie;
+    int64_t chunks = (p.cols + 7) / 8;
+    if (lie == ROWS_ALIKE) {
+      const int64_t more = alike_chunks(p.cols, sizeof(T));
+      if (more * 8 <= kMaxCols && sms >= 8) chunks = more;
+      else lie = ROWS_ANY;
+    }
+    const int c = chunks > 2 * kBwdThreads ? 4 : (chunks > 32 ? 2 : 1);
+    const int tpr = static_cast<int>((chunks + 32 * c - 1) / (32 * c) * 32);
+    const int per = bwd_rows(tpr);
+    const int64_t want = (p.rows + per - 1) / per;
     if (want < blocks) blocks = static_cast<int>(want);
-    if (p.aligned)
-      e = s.c == 1 ? launch_norm_bwd_c<T, 1, true>(p, s.tpr, blocks, st)
-                   : launch_norm_bwd_c<T, 2, true>(p, s.tpr, blocks, st);
-    else
-      e = s.c == 1 ? launch_norm_bwd_c<T, 1, false>(p, s.tpr, blocks, st)
-                   : launch_norm_bwd_c<T, 2, false>(p, s.tpr, blocks, st);
+    if (lie == ROWS_ALIKE) blocks = alike_blocks(p.rows, per, blocks);
+    e = c == 1   ? launch_norm_bwd_c<T, 1>(p, lie, tpr, blocks, st)
+        : c == 2 ? launch_norm_bwd_c<T, 2>(p, lie, tpr, blocks, st)
+                 : launch_norm_bwd_c<T, 4>(p, lie, tpr, blocks, st);
     if (e != cudaSuccess) return e;
   } else {
     // dw first: dx may overwrite dy or h

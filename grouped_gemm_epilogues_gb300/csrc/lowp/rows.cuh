@@ -123,16 +123,55 @@ __device__ __forceinline__ Raw8<T> load_row8(const T* row, int32_t col, int32_t 
   return r;
 }
 
+// Values k to 7 of the 8 that belong at `at`, a 16-byte boundary; the first n of them.
+template <typename T>
+__device__ __forceinline__ void store_from(T* at, int32_t k, const Raw8<T>& v) {
+  if constexpr (sizeof(T) == 2) {
+    const uint4 w = v.w[0];
+    uint8_t* b = reinterpret_cast<uint8_t*>(at);
+    if (k & 1) {
+      const uint32_t x = (k & 4) ? ((k & 2) ? w.w : w.z) : ((k & 2) ? w.y : w.x);
+      *reinterpret_cast<uint16_t*>(b + 2 * k) = static_cast<uint16_t>(x >> 16);
+    }
+    const int32_t e = (k + 1) & ~1;  // 0, 2, .. 8
+    if (e & 2) *reinterpret_cast<uint32_t*>(b + 2 * e) = (e & 4) ? w.w : w.y;
+    if (e <= 4) {
+      *reinterpret_cast<uint2*>(b + 8) = make_uint2(w.z, w.w);
+      if (e == 0) *reinterpret_cast<uint2*>(b) = make_uint2(w.x, w.y);
+    }
+  } else {
+    const T* t = reinterpret_cast<const T*>(&v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i >= k) at[i] = t[i];
+  }
+}
+template <typename T>
+__device__ __forceinline__ void store_up_to(T* at, int32_t n, const Raw8<T>& v) {
+  if constexpr (sizeof(T) == 2) {
+    const uint4 w = v.w[0];
+    uint8_t* b = reinterpret_cast<uint8_t*>(at);
+    if (n & 4) *reinterpret_cast<uint2*>(b) = make_uint2(w.x, w.y);
+    if (n & 2) *reinterpret_cast<uint32_t*>(b + 2 * (n & 4)) = (n & 4) ? w.z : w.x;
+    if (n & 1) {
+      const uint32_t x = (n & 4) ? ((n & 2) ? w.w : w.z) : ((n & 2) ? w.y : w.x);
+      *reinterpret_cast<uint16_t*>(b + 2 * (n & 6)) = static_cast<uint16_t>(x);
+    }
+  } else {
+    const T* t = reinterpret_cast<const T*>(&v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) at[i] = t[i];
+  }
+}
+
 // Eight values in 16-byte pieces where the row allows it, for a lane on its own.
 template <typename T>
 __device__ __forceinline__ void store_row8_aligned(T* row, int32_t col, int32_t cols, const Raw8<T>& v) {
   if (col + 8 <= cols) {
     store8(row + col, v);
-  } else {
-    const T* t = reinterpret_cast<const T*>(&v);
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (col + i < cols) row[col + i] = t[i];
+  } else if (col < cols) {
+    store_up_to(row + col, cols - col, v);
   }
 }
 

@@ -232,3 +232,73 @@ def test_norm_streams_and_graph():
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(outs[0], outs[1]) and torch.equal(outs[1], outs[2])
+
+
+# Rows a row group takes one after the other, on no particular boundary: starting at
+# the same place in every tensor (one offset), or not (several).
+MANY = [(9999, 77), (5000, 1003), (1300, 4099), (700, 8185)]
+OFFSETS = [(0, 0, 0, 0), (5, 5, 5, 5), (1, 3, 0, 6)]
+
+
+@pytest.mark.parametrize("rows,cols", MANY)
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("offsets", OFFSETS)
+def test_forward_many_rows(rows, cols, dtype, offsets):
+    x, r = (_rand(rows, cols, dtype, 21 + i, offsets[i]) for i in (0, 1))
+    w = _rand(1, cols, dtype, 25)[0]
+    h, y = (torch.full((rows, cols + o + 16), 9.0, dtype=dtype, device=DEV) for o in offsets[2:])
+    hv, yv = h[:, offsets[2]:][:, :cols], y[:, offsets[3]:][:, :cols]
+    inv = torch.empty(rows, device=DEV)
+    gge.gge_rmsnorm(x, w, Y=yv, residual=r, residual_out=hv, inv_rms=inv, eps=EPS)
+    rh, rinv, ry = lowp.rmsnorm(dec(x), dec(w), EPS, dec(r), FMT[dtype])
+    assert np.array_equal(dec(hv), rh)
+    _near(inv, rinv, REL, "inv")
+    _near(yv, ry, REL, "y")
+    for t, o in ((h, offsets[2]), (y, offsets[3])):
+        assert (t[:, :o] == 9.0).all() and (t[:, cols + o:] == 9.0).all()
+
+
+@pytest.mark.parametrize("rows,cols", MANY)
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("pad", [0, 8, 3])
+def test_forward_many_rows_alone(rows, cols, dtype, pad):
+    """x to y without a residual; y's rows `pad` elements wider than x's."""
+    x, w = _rand(rows, cols, dtype, 31), _rand(1, cols, torch.float32, 32)[0]
+    y = torch.full((rows, cols + pad), 9.0, dtype=dtype, device=DEV)
+    gge.gge_rmsnorm(x, w, Y=y[:, :cols], eps=EPS)
+    _, _, ry = lowp.rmsnorm(dec(x), dec(w), EPS, None, FMT[dtype])
+    _near(y[:, :cols], ry, REL, "y")
+    assert (y[:, cols:] == 9.0).all()
+
+
+@pytest.mark.parametrize("cols", [77, 1000, 1003])
+@pytest.mark.parametrize("offset", [0, 3])
+def test_one_residual_row_for_all(cols, offset):
+    x, w = _rand(3000, cols, torch.bfloat16, 41, offset), _rand(1, cols, torch.bfloat16, 42)[0]
+    r = _rand(1, cols, torch.bfloat16, 43, offset).expand(3000, cols)
+    h, y = torch.empty(3000, cols, dtype=torch.bfloat16, device=DEV), torch.empty_like(x)
+    gge.gge_rmsnorm(x, w, Y=y, residual=r, residual_out=h, eps=EPS)
+    rh, _, ry = lowp.rmsnorm(dec(x), dec(w), EPS, dec(r), FMT[torch.bfloat16])
+    assert np.array_equal(dec(h), rh)
+    _near(y, ry, REL, "y")
+
+
+@pytest.mark.parametrize("rows,cols", MANY + [(400, 8193), (400, 12001)])
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("offsets", OFFSETS)
+def test_backward_many_rows(rows, cols, dtype, offsets):
+    dy, h, dh = (_rand(rows, cols, dtype, 51 + i, offsets[i]) for i in range(3))
+    w = _rand(1, cols, dtype, 55)[0]
+    inv = torch.rsqrt(h.float().square().mean(1) + EPS)
+    dx = torch.full((rows, cols + offsets[3]), 9.0, dtype=dtype, device=DEV)
+    dw = torch.full((cols,), float("nan"), device=DEV)
+    gge.gge_rmsnorm_bwd(dy, h, w, inv, dx[:, offsets[3]:], dW=dw, dH=dh)
+    a, b, wv, iv = dec(dy), dec(h), dec(w), dec(inv)
+    rdx, rdw = lowp.rmsnorm_bwd(a, b, wv, iv, dec(dh))
+    assert (dx[:, :offsets[3]] == 9.0).all()
+    i = iv[:, None]
+    size = np.abs(i * a * wv) + np.abs(i * b) * i * i * (np.abs(a * wv) * np.abs(b)).mean(1, keepdims=True) + np.abs(dec(dh))
+    assert (np.abs(dec(dx[:, offsets[3]:]) - rdx) <= REL * size + formats.quantum(rdx, FMT[dtype])).all()
+    steps = (rows + 151) // 152 + 152 + 32
+    tol = (steps * 2.0 ** -24 + 2.0 ** -22) * np.abs(a * b * i).sum(0) + formats.quantum(rdw, formats.F32)
+    assert (np.abs(dec(dw) - rdw) <= tol).all()
