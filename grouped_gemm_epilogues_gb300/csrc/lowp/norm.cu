@@ -13,13 +13,12 @@
 // Both are bound by memory.  Blocks walk the rows with a grid stride; cp.async
 // keeps the next rows on their way to shared memory while a row is reduced in
 // registers and written, so every value is read once.  What limits them beside the
-// DRAM is instruction issue, hence the packed fp32 operations and, where every row
-// starts on a 16-byte boundary, a form (AL) without the shifting of rows.cuh.
-// Measured: bf16 16384 x 8192 with residual, mxfp8 and its values 190 us (6.4 TB/s,
-// 95 % of a copy's rate; the first version, without copies ahead and packed
-// arithmetic, 273); rows of 1999 fp16 values, which start anywhere, 2.7 TB/s, bound by
-// issue.  Two chunks a thread against one: 47 and 58 us for 16000 x 1999; four 50.
-// Backward 16384 x 4096 with dh 92 us (5.8 TB/s, 87 %).
+// DRAM is instruction issue, hence the packed fp32 operations and, where the rows' place
+// in memory allows it, forms without the shifting of rows.cuh (Rows).  Measured: bf16
+// 16384 x 8192 with residual, mxfp8 and its values 190 us (6.4 TB/s, 95 % of a copy's
+// rate; the first version, without copies ahead and packed arithmetic, 273).  Rows that
+// start on any 2 bytes, fp16 16000 x 1999: 26 us alike (4.9 TB/s), 40 shifted.  Backward 16384
+// x 4096 with dh 85 us (6.3 TB/s, 94 %), bf16 24000 x 1999 70 us (5.5 TB/s).
 #include <atomic>
 #include <numeric>
 
@@ -33,6 +32,15 @@ namespace {
 using namespace mx;
 
 constexpr int kMaxThreads = 1024;
+// Where the weights (and dw) stay in registers with the row, over its sum, a block has
+// half the threads with twice the registers, and up to four chunks of 8 values each.
+constexpr int kRowThreads = 512;
+
+// Rows of `bytes` in an SM's shared memory: the one at work and those on their way.
+// (A depth known at run time only, up to eight rows: 10 % slower for 8000 x 4096.)
+constexpr int ring_depth(int bytes, int most) {
+  return 210 * 1024 / bytes < most ? 210 * 1024 / bytes : most;
+}
 constexpr int kMaxCols = kMaxThreads * 2 * 8;  // longer rows take the *_long kernels
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -122,13 +130,13 @@ struct RowReader {
   }
   // Copy chunk c (`over` columns after chunk 0) of that row to this warp's `dst`.
   // `first`: nothing may be read in front of the row.
-  __device__ __forceinline__ void copy(uint32_t dst, int32_t col, int32_t over, int32_t cols,
+  __device__ __forceinline__ void copy(uint32_t dst, int32_t col, int32_t c, int32_t over, int32_t cols,
                                        bool first) const {
     constexpr int P = WarpRow<T>::kPieces;
     const int lane = threadIdx.x & 31;
     const int32_t left = (cols - col) * static_cast<int32_t>(sizeof(T));
     if constexpr (R != ROWS_ANY) {
-      if (R == ROWS_ALIKE && first && col < 0) {  // (one thread of the launch's first rows)
+      if (R == ROWS_ALIKE && c == 0 && first && col < 0) {  // (one thread of the launch's first rows)
         const T* at = next + over;
         for (int32_t i = -col; i < min(static_cast<int32_t>(16 / sizeof(T)), cols - col); ++i) {
           if constexpr (sizeof(T) == 2)
@@ -139,7 +147,7 @@ struct RowReader {
       }
 #pragma unroll
       for (int j = 0; j < P; ++j) {
-        if (R == ROWS_ALIKE && j == 0 && first && col < 0) continue;
+        if (R == ROWS_ALIKE && c == 0 && j == 0 && first && col < 0) continue;
         // (bytes past the row's end are zero-filled; none are read)
         if (left > 16 * j)
           ptx::cp_async_16(dst + 16u * (lane * P + j), next + over + j * (16 / sizeof(T)),
@@ -151,16 +159,16 @@ struct RowReader {
   }
 };
 
-// A lane's 8 values of a copied chunk of the row that starts at `row`; zeros where the
+// A lane's 8 values of the copied chunk c of the row that starts at `row`; zeros where the
 // chunk leaves the row.
 template <typename T, int R>
-__device__ __forceinline__ Raw8<T> take_chunk(uint32_t src, const T* row, int32_t col, int32_t cols) {
+__device__ __forceinline__ Raw8<T> take_chunk(uint32_t src, int32_t c, const T* row, int32_t col, int32_t cols) {
   constexpr int P = WarpRow<T>::kPieces;
   if constexpr (R != ROWS_ANY) {
     Raw8<T> r;
 #pragma unroll
     for (int j = 0; j < P; ++j) r.w[j] = ptx::ld_shared_v4(src + 16u * ((threadIdx.x & 31) * P + j));
-    if (R == ROWS_ALIKE && col < 0) {
+    if (R == ROWS_ALIKE && c == 0 && col < 0) {
       clear_front(r, -col);
       clear_past(r, col, cols);
     }
@@ -173,8 +181,8 @@ __device__ __forceinline__ Raw8<T> take_chunk(uint32_t src, const T* row, int32_
 }
 
 template <typename T, int R>
-__device__ __forceinline__ void put_chunk(T* row, int32_t col, int32_t cols, const Raw8<T>& v) {
-  if (R == ROWS_ALIKE && col < 0) {
+__device__ __forceinline__ void put_chunk(T* row, int32_t c, int32_t col, int32_t cols, const Raw8<T>& v) {
+  if (R == ROWS_ALIKE && c == 0 && col < 0) {
     if (col + 8 <= cols) {
       store_from(row + col, -col, v);
     } else {  // (a row shorter than 8)
@@ -200,33 +208,43 @@ int alike_blocks(int64_t rows, int per_block, int64_t blocks) {
 
 // ------------------------------------------------------------ forward
 
-// Rows in shared memory: the one at work and, where it fits, the next.
-template <typename T, int C>
+// Threads a block has at most.  ALIKE's weights stay in registers.  The others take
+// them from L1 again for each row: with codes, more warps are worth more (mxfp8 16384 x
+// 8192 with residual 190 us, with 512 threads and the weights in registers 258; ALIKE,
+// bf16 24000 x 1999 with residual, 83 and 64).
+template <int R>
+constexpr int norm_threads() {
+  return R == ROWS_ALIKE ? kRowThreads : kMaxThreads;
+}
+
+// Rows in shared memory: in ALIKE, which has half the rows at work, up to four.
+template <typename T, int C, int R>
 constexpr int norm_depth() {
-  return sizeof(T) == 4 && C == 2 ? 1 : 2;
+  return ring_depth(norm_threads<R>() / 32 * C * 2 * WarpRow<T>::kBytes, R == ROWS_ALIKE ? 4 : 2);
 }
 
 // A row is spread over `tpr` threads; thread i holds the 8-value chunks i, i + tpr, ...
 // The block's row groups run on their own: what they share is shared memory's size.
 template <typename T, int C, int FMT, int R>
-__global__ void __launch_bounds__(kMaxThreads)
+__global__ void __launch_bounds__(norm_threads<R>())
     norm_kernel(const __grid_constant__ NormParams p, int tpr) {
   __shared__ float slots[64];
   extern __shared__ uint8_t ring_raw[];
   ptx::griddep_launch_dependents();
-  constexpr int D = norm_depth<T, C>();
   const int per_block = blockDim.x / tpr;
   const int sub = threadIdx.x / tpr, t = threadIdx.x % tpr;
   const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   const int32_t cols = p.cols;
+  constexpr int D = norm_depth<T, C, R>();
+  const bool has_res = p.residual != nullptr;
   // this warp's buffers: [row in flight][chunk][x, residual]
   constexpr uint32_t kBuf = WarpRow<T>::kBytes;
-  const uint32_t ring = ptx::smem_addr(ring_raw) + (threadIdx.x >> 5) * (C * 2 * kBuf);
-  const uint32_t ring_row = warps * (C * 2 * kBuf);
+  constexpr uint32_t kRow = 2 * C * kBuf;
+  const uint32_t ring = ptx::smem_addr(ring_raw) + (threadIdx.x >> 5) * kRow;
+  const uint32_t ring_row = warps * kRow;
   const uint32_t rows = static_cast<uint32_t>(p.rows);  // (below 2^31, and so is a step past them)
   const uint32_t step = gridDim.x * per_block;
   uint32_t row = blockIdx.x * per_block + sub;
-  const bool has_res = p.residual != nullptr;
   RowReader<T, R> x, res;
   const int32_t skew = R == ROWS_ALIKE ? row_skew<T>(static_cast<const T*>(p.x) + row * p.ldx) : 0;
   const int32_t col0 = t * 8 - skew;         // chunk 0's first column
@@ -250,8 +268,8 @@ __global__ void __launch_bounds__(kMaxThreads)
       for (int c = 0; c < C; ++c) {
         const uint32_t dst = ring + slot * ring_row + c * 2 * kBuf;
         const int32_t over = c * tpr * 8;
-        x.copy(dst, col0 + over, over, cols, ahead * p.ldx < 8);
-        if (has_res) res.copy(dst + kBuf, col0 + over, over, cols, ahead * p.ldr < 8);
+        x.copy(dst, col0 + over, c, over, cols, ahead * p.ldx < 8);
+        if (has_res) res.copy(dst + kBuf, col0 + over, c, over, cols, ahead * p.ldr < 8);
       }
       x.next += static_cast<int64_t>(step) * p.ldx;
       res.next += static_cast<int64_t>(step) * p.ldr;
@@ -274,11 +292,11 @@ __global__ void __launch_bounds__(kMaxThreads)
     for (int c = 0; c < C; ++c) {
       const int32_t col = col0 + c * tpr * 8;
       const uint32_t src = ring + slot * ring_row + c * 2 * kBuf;
-      h[c] = take_chunk<T, R>(src, static_cast<const T*>(p.x) + row * p.ldx, col, cols);
+      h[c] = take_chunk<T, R>(src, c, static_cast<const T*>(p.x) + row * p.ldx, col, cols);
       if (has_res) {
-        h[c] = add8(h[c], take_chunk<T, R>(src + kBuf, static_cast<const T*>(p.residual) + row * p.ldr, col, cols));
+        h[c] = add8(h[c], take_chunk<T, R>(src + kBuf, c, static_cast<const T*>(p.residual) + row * p.ldr, col, cols));
         if (p.h != nullptr && warp_col + c * tpr * 8 < cols)
-          put_chunk<T, R>(static_cast<T*>(p.h) + row * p.ldh, col, cols, h[c]);
+          put_chunk<T, R>(static_cast<T*>(p.h) + row * p.ldh, c, col, cols, h[c]);
       }
       float2 v[4];
       widen(h[c], v);
@@ -306,7 +324,7 @@ __global__ void __launch_bounds__(kMaxThreads)
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         v[i] = __fmul2_rn(__fmul2_rn(v[i], make_float2(inv, inv)), R == ROWS_ALIKE ? wk[c][i] : w[i]);
-      if (p.y != nullptr) put_chunk<T, R>(static_cast<T*>(p.y) + row * p.ldy, col, cols, narrow<T>(v));
+      if (p.y != nullptr) put_chunk<T, R>(static_cast<T*>(p.y) + row * p.ldy, c, col, cols, narrow<T>(v));
       if constexpr (FMT != FMT_NONE) {
         constexpr int B = Fmt<FMT>::kBlock;
         const Quantised z = quantise8<FMT>(v, tscale, col >= (cols + B - 1) / B * B);
@@ -405,53 +423,56 @@ __global__ void norm_long_kernel(const __grid_constant__ NormParams p) {
   }
 }
 
-// Threads a row of `chunks` 8-value chunks (whole warps), and chunks a thread (1 or 2).
+// How a row is spread: chunks a thread, threads a row (whole warps), rows a block, and
+// blocks an SM.  Row groups of several warps have a barrier each, of the 15 beside the
+// block's.
 struct RowShape {
-  int tpr, c;
+  int c, tpr, per, blocks;
 };
-RowShape row_shape(int64_t chunks, bool few) {
-  const int c = chunks > (few ? kMaxThreads : 32) ? 2 : 1;
-  const int tpr = static_cast<int>((chunks + 32 * c - 1) / (32 * c) * 32);
-  return {tpr, c};
+int whole_warps(int64_t chunks, int c) { return static_cast<int>((chunks + 32 * c - 1) / (32 * c) * 32); }
+
+// ... with up to 64 registers a thread: blocks such that as many rows as possible are at
+// work.  An SM has four quarters of 8 such warps, and a block's warps go round them.
+// (1536 columns, 96 threads a row: 5 rows a block, twice, 34 us for 48 M values; 2 rows
+// a block, which leaves room for four blocks, 46.)  Few rows have one chunk a thread
+// (latency); many two, so that a row's barrier costs less.
+RowShape many_threads(int64_t chunks, bool few) {
+  RowShape s{chunks > (few ? kMaxThreads : 32) ? 2 : 1, 0, 0, 0};
+  s.tpr = whole_warps(chunks, s.c);
+  for (int per = 1; per * s.tpr <= kMaxThreads && (s.tpr == 32 || per <= 15); ++per) {
+    const int warps = per * s.tpr / 32;
+    const int blocks = 8 / ((warps + 3) / 4);
+    const int now = per * blocks, best = s.per * s.blocks;
+    // (blocks below 256 threads were slower at the same number of rows; above, alike)
+    if (now > best || (now == best && s.per * s.tpr < 256)) s.per = per, s.blocks = blocks;
+  }
+  return s;
 }
 
-// Rows a block, and blocks an SM, such that as many rows as possible are at work: an
-// SM has four quarters of 8 warps of 64 registers a thread, and a block's warps go
-// round them.  Row groups of several warps have a barrier each, of the 15 beside the
-// block's.  (1536 columns, 96 threads a row: 5 rows a block, twice, 34 us for 48 M
-// values; 2 rows a block, which leaves room for four blocks, 46.)
-struct BlockShape {
-  int per, blocks;
-};
-BlockShape block_shape(int tpr) {
-  BlockShape best{0, 0};
-  for (int per = 1; per * tpr <= kMaxThreads && (tpr == 32 || per <= 15); ++per) {
-    const int warps = per * tpr / 32;
-    const int blocks = 8 / ((warps + 3) / 4);
-    // (blocks below 256 threads were slower at the same number of rows; above, alike)
-    const bool more = per * blocks > best.per * best.blocks;
-    if (more || (per * blocks == best.per * best.blocks && best.per * tpr < 256)) best = {per, blocks};
-  }
-  return best;
+// ... with up to 128: one block.  Rows of more than `two` chunks have four a thread.
+RowShape many_registers(int64_t chunks, int64_t two) {
+  RowShape s{chunks > two ? 4 : (chunks > 32 ? 2 : 1), 0, 0, 1};
+  s.tpr = whole_warps(chunks, s.c);
+  s.per = kRowThreads / s.tpr;
+  return s;
 }
 
 // Chunks of a row of `cols` values that starts at any skew.
 int64_t alike_chunks(int64_t cols, int value_bytes) { return (cols + 16 / value_bytes - 1 + 7) / 8; }
 
 template <typename T, int C, int FMT, int R>
-cudaError_t launch_norm_c(const NormParams& p, int tpr, int sms, cudaStream_t st) {
+cudaError_t launch_norm_c(const NormParams& p, const RowShape& s, int sms, cudaStream_t st) {
   static std::atomic<size_t> set[64];
-  const BlockShape shape = block_shape(tpr);
-  const int per = shape.per, block = per * tpr;
-  const size_t smem = static_cast<size_t>(norm_depth<T, C>()) * (block / 32) * C * 2 * WarpRow<T>::kBytes;
+  const int block = s.per * s.tpr;
+  const size_t smem = static_cast<size_t>(norm_depth<T, C, R>()) * (block / 32) * C * 2 * WarpRow<T>::kBytes;
   const cudaError_t e = allow_smem(norm_kernel<T, C, FMT, R>, set, smem);
   if (e != cudaSuccess) return e;
   // as many blocks as an SM holds, each with its share of the rows
-  const int64_t resident = static_cast<int64_t>(sms) * shape.blocks;
-  const int64_t want = (p.rows + per - 1) / per;
+  const int64_t resident = static_cast<int64_t>(sms) * s.blocks;
+  const int64_t want = (p.rows + s.per - 1) / s.per;
   int blocks = static_cast<int>(want < resident ? want : resident);
-  if (R == ROWS_ALIKE) blocks = alike_blocks(p.rows, per, blocks);
-  return launch_pdl(norm_kernel<T, C, FMT, R>, dim3(blocks), dim3(block), smem, st, p, tpr);
+  if (R == ROWS_ALIKE) blocks = alike_blocks(p.rows, s.per, blocks);
+  return launch_pdl(norm_kernel<T, C, FMT, R>, dim3(blocks), dim3(block), smem, st, p, s.tpr);
 }
 
 template <typename T, int FMT>
@@ -459,21 +480,23 @@ cudaError_t launch_norm_t(const NormParams& p, int sms, cudaStream_t st) {
   const int64_t group = FMT == FMT_NONE ? 8 : Fmt<FMT == FMT_NONE ? 0 : FMT>::kGroup;
   const int64_t span = (p.cols + group - 1) / group * group;
   if (span <= kMaxCols) {
-    // few rows: one chunk a thread (latency); many: two, so that a row's barrier costs less
-    const RowShape s = row_shape(span / 8, p.rows <= sms);
-    if (p.rows_lie == ROWS_ALIGNED)
-      return s.c == 1 ? launch_norm_c<T, 1, FMT, ROWS_ALIGNED>(p, s.tpr, sms, st)
-                      : launch_norm_c<T, 2, FMT, ROWS_ALIGNED>(p, s.tpr, sms, st);
     if constexpr (FMT == FMT_NONE) {
       const int64_t chunks = alike_chunks(p.cols, sizeof(T));
       if (p.rows_lie == ROWS_ALIKE && chunks * 8 <= kMaxCols && sms >= 8) {
-        const RowShape a = row_shape(chunks, p.rows <= sms);
-        return a.c == 1 ? launch_norm_c<T, 1, FMT, ROWS_ALIKE>(p, a.tpr, sms, st)
-                        : launch_norm_c<T, 2, FMT, ROWS_ALIKE>(p, a.tpr, sms, st);
+        // (16 bits, 24000 x 1999, two and four: 49 and 35 us, with residual 69 and 66; 48000 x
+        // 1003 49 and 36; fp32 12000 x 1999 38 and 38, with residual 66 and 71)
+        const RowShape s = many_registers(chunks, sizeof(T) == 2 ? 64 : 2 * kRowThreads);
+        return s.c == 1   ? launch_norm_c<T, 1, FMT, ROWS_ALIKE>(p, s, sms, st)
+               : s.c == 2 ? launch_norm_c<T, 2, FMT, ROWS_ALIKE>(p, s, sms, st)
+                          : launch_norm_c<T, 4, FMT, ROWS_ALIKE>(p, s, sms, st);
       }
     }
-    return s.c == 1 ? launch_norm_c<T, 1, FMT, ROWS_ANY>(p, s.tpr, sms, st)
-                    : launch_norm_c<T, 2, FMT, ROWS_ANY>(p, s.tpr, sms, st);
+    const RowShape s = many_threads(span / 8, p.rows <= sms);
+    if (p.rows_lie == ROWS_ALIGNED)
+      return s.c == 1 ? launch_norm_c<T, 1, FMT, ROWS_ALIGNED>(p, s, sms, st)
+                      : launch_norm_c<T, 2, FMT, ROWS_ALIGNED>(p, s, sms, st);
+    return s.c == 1 ? launch_norm_c<T, 1, FMT, ROWS_ANY>(p, s, sms, st)
+                    : launch_norm_c<T, 2, FMT, ROWS_ANY>(p, s, sms, st);
   }
   return launch_pdl(norm_long_kernel<T, FMT>,
                     dim3(static_cast<unsigned>(p.rows < 65536 ? p.rows : 65536)), dim3(kMaxThreads), 0, st, p);
@@ -491,27 +514,22 @@ cudaError_t launch_norm_f(const NormParams& p, int sms, cudaStream_t st) {
 
 // ----------------------------------------------------------- backward
 
-// dw, the weights and a row stay in registers over the row's sum, so a block has few
-// threads with many registers, and up to four chunks a thread.
-constexpr int kBwdThreads = 512;
-
-// Rows in shared memory: what fits beside each other for a whole block.
-template <typename T, int C>
+// Rows in shared memory (bf16 8000 x 4096 with dh, three and four: 46.2 and 47.3 us;
+// 24000 x 1999 80 and 70).
+template <typename T, int C, int R>
 constexpr int bwd_depth() {
-  const int row = kBwdThreads / 32 * C * 3 * WarpRow<T>::kBytes;
-  return 3 * row <= 210 * 1024 ? 3 : (2 * row <= 210 * 1024 ? 2 : 1);
+  return ring_depth(kRowThreads / 32 * C * 3 * WarpRow<T>::kBytes, R == ROWS_ALIKE ? 4 : 3);
 }
 
 // A block takes as many rows at a time as its threads hold.  Each thread keeps its
 // columns' share of dw in registers; at the end the block's row groups add theirs
 // up and leave one row of partial sums.
 template <typename T, int C, int R>
-__global__ void __launch_bounds__(kBwdThreads)
+__global__ void __launch_bounds__(kRowThreads)
     norm_bwd_kernel(const __grid_constant__ NormBwdParams p, int tpr) {
   __shared__ float slots[64];
   extern __shared__ uint8_t ring_raw[];
   ptx::griddep_launch_dependents();
-  constexpr int D = bwd_depth<T, C>();
   // g and h stay in registers over the row's sum, or are made again from shared memory
   constexpr bool kKeep = C < 4;
   const int per_block = blockDim.x / tpr;
@@ -519,12 +537,15 @@ __global__ void __launch_bounds__(kBwdThreads)
   const int lane = threadIdx.x & 31;
   const int32_t cols = p.cols;
   constexpr uint32_t kBuf = WarpRow<T>::kBytes;
-  const uint32_t ring_row = (blockDim.x >> 5) * (C * 3 * kBuf);
-  const uint32_t ring = ptx::smem_addr(ring_raw) + (threadIdx.x >> 5) * (C * 3 * kBuf);
+  constexpr int D = bwd_depth<T, C, R>();
+  const bool has_dh = p.dh != nullptr;
+  // this warp's buffers: [row in flight][chunk][dy, h, dh]
+  constexpr uint32_t kRow = 3 * C * kBuf;
+  const uint32_t ring = ptx::smem_addr(ring_raw) + (threadIdx.x >> 5) * kRow;
+  const uint32_t ring_row = (blockDim.x >> 5) * kRow;
   const uint32_t rows = static_cast<uint32_t>(p.rows);  // (below 2^31, and so is a step past them)
   const uint32_t step = gridDim.x * per_block;
   uint32_t row = blockIdx.x * per_block + sub;
-  const bool has_dh = p.dh != nullptr;
   RowReader<T, R> dy, h, dh;
   const int32_t skew = R == ROWS_ALIKE ? row_skew<T>(static_cast<const T*>(p.h) + row * p.ldh) : 0;
   const int32_t col0 = t * 8 - skew;         // chunk 0's first column
@@ -552,9 +573,9 @@ __global__ void __launch_bounds__(kBwdThreads)
       for (int c = 0; c < C; ++c) {
         const uint32_t dst = ring + slot * ring_row + c * 3 * kBuf;
         const int32_t over = c * tpr * 8, col = col0 + over;
-        dy.copy(dst, col, over, cols, ahead * p.lddy < 8);
-        h.copy(dst + kBuf, col, over, cols, ahead * p.ldh < 8);
-        if (has_dh) dh.copy(dst + 2 * kBuf, col, over, cols, ahead * p.lddh < 8);
+        dy.copy(dst, col, c, over, cols, ahead * p.lddy < 8);
+        h.copy(dst + kBuf, col, c, over, cols, ahead * p.ldh < 8);
+        if (has_dh) dh.copy(dst + 2 * kBuf, col, c, over, cols, ahead * p.lddh < 8);
       }
       dy.next += static_cast<int64_t>(step) * p.lddy;
       h.next += static_cast<int64_t>(step) * p.ldh;
@@ -585,9 +606,9 @@ __global__ void __launch_bounds__(kBwdThreads)
       const int32_t col = col0 + c * tpr * 8;
       float2 hv[4];
       float2(&z)[4] = g[kKeep ? c : 0];
-      widen(take_chunk<T, R>(src + c * 3 * kBuf, static_cast<const T*>(p.dy) + row * p.lddy, col, cols), z);
+      widen(take_chunk<T, R>(src + c * 3 * kBuf, c, static_cast<const T*>(p.dy) + row * p.lddy, col, cols), z);
       Raw8<T>& raw = hr[kKeep ? c : 0];
-      raw = take_chunk<T, R>(src + c * 3 * kBuf + kBuf, static_cast<const T*>(p.h) + row * p.ldh, col, cols);
+      raw = take_chunk<T, R>(src + c * 3 * kBuf + kBuf, c, static_cast<const T*>(p.h) + row * p.ldh, col, cols);
       widen(raw, hv);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -606,8 +627,8 @@ __global__ void __launch_bounds__(kBwdThreads)
       float2 v[4];
       float2(&z)[4] = g[kKeep ? c : 0];
       if constexpr (!kKeep) {
-        hr[0] = take_chunk<T, R>(src + c * 3 * kBuf + kBuf, static_cast<const T*>(p.h) + row * p.ldh, col, cols);
-        widen(take_chunk<T, R>(src + c * 3 * kBuf, static_cast<const T*>(p.dy) + row * p.lddy, col, cols), z);
+        hr[0] = take_chunk<T, R>(src + c * 3 * kBuf + kBuf, c, static_cast<const T*>(p.h) + row * p.ldh, col, cols);
+        widen(take_chunk<T, R>(src + c * 3 * kBuf, c, static_cast<const T*>(p.dy) + row * p.lddy, col, cols), z);
 #pragma unroll
         for (int i = 0; i < 4; ++i) z[i] = __fmul2_rn(z[i], w[c][i]);
       }
@@ -615,11 +636,11 @@ __global__ void __launch_bounds__(kBwdThreads)
 #pragma unroll
       for (int i = 0; i < 4; ++i) z[i] = __fmul2_rn(inv2, __ffma2_rn(v[i], make_float2(k, k), z[i]));
       if (has_dh) {
-        widen(take_chunk<T, R>(src + c * 3 * kBuf + 2 * kBuf, static_cast<const T*>(p.dh) + row * p.lddh, col, cols), v);
+        widen(take_chunk<T, R>(src + c * 3 * kBuf + 2 * kBuf, c, static_cast<const T*>(p.dh) + row * p.lddh, col, cols), v);
 #pragma unroll
         for (int i = 0; i < 4; ++i) z[i] = __fadd2_rn(z[i], v[i]);
       }
-      put_chunk<T, R>(static_cast<T*>(p.dx) + row * p.lddx, col, cols, narrow<T>(z));
+      put_chunk<T, R>(static_cast<T*>(p.dx) + row * p.lddx, c, col, cols, narrow<T>(z));
     }
     slot = (slot + 1) % D;
   }
@@ -711,24 +732,20 @@ __global__ void __launch_bounds__(1024)
   if (lane == 0 && blockIdx.x * 32 + warp < cols) dw[blockIdx.x * 32 + warp] = s;
 }
 
-// Rows a block: row groups of several warps have a barrier each, of the 15 beside the
-// block's (64 threads a row or more leave 8 of them at most).
-int bwd_rows(int tpr) { return kBwdThreads / tpr; }
-
 template <typename T, int C, int R>
-cudaError_t launch_norm_bwd_r(const NormBwdParams& p, int tpr, int blocks, cudaStream_t st) {
+cudaError_t launch_norm_bwd_r(const NormBwdParams& p, const RowShape& s, int blocks, cudaStream_t st) {
   static std::atomic<size_t> set[64];
-  constexpr size_t smem = static_cast<size_t>(bwd_depth<T, C>()) * (kBwdThreads / 32) * C * 3 * WarpRow<T>::kBytes;
+  constexpr size_t smem = static_cast<size_t>(bwd_depth<T, C, R>()) * (kRowThreads / 32) * C * 3 * WarpRow<T>::kBytes;
   const cudaError_t e = allow_smem(norm_bwd_kernel<T, C, R>, set, smem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(norm_bwd_kernel<T, C, R>, dim3(blocks), dim3(bwd_rows(tpr) * tpr), smem, st, p, tpr);
+  return launch_pdl(norm_bwd_kernel<T, C, R>, dim3(blocks), dim3(s.per * s.tpr), smem, st, p, s.tpr);
 }
 
 template <typename T, int C>
-cudaError_t launch_norm_bwd_c(const NormBwdParams& p, int lie, int tpr, int blocks, cudaStream_t st) {
-  if (lie == ROWS_ALIGNED) return launch_norm_bwd_r<T, C, ROWS_ALIGNED>(p, tpr, blocks, st);
-  if (lie == ROWS_ALIKE) return launch_norm_bwd_r<T, C, ROWS_ALIKE>(p, tpr, blocks, st);
-  return launch_norm_bwd_r<T, C, ROWS_ANY>(p, tpr, blocks, st);
+cudaError_t launch_norm_bwd_c(const NormBwdParams& p, int lie, const RowShape& s, int blocks, cudaStream_t st) {
+  if (lie == ROWS_ALIGNED) return launch_norm_bwd_r<T, C, ROWS_ALIGNED>(p, s, blocks, st);
+  if (lie == ROWS_ALIKE) return launch_norm_bwd_r<T, C, ROWS_ALIKE>(p, s, blocks, st);
+  return launch_norm_bwd_r<T, C, ROWS_ANY>(p, s, blocks, st);
 }
 
 template <typename T>
@@ -745,15 +762,18 @@ cudaError_t launch_norm_bwd_t(const NormBwdParams& p, int sms, cudaStream_t st) 
       if (more * 8 <= kMaxCols && sms >= 8) chunks = more;
       else lie = ROWS_ANY;
     }
-    const int c = chunks > 2 * kBwdThreads ? 4 : (chunks > 32 ? 2 : 1);
-    const int tpr = static_cast<int>((chunks + 32 * c - 1) / (32 * c) * 32);
-    const int per = bwd_rows(tpr);
-    const int64_t want = (p.rows + per - 1) / per;
+    // From 513 chunks on, two a thread leave a block with one row at work and nothing to do
+    // while its sum comes together; four leave two or three, but fewer on their way.  In 16
+    // bits that is better for three (8000 x 5120 65 to 62 us, 8192 columns 49 to 54), and in
+    // ALIKE, where a row's ends take longer (12000 x 4097 108 to 79 us; 1999 columns 70 to 73).
+    const bool four = sizeof(T) == 2 && (lie == ROWS_ALIKE || whole_warps(chunks, 4) * 3 <= kRowThreads);
+    const RowShape s = many_registers(chunks, four ? kRowThreads : 2 * kRowThreads);
+    const int64_t want = (p.rows + s.per - 1) / s.per;
     if (want < blocks) blocks = static_cast<int>(want);
-    if (lie == ROWS_ALIKE) blocks = alike_blocks(p.rows, per, blocks);
-    e = c == 1   ? launch_norm_bwd_c<T, 1>(p, lie, tpr, blocks, st)
-        : c == 2 ? launch_norm_bwd_c<T, 2>(p, lie, tpr, blocks, st)
-                 : launch_norm_bwd_c<T, 4>(p, lie, tpr, blocks, st);
+    if (lie == ROWS_ALIKE) blocks = alike_blocks(p.rows, s.per, blocks);
+    e = s.c == 1   ? launch_norm_bwd_c<T, 1>(p, lie, s, blocks, st)
+        : s.c == 2 ? launch_norm_bwd_c<T, 2>(p, lie, s, blocks, st)
+                   : launch_norm_bwd_c<T, 4>(p, lie, s, blocks, st);
     if (e != cudaSuccess) return e;
   } else {
     // dw first: dx may overwrite dy or h
