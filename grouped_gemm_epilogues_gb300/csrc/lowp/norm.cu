@@ -449,11 +449,18 @@ RowShape many_threads(int64_t chunks, bool few) {
   return s;
 }
 
-// ... with up to 128: one block.  Rows of more than `two` chunks have four a thread.
-RowShape many_registers(int64_t chunks, int64_t two) {
-  RowShape s{chunks > two ? 4 : (chunks > 32 ? 2 : 1), 0, 0, 1};
+// ... with up to 128: one block.  Rows of more than `two` chunks have four a thread.  Few
+// rows are spread over `spread` SMs, and with one a block, a row has as many threads as it
+// can use.  The forward takes every SM (8 x 1999 4.3 to 2.3 us against blocks filled first);
+// the backward 64, as each block leaves a row of dw's sums (152 x 1536 5.2 us, 6.1 with all
+// 152; 8 x 1536 4.9 to 4.4).
+RowShape many_registers(int64_t chunks, int64_t two, int64_t rows, int spread) {
+  const bool few = rows <= spread;
+  RowShape s{chunks > (few ? 2 * kRowThreads : two) ? 4 : (chunks > (few ? kRowThreads : 32) ? 2 : 1), 0, 0, 1};
   s.tpr = whole_warps(chunks, s.c);
   s.per = kRowThreads / s.tpr;
+  const int64_t each = (rows + spread - 1) / spread;
+  if (each < s.per) s.per = static_cast<int>(each);
   return s;
 }
 
@@ -485,7 +492,7 @@ cudaError_t launch_norm_t(const NormParams& p, int sms, cudaStream_t st) {
       if (p.rows_lie == ROWS_ALIKE && chunks * 8 <= kMaxCols && sms >= 8) {
         // (16 bits, 24000 x 1999, two and four: 49 and 35 us, with residual 69 and 66; 48000 x
         // 1003 49 and 36; fp32 12000 x 1999 38 and 38, with residual 66 and 71)
-        const RowShape s = many_registers(chunks, sizeof(T) == 2 ? 64 : 2 * kRowThreads);
+        const RowShape s = many_registers(chunks, sizeof(T) == 2 ? 64 : 2 * kRowThreads, p.rows, sms);
         return s.c == 1   ? launch_norm_c<T, 1, FMT, ROWS_ALIKE>(p, s, sms, st)
                : s.c == 2 ? launch_norm_c<T, 2, FMT, ROWS_ALIKE>(p, s, sms, st)
                           : launch_norm_c<T, 4, FMT, ROWS_ALIKE>(p, s, sms, st);
@@ -767,7 +774,7 @@ cudaError_t launch_norm_bwd_t(const NormBwdParams& p, int sms, cudaStream_t st) 
     // bits that is better for three (8000 x 5120 65 to 62 us, 8192 columns 49 to 54), and in
     // ALIKE, where a row's ends take longer (12000 x 4097 108 to 79 us; 1999 columns 70 to 73).
     const bool four = sizeof(T) == 2 && (lie == ROWS_ALIKE || whole_warps(chunks, 4) * 3 <= kRowThreads);
-    const RowShape s = many_registers(chunks, four ? kRowThreads : 2 * kRowThreads);
+    const RowShape s = many_registers(chunks, four ? kRowThreads : 2 * kRowThreads, p.rows, sms < 64 ? sms : 64);
     const int64_t want = (p.rows + s.per - 1) / s.per;
     if (want < blocks) blocks = static_cast<int>(want);
     if (lie == ROWS_ALIKE) blocks = alike_blocks(p.rows, s.per, blocks);
