@@ -40,6 +40,13 @@ __host__ __device__ __forceinline__ int64_t scale_word(int64_t row, int64_t kg, 
   return ((row >> 7) * kgroups + kg) * 512 + (row & 31) * 16 + ((row >> 5) & 3) * 4;
 }
 
+// Columns up to the end of a row's last scale word (its blocks past the row are padding;
+// a row of up to 2^31 columns has up to 2^25 words, so the product takes 64 bits).
+template <int FMT>
+__host__ __device__ __forceinline__ int64_t scale_span(int64_t kgroups) {
+  return kgroups * Fmt<FMT>::kGroup;
+}
+
 // ------------------------------------------------------------------ scales
 
 // Biased exponent of a power-of-two scale from a block's largest |x| (as bits).

@@ -359,7 +359,7 @@ __global__ void norm_long_kernel(const __grid_constant__ NormParams p) {
     const int64_t row = row0 + sub;
     const bool live = row < p.rows;
     float ss = 0.f;
-    auto value = [&](int32_t col, bool write) {
+    auto value = [&](int64_t col, bool write) {
       float a = to_float<T>(x[row * p.ldx + col]);
       if (res != nullptr) {
         const T h = from_float<T>(a + to_float<T>(res[row * p.ldr + col]));
@@ -380,8 +380,9 @@ __global__ void norm_long_kernel(const __grid_constant__ NormParams p) {
     const float inv = __frsqrt_rn(ss / static_cast<float>(cols) + p.eps);
     if (live && t == 0 && p.inv != nullptr) p.inv[row] = inv;
     // columns up to the end of the last scale word (whole warps take part)
-    const int32_t end = FMT == FMT_NONE ? cols : static_cast<int32_t>(p.q.kgroups) * 128;
-    for (int32_t col = t; col - lane < end; col += tpr) {
+    int64_t end = cols;
+    if constexpr (FMT != FMT_NONE) end = scale_span<FMT>(p.q.kgroups);
+    for (int64_t col = t; col - lane < end; col += tpr) {
       float a = 0.f;
       if (live && col < cols) {
         a = (value(col, true) * inv) * load_any(p.weight, col, p.w_dtype);
@@ -395,7 +396,7 @@ __global__ void norm_long_kernel(const __grid_constant__ NormParams p) {
         float factor;
         uint32_t s = block_scale<FMT>(amax, tscale, factor);
         const float unit = scale_value<FMT>(s);
-        const int32_t block = col / Fmt<FMT>::kBlock;
+        const int64_t block = col / Fmt<FMT>::kBlock;
         const float c = a * factor;
         float back;
         if constexpr (FMT == FMT_MXFP8) {
@@ -484,8 +485,8 @@ cudaError_t launch_norm_c(const NormParams& p, const RowShape& s, int sms, cudaS
 
 template <typename T, int FMT>
 cudaError_t launch_norm_t(const NormParams& p, int sms, cudaStream_t st) {
-  const int64_t group = FMT == FMT_NONE ? 8 : Fmt<FMT == FMT_NONE ? 0 : FMT>::kGroup;
-  const int64_t span = (p.cols + group - 1) / group * group;
+  int64_t span = (static_cast<int64_t>(p.cols) + 7) / 8 * 8;
+  if constexpr (FMT != FMT_NONE) span = scale_span<FMT>(p.q.kgroups);
   if (span <= kMaxCols) {
     if constexpr (FMT == FMT_NONE) {
       const int64_t chunks = alike_chunks(p.cols, sizeof(T));

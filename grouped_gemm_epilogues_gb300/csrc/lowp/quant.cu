@@ -322,7 +322,7 @@ __global__ void __launch_bounds__(256, 4) quantize_cols_kernel(const __grid_cons
 
 template <typename T, int FMT, bool AL>
 cudaError_t launch_quantize_t(const QuantParams& p, cudaStream_t st) {
-  const int64_t span = p.q.kgroups * Fmt<FMT>::kGroup;
+  const int64_t span = scale_span<FMT>(p.q.kgroups);
   if (p.stride_col == 1 || p.cols == 1) {
     const RowTiles tiles = row_tiles(span, AL);
     return launch_pdl(quantize_rows_kernel<T, FMT, AL>, row_grid(tiles, p.rows, p.batch), dim3(256), 0, st,

@@ -79,3 +79,32 @@ def test_product(tile_n):
     gge.gge_gemm_mx(qt, qb, D=d2, PostAct=p2, C=c[-TAIL:].clone(), beta=0.5, act="silu", config=cfg)
     _same(d[-TAIL:], d2)
     _same(p[-TAIL:], p2)
+
+
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp8"])
+def test_norm_of_one_row_past_2_30_columns(fmt):
+    """nvfp4 has a scale word every 64 columns: twice as many a row as the other formats.  The
+    codes, scales and values are what gge_mx_quantize makes of the same fp32 y."""
+    cols = 2 ** 30 + 1077
+    g = torch.Generator(device=DEV).manual_seed(8)
+    x = torch.empty(1, cols, device=DEV).normal_(generator=g)
+    w = _rand(1, cols, 9)[0]
+    t = torch.tensor([2.0 ** -9], device=DEV) if fmt == "nvfp4" else None
+    y, inv = torch.full_like(x, 9.0), torch.zeros(1, device=DEV)
+    values = torch.full((1, cols), 9.0, dtype=torch.bfloat16, device=DEV)
+    q, q2 = (gge.mx_empty(1, cols, fmt, device=DEV, tensor_scale=t) for _ in range(2))
+    for z in (q, q2):
+        z.codes.fill_(0xA5)
+        z.scales.fill_(0xA5)
+    gge.gge_rmsnorm(x, w, Y=y, Q=q, values=values, inv_rms=inv, eps=1e-5)
+    for at in (0, cols // 2, cols - 4096):
+        # two products in fp32, as the kernel takes them
+        _same(y[:, at:at + 4096], x[:, at:at + 4096] * inv * w[at:at + 4096].float())
+    # (a thread adds up 2^20 squares one after the other: 2^-4 at most, about 2^-14 in fact)
+    assert abs(float(inv) - float(x.double().square().mean() + 1e-5) ** -0.5) < 2.0 ** -4
+    del x, w
+    values2 = torch.empty_like(values)
+    gge.gge_mx_quantize(y, q2, values=values2)
+    _same(q.codes, q2.codes)
+    _same(q.scales.view(-1, 32, 16)[:, 0, :4], q2.scales.view(-1, 32, 16)[:, 0, :4])
+    _same(values, values2)
