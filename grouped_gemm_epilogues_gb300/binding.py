@@ -625,20 +625,6 @@ def gge_mx_dequantize(Q, Y):
         raise GgeError(code, "gge_mx_dequantize")
 
 
-_workspace_bytes = {}   # per device: gge_workspace_size, gge_workspace_size_rmsnorm_bwd(0), and a column
-
-
-def _need(device):
-    n = _workspace_bytes.get(device.index)
-    if n is None:
-        lib = load()
-        with torch.cuda.device(device):
-            fixed = lib.gge_workspace_size_rmsnorm_bwd(0)
-            n = (lib.gge_workspace_size(None, 0), fixed, lib.gge_workspace_size_rmsnorm_bwd(1) - fixed)
-        _workspace_bytes[device.index] = n
-    return n
-
-
 def gge_gemm_mx(A, B, D=None, C=None, PostAct=None, act="none", alpha=1.0, beta=1.0,
                 alpha_dev=None, beta_dev=None, config=None, workspace=None):
     """D = alpha * A @ B^T + beta * C and / or PostAct = act(same) of MxTensors A (M, K) and
@@ -678,14 +664,10 @@ def gge_rmsnorm(X, weight, Y=None, residual=None, residual_out=None, Q=None, val
 
 def gge_rmsnorm_bwd(dY, H, weight, inv_rms, dX, dW=None, dH=None, workspace=None):
     """Backward of gge_rmsnorm: dX (the gradient of X and of the residual) from dY, the saved H
-    (residual_out, or X) and inv_rms; dW (fp32, optional); dH the gradient reaching H directly."""
-    if dW is None:
-        ws = None
-    else:
-        dev = dY.device
-        _, fixed, a_col = _need(dev)
-        need = fixed + a_col * dY.shape[-1]
-        ws = _shared(dev, need) if workspace is None else _ws(dev, need, workspace)
+    (residual_out, or X) and inv_rms; dW (fp32, optional); dH the gradient reaching H directly.
+    dW's partial sums take gge_workspace_size_rmsnorm_bwd(cols) bytes: memory of the call's own
+    from torch's allocator on the current stream, or the caller's ``workspace``."""
+    ws = None if workspace is None else _ws(dY.device, 0, workspace)
     code = (_marshal or _load_marshal()).rmsnorm_bwd(dY, H, weight, inv_rms, dX, dW, dH, ws)
     if code:
         raise GgeError(code, "gge_rmsnorm_bwd")

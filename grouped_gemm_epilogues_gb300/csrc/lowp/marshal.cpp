@@ -325,13 +325,21 @@ PyObject* rmsnorm_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
   g.reserved = 0;
   g.inv_rms = static_cast<const float*>(inv);
   g.dweight = static_cast<float*>(dw);
+  // the partial sums' memory: the caller's, or this call's own.  That is handed back at the
+  // end, for the stream's later kernels, and inside a capture belongs to the graph
   void* wp = nullptr;
   size_t wn = 0;
+  at::Tensor own;
   if (a[7] != Py_None) {
     const at::Tensor* ws = tensor(a[7], "workspace", dev);
     if (ws == nullptr) return nullptr;
     wp = ws->data_ptr();
     wn = static_cast<size_t>(ws->numel());
+  } else if (dw != nullptr) {
+    wn = gge_workspace_size_rmsnorm_bwd(g.dy.cols);
+    own = at::empty({static_cast<int64_t>(wn)},
+                    at::TensorOptions().dtype(at::kByte).device(at::kCUDA, static_cast<c10::DeviceIndex>(dev)));
+    wp = own.data_ptr();
   }
   gge_stream_t st = stream(dev);
   GGE_CALL(gge_rmsnorm_bwd(&g, wp, wn, st));

@@ -4,7 +4,7 @@ run on the CPU."""
 import os
 import subprocess
 
-import pytest
+import torch
 
 from grouped_gemm_epilogues_gb300 import build
 
@@ -45,3 +45,36 @@ def test_scale_span_in_64_bits_and_by_the_format_s_group(tmp_path):
     assert len(rows) == 8
     for kg, mxfp8, mxfp4, nvfp4 in rows:
         assert (mxfp8, mxfp4, nvfp4) == (128 * kg, 128 * kg, 64 * kg)
+
+
+class _Marshal:
+    """Stands in for the compiled module: keeps each call's arguments, reports success."""
+
+    def __init__(self):
+        self.calls = []
+
+    def __getattr__(self, name):
+        def call(*args):
+            self.calls.append((name, args))
+            return 0
+        return call
+
+
+def test_backward_norm_does_not_keep_its_partial_sums_in_the_shared_workspace(monkeypatch):
+    """They grow with the width: a captured graph would go on writing to a workspace that a
+    wider call has replaced.  The compiled module takes a buffer of the call's own."""
+    from grouped_gemm_epilogues_gb300 import binding as b
+
+    def refuse(*args):
+        raise AssertionError("shared workspace")
+
+    fake = _Marshal()
+    monkeypatch.setattr(b, "_marshal", fake)
+    monkeypatch.setattr(b, "_shared_workspace", refuse)
+    monkeypatch.setattr(b, "load", refuse)
+    x, v, row = torch.zeros(4, 8), torch.zeros(8), torch.zeros(4)
+    b.gge_rmsnorm_bwd(x, x, v, row, x, dW=v)
+    b.gge_rmsnorm_bwd(x, x, v, row, x)
+    own = torch.zeros(1 << 20, dtype=torch.uint8)
+    b.gge_rmsnorm_bwd(x, x, v, row, x, dW=v, workspace=own)
+    assert [args[7] for _, args in fake.calls] == [None, None, own]

@@ -302,3 +302,49 @@ def test_backward_many_rows(rows, cols, dtype, offsets):
     steps = (rows + 151) // 152 + 152 + 32
     tol = (steps * 2.0 ** -24 + 2.0 ** -22) * np.abs(a * b * i).sum(0) + formats.quantum(rdw, formats.F32)
     assert (np.abs(dec(dw) - rdw) <= tol).all()
+
+
+@pytest.mark.parametrize("cols", [1000, 1003])
+def test_captured_backward_then_a_wider_call(cols):
+    """A graph's dW has to stay right, and other tensors untouched, after a wider call and new
+    allocations between the capture and the replay."""
+    dy, h = (_rand(300, cols, torch.bfloat16, s) for s in (61, 62))
+    w = _rand(1, cols, torch.bfloat16, 63)[0]
+    inv = torch.rsqrt(h.float().square().mean(1) + EPS)
+    dx, dw = torch.empty_like(dy), torch.empty(cols, device=DEV)
+    gge.gge_rmsnorm_bwd(dy, h, w, inv, dx, dW=dw)
+    want_dx, want_dw = dx.clone(), dw.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        gge.gge_rmsnorm_bwd(dy, h, w, inv, dx, dW=dw)
+    wide = [_rand(300, 12000, torch.bfloat16, s) for s in (64, 65)]
+    wdx, wdw = torch.empty_like(wide[0]), torch.empty(12000, device=DEV)
+    winv = torch.rsqrt(wide[1].float().square().mean(1) + EPS)
+    gge.gge_rmsnorm_bwd(wide[0], wide[1], _rand(1, 12000, torch.bfloat16, 66)[0], winv, wdx, dW=wdw)
+    others = [torch.full((n,), 7.0, device=DEV) for n in (1 << 18, 1 << 20, 1 << 22) for _ in range(8)]
+    dx.fill_(9.0)
+    dw.fill_(9.0)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(dx, want_dx) and torch.equal(dw, want_dw)
+    assert all((t == 7.0).all() for t in others)
+
+
+def test_backward_on_two_streams_at_once():
+    """Calls without a workspace of the caller's do not share their partial sums."""
+    cases = []
+    for i, cols in enumerate((1536, 2000)):
+        dy, h = (_rand(4000, cols, torch.bfloat16, 71 + 2 * i + j) for j in (0, 1))
+        w, inv = _rand(1, cols, torch.bfloat16, 75 + i)[0], torch.rsqrt(h.float().square().mean(1) + EPS)
+        want = torch.empty(cols, device=DEV)
+        gge.gge_rmsnorm_bwd(dy, h, w, inv, torch.empty_like(dy), dW=want)
+        cases.append((torch.cuda.Stream(), (dy, h, w, inv, torch.empty_like(dy)), want,
+                      [torch.empty_like(want) for _ in range(10)]))
+    torch.cuda.synchronize()
+    for n in range(10):
+        for stream, args, _, dws in cases:
+            with torch.cuda.stream(stream):
+                gge.gge_rmsnorm_bwd(*args, dW=dws[n])
+    torch.cuda.synchronize()
+    for _, _, want, dws in cases:
+        assert all(torch.equal(want, d) for d in dws)
