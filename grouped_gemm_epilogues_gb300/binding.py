@@ -201,23 +201,38 @@ def view(t: torch.Tensor, kind: str) -> GgeTensor:
                      sr, sc, sb)
 
 
-_workspaces = {}
+_workspaces = {}   # per device index
+_replaced = {}     # ... and those it had before, which captured graphs may still use
+_workspace_lock = threading.Lock()
+
+
+def _zeroed(dev, nbytes):
+    """Zeroed device memory.  Inside a capture torch's allocator would give the graph's, and
+    the zeroing would be left to the replays: there it is made beside the capture, at once."""
+    if torch.cuda.is_current_stream_capturing():
+        return _load_marshal().zeroed(nbytes, dev.index)
+    return torch.zeros(nbytes, dtype=torch.uint8, device=dev)
 
 
 def workspace(device=None, nbytes: int = 256) -> torch.Tensor:
-    """The per-device workspace (zeroed when made), at least ``nbytes`` long.
-    Growing it keeps the status words (the first 256 bytes) of the old one."""
+    """The per-device workspace (zeroed when made), at least ``nbytes`` long.  Where a
+    longer one replaces it, it stays allocated, for the graphs captured with it
+    (gge_read_device_status reads both); each is twice as long as the last, so those kept
+    take no more than the one in use."""
     dev = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
     if dev.index is None:
         dev = torch.device("cuda", torch.cuda.current_device())
     ws = _workspaces.get(dev.index)
-    if ws is None or ws.numel() < nbytes:
-        new = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=dev)
-        if ws is not None:
-            new[:256].copy_(ws[:256])
-        ws = new
-        _workspaces[dev.index] = ws
-    return ws
+    if ws is not None and ws.numel() >= nbytes:
+        return ws
+    with _workspace_lock:
+        ws = _workspaces.get(dev.index)
+        if ws is None or ws.numel() < nbytes:
+            new = _zeroed(dev, max(nbytes, 256, 2 * ws.numel() if ws is not None else 0))
+            if ws is not None:
+                _replaced.setdefault(dev.index, []).append(ws)
+            _workspaces[dev.index] = ws = new
+        return ws
 
 
 def new_workspace(device=None, nbytes: int = 32 << 20) -> torch.Tensor:
@@ -419,11 +434,19 @@ def gge_read_static_scratch_status(device=None):
 
 def gge_read_device_status(device=None, workspace=None):
     """Synchronise the current stream and return (status_name, where, tile) recorded in
-    the shared per-device workspace (or in ``workspace``, a caller's); clears it."""
+    the shared per-device workspace or one that it replaced (or in ``workspace``, a
+    caller's); clears it."""
     lib = load()
-    ws = workspace if workspace is not None else _shared_workspace(device)
+    if workspace is not None:
+        places = [workspace]
+    else:
+        shared = _shared_workspace(device)
+        places = [shared] + next((old for i, old in _replaced.items() if _workspaces[i] is shared), [])
     detail = (c_i32 * 2)()
-    code = lib.gge_read_device_status(ctypes.c_void_p(ws.data_ptr()), _stream(ws), detail)
+    for ws in places:
+        code = lib.gge_read_device_status(ctypes.c_void_p(ws.data_ptr()), _stream(ws), detail)
+        if code != 0:
+            break
     return STATUS.get(code, str(code)), detail[0], detail[1]
 
 

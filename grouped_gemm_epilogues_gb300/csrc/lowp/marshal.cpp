@@ -7,6 +7,9 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <ATen/ATen.h>
+#include <c10/cuda/CUDAException.h>
+#include <c10/cuda/CUDAGraphsC10Utils.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 
 #include "../../../include/gge.h"
@@ -346,6 +349,29 @@ PyObject* rmsnorm_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+// zeroed(bytes, device) -> uint8 tensor that is zeroed when this returns and never given
+// back, also while a stream is captured (the calls are no part of the capture).
+PyObject* zeroed(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (!count(n, 2)) return nullptr;
+  const int64_t bytes = PyLong_AsLongLong(a[0]), dev = PyLong_AsLongLong(a[1]);
+  if (PyErr_Occurred()) return nullptr;
+  const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(dev));
+  const c10::cuda::CUDAStreamCaptureModeGuard relaxed(cudaStreamCaptureModeRelaxed);
+  void* p = nullptr;
+  C10_CUDA_CHECK(cudaMalloc(&p, static_cast<size_t>(bytes)));
+  cudaStream_t st = nullptr;
+  C10_CUDA_CHECK(cudaStreamCreateWithFlags(&st, cudaStreamNonBlocking));
+  const cudaError_t set = cudaMemsetAsync(p, 0, static_cast<size_t>(bytes), st);
+  const cudaError_t done = cudaStreamSynchronize(st);
+  C10_CUDA_CHECK(cudaStreamDestroy(st));
+  C10_CUDA_CHECK(set);
+  C10_CUDA_CHECK(done);
+  return THPVariable_Wrap(at::from_blob(
+      p, {bytes}, at::TensorOptions().dtype(at::kByte).device(at::kCUDA, static_cast<c10::DeviceIndex>(dev))));
+  END_HANDLE_TH_ERRORS
+}
+
 template <PyObject* (*F)(PyObject*, PyObject* const*, Py_ssize_t)>
 PyMethodDef method(const char* name) {
   return PyMethodDef{name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(F)), METH_FASTCALL, nullptr};
@@ -354,6 +380,7 @@ PyMethodDef method(const char* name) {
 PyMethodDef kMethods[] = {method<mx_alloc>("mx_alloc"), method<mx_wrap>("mx_wrap"), method<quantize>("quantize"),
                           method<dequantize>("dequantize"), method<gemm_mx>("gemm_mx"),
                           method<rmsnorm>("rmsnorm"), method<rmsnorm_bwd>("rmsnorm_bwd"),
+                          method<zeroed>("zeroed"),
                           {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "gge_marshal", nullptr, -1, kMethods,

@@ -54,3 +54,41 @@ def test_first_call_inside_graph_capture(tmp_path, cta_group):
     got = torch.load(out_path)
     w = wl.small("gemm_act_4096_bf16_gelu", 300, 520, 200, 2)
     _check_plain(w, wl.make(w), got)
+
+
+EAGER_BETWEEN = r"""
+import sys, torch
+sys.path.insert(0, sys.argv[1])
+from grouped_gemm_epilogues_gb300 import binding as b
+dev = torch.device("cuda", 0)
+g = torch.Generator(device=dev).manual_seed(1)
+m, n, k = 4096, 4096, 4096       # (its last wave is split: tickets and partial sums in the workspace)
+A, B = (torch.randn(r, k, generator=g, device=dev).bfloat16() for r in (m, n))
+junk = [torch.full((1 << 22,), 0x01010101, dtype=torch.int32, device=dev) for _ in range(4)]
+del junk                          # what a workspace that nobody zeroes may start with
+D = [torch.empty(m, n, dtype=torch.bfloat16, device=dev) for _ in range(3)]
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    b.gge_gemm(A, B, D[0])
+small = b.workspace(dev)
+assert not small.any(), "the workspace is zeroed when the capture is over"
+b.gge_gemm(A, B, D[1])            # on the same workspace, before the first replay
+wide = b.workspace(dev, 2 * small.numel())
+b.gge_gemm(A, B, D[2])
+graph.replay()
+graph.replay()
+torch.cuda.synchronize()
+assert b.gge_read_device_status(dev)[0] == "GGE_OK"
+assert b.workspace(dev) is wide and any(t is small for t in b._replaced[0])
+assert torch.equal(D[0], D[1]) and torch.equal(D[0], D[2])
+want = A.float() @ B.float().t()
+assert float((D[0].float() - want).norm() / want.norm()) < 2.0 ** -7
+"""
+
+
+def test_workspace_first_made_inside_a_capture():
+    """Made beside the capture and zeroed at once, so that calls before the first replay can
+    use it; the graph keeps its own when a longer one replaces it."""
+    r = subprocess.run([sys.executable, "-c", EAGER_BETWEEN, ROOT], capture_output=True, text=True, timeout=600)
+    assert r.returncode == 0, r.stdout[-2000:] + r.stderr[-4000:]
