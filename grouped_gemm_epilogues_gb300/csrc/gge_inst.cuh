@@ -1,36 +1,16 @@
 // Shared body of the per-instantiation translation units.
 #pragma once
 
-#include <atomic>
-
 #include "gge_kernel.cuh"
 #include "gge_launch.h"
 
 namespace gge {
 
-template <int BN, bool GATHER, int CG, bool TR = false>
-cudaError_t set_smem_limit(size_t smem) {
-  auto kern = gemm_kernel<BN, GATHER, CG, TR>;
-  // the dynamic shared-memory limit is a per-device function attribute
-  static std::atomic<size_t> smem_set[64];
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= 64 || smem_set[dev].load() < smem) {
-    RelaxedCaptureMode relaxed;
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(smem));
-    if (e != cudaSuccess) return e;
-    if (dev >= 0 && dev < 64) smem_set[dev].store(smem);
-  }
-  return cudaSuccess;
-}
-
 template <int BN, bool GATHER, int CG, bool TR>
 cudaError_t launch_gemm(const CUtensorMap& tmA, const CUtensorMap& tmB, const Params& p,
                         const LaunchShape& shape, cudaStream_t stream) {
   auto kern = gemm_kernel<BN, GATHER, CG, TR>;
-  cudaError_t e = set_smem_limit<BN, GATHER, CG, TR>(shape.smem);
+  cudaError_t e = allow_smem<gemm_kernel<BN, GATHER, CG, TR>>();
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[2];
   cudaLaunchConfig_t cfg = {};
@@ -62,7 +42,7 @@ int kernel_threads() {
 template <int BN, bool GATHER, int CG>
 int max_active_units(size_t smem, int cluster) {
   auto kern = gemm_kernel<BN, GATHER, CG>;
-  if (set_smem_limit<BN, GATHER, CG>(smem) != cudaSuccess) return -1;
+  if (allow_smem<gemm_kernel<BN, GATHER, CG, false>>() != cudaSuccess) return -1;
   if (cluster <= 1) {
     int per_sm = 0, dev = 0, sms = 0;
     if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, KernelCfg<BN, GATHER, CG>::kThreads,

@@ -4,6 +4,9 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
+#include <cstdint>
+
 #include "../../include/gge.h"
 #include "gge_params.h"
 
@@ -21,6 +24,35 @@ struct RelaxedCaptureMode {
   RelaxedCaptureMode(const RelaxedCaptureMode&) = delete;
   RelaxedCaptureMode& operator=(const RelaxedCaptureMode&) = delete;
 };
+
+// Let blocks of a kernel have all the shared memory that a block on the current device
+// can (a per-device attribute of the kernel).  Always the same number: launches that set
+// it to what they need themselves could lower it under another thread's.  `done`: a bit
+// for each device.
+inline cudaError_t allow_most_smem(const void* kern, std::atomic<uint64_t>* done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev >= 0 && dev < 64 ? uint64_t(1) << dev : 0;
+  if ((done->load() & bit) != 0) return cudaSuccess;
+  RelaxedCaptureMode relaxed;
+  int most = 0;
+  cudaFuncAttributes fa = {};
+  e = cudaDeviceGetAttribute(&most, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
+  if (e == cudaSuccess) e = cudaFuncGetAttributes(&fa, kern);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             most - static_cast<int>(fa.sharedSizeBytes));
+  if (e == cudaSuccess) done->fetch_or(bit);
+  return e;
+}
+
+// ... once for each kernel, whatever the launch.
+template <auto Kern>
+cudaError_t allow_smem() {
+  static std::atomic<uint64_t> done{0};
+  return allow_most_smem(reinterpret_cast<const void*>(Kern), &done);
+}
 
 struct LaunchShape {
   int grid;

@@ -4,7 +4,6 @@
 
 #include <cuda_runtime.h>
 
-#include <atomic>
 #include <cstdint>
 
 #include "../gge_launch.h"
@@ -96,21 +95,6 @@ int norm_bwd_blocks(int64_t rows, int sms);
 cudaError_t launch_norm_bwd(const NormBwdParams& p, int sms, cudaStream_t st);
 cudaError_t launch_quantize(const QuantParams& p, cudaStream_t st);
 cudaError_t launch_dequantize(const DequantParams& p, cudaStream_t st);
-
-// Opt in to `smem` bytes of shared memory (a per-device attribute of the kernel).
-template <typename... A>
-cudaError_t allow_smem(void (*kern)(A...), std::atomic<size_t>* set, size_t smem) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= 64 || set[dev].load() < smem) {
-    RelaxedCaptureMode relaxed;
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-    if (e != cudaSuccess) return e;
-    if (dev >= 0 && dev < 64) set[dev].store(smem);
-  }
-  return cudaSuccess;
-}
 
 // Launch with programmatic stream serialisation: the kernel sets up, then waits
 // (griddepcontrol.wait) for the stream's previous kernel before it touches

@@ -1,29 +1,10 @@
 // Shared body of the block-scaled product's translation units.
 #pragma once
 
-#include <atomic>
-
 #include "mx_gemm.cuh"
 
 namespace gge {
 namespace mx {
-
-template <int BN, int CG, int FMT, bool TR>
-cudaError_t mx_smem_limit(size_t smem) {
-  // the dynamic shared-memory limit is a per-device function attribute
-  static std::atomic<size_t> smem_set[64];
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= 64 || smem_set[dev].load() < smem) {
-    RelaxedCaptureMode relaxed;
-    e = cudaFuncSetAttribute(mx_gemm_kernel<BN, CG, FMT, TR>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-    if (e != cudaSuccess) return e;
-    if (dev >= 0 && dev < 64) smem_set[dev].store(smem);
-  }
-  return cudaSuccess;
-}
 
 template <int BN, int CG, int FMT, bool TR>
 cudaLaunchConfig_t mx_config(int grid, size_t smem, int cluster, cudaStream_t stream,
@@ -50,7 +31,7 @@ cudaLaunchConfig_t mx_config(int grid, size_t smem, int cluster, cudaStream_t st
 template <int BN, int CG, int FMT, bool TR>
 cudaError_t mx_launch_one(const MxMaps& m, const MxParams& mp, const LaunchShape& shape,
                           cudaStream_t stream) {
-  const cudaError_t e = mx_smem_limit<BN, CG, FMT, TR>(shape.smem);
+  const cudaError_t e = allow_smem<mx_gemm_kernel<BN, CG, FMT, TR>>();
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[2];
   const cudaLaunchConfig_t cfg = mx_config<BN, CG, FMT, TR>(shape.grid, shape.smem, shape.cluster, stream, attr);
@@ -59,7 +40,7 @@ cudaError_t mx_launch_one(const MxMaps& m, const MxParams& mp, const LaunchShape
 
 template <int BN, int CG, int FMT, bool TR>
 int mx_units_one(size_t smem, int cluster) {
-  if (mx_smem_limit<BN, CG, FMT, TR>(smem) != cudaSuccess) return -1;
+  if (allow_smem<mx_gemm_kernel<BN, CG, FMT, TR>>() != cudaSuccess) return -1;
   if (cluster == 1) {
     int per_sm = 0, dev = 0, sms = 0;
     if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, mx_gemm_kernel<BN, CG, FMT, TR>,

@@ -19,7 +19,6 @@
 // rate; the first version, without copies ahead and packed arithmetic, 273).  Rows that
 // start on any 2 bytes, fp16 16000 x 1999: 26 us alike (4.9 TB/s), 40 shifted.  Backward 16384
 // x 4096 with dh 85 us (6.3 TB/s, 94 %), bf16 24000 x 1999 70 us (5.5 TB/s).
-#include <atomic>
 #include <numeric>
 
 #include "lowp_launch.h"
@@ -470,10 +469,9 @@ int64_t alike_chunks(int64_t cols, int value_bytes) { return (cols + 16 / value_
 
 template <typename T, int C, int FMT, int R>
 cudaError_t launch_norm_c(const NormParams& p, const RowShape& s, int sms, cudaStream_t st) {
-  static std::atomic<size_t> set[64];
   const int block = s.per * s.tpr;
   const size_t smem = static_cast<size_t>(norm_depth<T, C, R>()) * (block / 32) * C * 2 * WarpRow<T>::kBytes;
-  const cudaError_t e = allow_smem(norm_kernel<T, C, FMT, R>, set, smem);
+  const cudaError_t e = allow_smem<norm_kernel<T, C, FMT, R>>();
   if (e != cudaSuccess) return e;
   // as many blocks as an SM holds, each with its share of the rows
   const int64_t resident = static_cast<int64_t>(sms) * s.blocks;
@@ -742,9 +740,8 @@ __global__ void __launch_bounds__(1024)
 
 template <typename T, int C, int R>
 cudaError_t launch_norm_bwd_r(const NormBwdParams& p, const RowShape& s, int blocks, cudaStream_t st) {
-  static std::atomic<size_t> set[64];
   constexpr size_t smem = static_cast<size_t>(bwd_depth<T, C, R>()) * (kRowThreads / 32) * C * 3 * WarpRow<T>::kBytes;
-  const cudaError_t e = allow_smem(norm_bwd_kernel<T, C, R>, set, smem);
+  const cudaError_t e = allow_smem<norm_bwd_kernel<T, C, R>>();
   if (e != cudaSuccess) return e;
   return launch_pdl(norm_bwd_kernel<T, C, R>, dim3(blocks), dim3(s.per * s.tpr), smem, st, p, s.tpr);
 }

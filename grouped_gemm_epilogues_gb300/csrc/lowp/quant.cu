@@ -7,8 +7,6 @@
 // are bound by memory.  Measured with the codes' values written too: 8192 x 8192 bf16
 // to nvfp4 54 us (5.7 TB/s, 85 % of a copy's rate; issue 83 % busy, two divisions a
 // block), transposed 59 us; 4096 x 32768 to mxfp8 transposed 128 us (5.3 TB/s, 79 %).
-#include <atomic>
-
 #include "lowp_launch.h"
 #include "rows.cuh"
 
@@ -331,10 +329,10 @@ cudaError_t launch_quantize_t(const QuantParams& p, cudaStream_t st) {
   constexpr int kRows = kTWords * (4 / sizeof(T));
   constexpr size_t smem = kTCols * kTPitch * 4 + kRows * (kTCols / Fmt<FMT>::kBlock) +
                           kRows * (kTCols * Fmt<FMT>::kBits / 8 + 16);
-  static std::atomic<size_t> set[2][64];
   const bool half = p.q.values != nullptr && p.q.v_dtype == 1;
   const auto kern = half ? quantize_cols_kernel<T, FMT, AL, __half> : quantize_cols_kernel<T, FMT, AL, __nv_bfloat16>;
-  const cudaError_t e = allow_smem(kern, set[half], smem);
+  const cudaError_t e = half ? allow_smem<quantize_cols_kernel<T, FMT, AL, __half>>()
+                             : allow_smem<quantize_cols_kernel<T, FMT, AL, __nv_bfloat16>>();
   if (e != cudaSuccess) return e;
   return launch_pdl(kern,
                     dim3(static_cast<unsigned>((span + kTCols - 1) / kTCols),

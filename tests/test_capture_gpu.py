@@ -92,3 +92,53 @@ def test_workspace_first_made_inside_a_capture():
     use it; the graph keeps its own when a longer one replaces it."""
     r = subprocess.run([sys.executable, "-c", EAGER_BETWEEN, ROOT], capture_output=True, text=True, timeout=600)
     assert r.returncode == 0, r.stdout[-2000:] + r.stderr[-4000:]
+
+
+THREADS = r"""
+import sys, threading, torch
+sys.path.insert(0, sys.argv[1])
+from grouped_gemm_epilogues_gb300 import binding as b
+dev = torch.device("cuda", 0)
+g = torch.Generator(device=dev).manual_seed(1)
+def draw(*shape):
+    return torch.randn(*shape, generator=g, device=dev).bfloat16()
+b.workspace(dev)
+norms = [(draw(500, c), draw(c)) for c in (64, 512, 2048, 4096, 8192, 16384, 1003, 7999)]
+wide = [draw(n, 1024) for n in (64, 128, 256, 512)]
+qs = [b.mx_empty(w.shape[0], 1024, "mxfp8", device=dev) for w in wide]
+torch.cuda.synchronize()
+go, errors, outs = threading.Barrier(12), [], {}
+def norm(i):
+    x, w = norms[i]
+    y = torch.empty_like(x)
+    go.wait()
+    b.gge_rmsnorm(x, w, Y=y)
+    outs[i] = y
+def product(i):
+    d = torch.empty(wide[i].shape[0], wide[i].shape[0], dtype=torch.bfloat16, device=dev)
+    go.wait()
+    b.gge_mx_quantize(wide[i], qs[i])
+    b.gge_gemm_mx(qs[i], qs[i], D=d, config=b.make_config(stages=2 + i))
+def run(f, i):
+    try:
+        with torch.cuda.stream(torch.cuda.Stream()):
+            f(i)
+            torch.cuda.current_stream().synchronize()
+    except Exception as e:
+        errors.append((f.__name__, i, repr(e)))
+threads = [threading.Thread(target=run, args=(f, i)) for f, n in ((norm, 8), (product, 4)) for i in range(n)]
+for t in threads: t.start()
+for t in threads: t.join()
+for i in range(8):          # and every shape still launches afterwards
+    y = torch.empty_like(norms[i][0])
+    b.gge_rmsnorm(*norms[i], Y=y)
+    if not torch.equal(y, outs[i]): errors.append(("again", i))
+torch.cuda.synchronize()
+assert not errors, errors
+assert b.gge_read_device_status(dev)[0] == "GGE_OK"
+"""
+
+
+def test_first_calls_in_several_threads():
+    r = subprocess.run([sys.executable, "-c", THREADS, ROOT], capture_output=True, text=True, timeout=600)
+    assert r.returncode == 0, r.stdout[-2000:] + r.stderr[-4000:]

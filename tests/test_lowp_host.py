@@ -78,3 +78,68 @@ def test_backward_norm_does_not_keep_its_partial_sums_in_the_shared_workspace(mo
     own = torch.zeros(1 << 20, dtype=torch.uint8)
     b.gge_rmsnorm_bwd(x, x, v, row, x, dW=v, workspace=own)
     assert [args[7] for _, args in fake.calls] == [None, None, own]
+
+
+LIMIT = r"""
+#include <chrono>
+#include <cstdio>
+#include <thread>
+#include "gge_launch.h"
+// a device whose blocks may have 232448 bytes, kernels with 256 and 1024 static ones, and
+// attribute calls that take their time
+static std::atomic<int> limit[3], sets;
+void kern(int) {}
+void other(int) {}
+static int which(const void* f) { return f == reinterpret_cast<const void*>(kern) ? 0 : 1; }
+static thread_local int device = 0;
+extern "C" {
+cudaError_t cudaGetDevice(int* d) { *d = device; return cudaSuccess; }
+cudaError_t cudaThreadExchangeStreamCaptureMode(cudaStreamCaptureMode*) { return cudaSuccess; }
+cudaError_t cudaDeviceGetAttribute(int* v, cudaDeviceAttr a, int) {
+  *v = a == cudaDevAttrMaxSharedMemoryPerBlockOptin ? 232448 : -1;
+  return cudaSuccess;
+}
+cudaError_t cudaFuncGetAttributes(cudaFuncAttributes* a, const void* f) {
+  a->sharedSizeBytes = which(f) == 0 ? 256 : 1024;
+  return cudaSuccess;
+}
+cudaError_t cudaFuncSetAttribute(const void* f, cudaFuncAttribute, int v) {
+  std::this_thread::sleep_for(std::chrono::milliseconds(20 + 30 * (sets++ % 3)));
+  limit[device == 0 ? which(f) : 2] = v;
+  std::this_thread::sleep_for(std::chrono::milliseconds(20));
+  return cudaSuccess;
+}
+}
+int main() {
+  std::atomic<int> short_of{0};
+  std::thread t[8];
+  for (int i = 0; i < 8; ++i)
+    t[i] = std::thread([i, &short_of] {
+      std::this_thread::sleep_for(std::chrono::milliseconds(7 * i));
+      for (int n = 0; n < 5; ++n) {
+        if (gge::allow_smem<kern>() != cudaSuccess || limit[0] != 232448 - 256) ++short_of;
+        if (gge::allow_smem<other>() != cudaSuccess || limit[1] != 232448 - 1024) ++short_of;
+      }
+    });
+  for (auto& x : t) x.join();
+  const int before = sets;
+  gge::allow_smem<kern>();
+  const int again = sets - before;
+  device = 1;
+  gge::allow_smem<kern>();
+  std::printf("%d %d %d\n", (int)short_of, again, (int)limit[2]);
+}
+"""
+
+
+def test_shared_memory_limit_of_first_calls_in_several_threads(tmp_path):
+    """Whatever the order of their calls, no thread finds a limit below the device's, and a
+    kernel's limit is set on each device."""
+    src, exe = tmp_path / "limit.cpp", tmp_path / "limit"
+    src.write_text(LIMIT)
+    cuda = os.path.join(os.path.dirname(os.path.dirname(build.nvcc())), "include")
+    r = subprocess.run(["g++", "-std=c++17", "-I", build.CSRC, "-I", cuda, str(src), "-o", str(exe), "-lpthread"],
+                       capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+    r = subprocess.run([str(exe)], capture_output=True, text=True, timeout=60)
+    assert r.stdout.split() == ["0", "0", str(232448 - 256)], r.stdout + r.stderr
