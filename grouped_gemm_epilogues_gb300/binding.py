@@ -170,12 +170,15 @@ def load(path: str = None, build_if_missing: bool = True) -> ctypes.CDLL:
 
 
 def _load_marshal():
-    """The compiled marshalling of the low-precision entry points (gge_marshal.so)."""
+    """The compiled marshalling of the low-precision entry points (gge_marshal)."""
     global _marshal
     load()
     with _lock:
         if _marshal is None:
-            spec = importlib.util.spec_from_file_location("gge_marshal", _build.MARSHAL)
+            path = _build.marshal_path()
+            if not os.path.exists(path):
+                _build.build()
+            spec = importlib.util.spec_from_file_location("gge_marshal", path)
             module = importlib.util.module_from_spec(spec)
             spec.loader.exec_module(module)
             _marshal = module
