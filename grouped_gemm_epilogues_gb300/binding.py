@@ -8,8 +8,11 @@ stream.  There is no fallback: if the library cannot be loaded, ``load()``
 raises.
 """
 
+import contextlib
 import ctypes
+import functools
 import importlib.util
+import inspect
 import os
 import threading
 
@@ -222,9 +225,7 @@ def workspace(device=None, nbytes: int = 256) -> torch.Tensor:
     longer one replaces it, it stays allocated, for the graphs captured with it
     (gge_read_device_status reads both); each is twice as long as the last, so those kept
     take no more than the one in use."""
-    dev = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
-    if dev.index is None:
-        dev = torch.device("cuda", torch.cuda.current_device())
+    dev = _cuda_device(device)
     ws = _workspaces.get(dev.index)
     if ws is not None and ws.numel() >= nbytes:
         return ws
@@ -317,8 +318,33 @@ def _check(code, where):
         raise GgeError(code, where)
 
 
+def _current(dev):
+    """The library plans and launches on the current device: makes ``dev`` that one (a host
+    tensor's makes no difference) for the length of a with statement."""
+    if dev.type != "cuda" or dev.index is None or torch.cuda.current_device() == dev.index:
+        return contextlib.nullcontext()
+    return torch.cuda.device(dev)
+
+
+def _on_device_of(name):
+    """Calls the function with the device of its argument ``name``, a tensor, current."""
+    def wrap(f):
+        at = list(inspect.signature(f).parameters).index(name)
+
+        @functools.wraps(f)
+        def call(*args, **kw):
+            dev = getattr(args[at] if len(args) > at else kw.get(name), "device", None)
+            if dev is None or dev.type != "cuda" or torch.cuda.current_device() == dev.index:
+                return f(*args, **kw)
+            with torch.cuda.device(dev):
+                return f(*args, **kw)
+        return call
+    return wrap
+
+
 # ------------------------------------------------------------- entry points
 
+@_on_device_of("A")
 def gge_gemm(A, B, D, C=None, alpha=1.0, beta=1.0, alpha_dev=None, beta_dev=None, config=None,
              workspace=None):
     """D = alpha * A @ B^T + beta * C.  A (L,M,K)/(M,K), B (L,N,K)/(N,K), D (L,M,N)/(M,N).
@@ -331,6 +357,7 @@ def gge_gemm(A, B, D, C=None, alpha=1.0, beta=1.0, alpha_dev=None, beta_dev=None
                         _stream(D)), "gge_gemm")
 
 
+@_on_device_of("A")
 def gge_gemm_act(A, B, PostAct, act, D=None, C=None, alpha=1.0, beta=1.0, alpha_dev=None,
                  beta_dev=None, config=None, workspace=None):
     """D (optional) and PostAct = act(alpha * A @ B^T + beta * C)."""
@@ -342,6 +369,7 @@ def gge_gemm_act(A, B, PostAct, act, D=None, C=None, alpha=1.0, beta=1.0, alpha_
                             _stream(PostAct)), "gge_gemm_act")
 
 
+@_on_device_of("A")
 def gge_gemm_dact(A, B, PreAct, D, act, PostAct=None, config=None, workspace=None):
     """Backward activation epilogue: D = act'(PreAct) * (A @ B^T), PostAct = act(PreAct)."""
     lib = load()
@@ -351,6 +379,7 @@ def gge_gemm_dact(A, B, PreAct, D, act, PostAct=None, config=None, workspace=Non
                              _stream(D)), "gge_gemm_dact")
 
 
+@_on_device_of("A")
 def gge_gemm_act_static_scratch(A, B, PostAct, act, D=None, C=None, alpha=1.0, beta=1.0,
                                 config=None):
     """gge_gemm_act for callers that cannot allocate: no workspace argument, the
@@ -362,6 +391,7 @@ def gge_gemm_act_static_scratch(A, B, PostAct, act, D=None, C=None, alpha=1.0, b
            "gge_gemm_act_static_scratch")
 
 
+@_on_device_of("A")
 def gge_gemm_varlen_m(A, B, cu_seqlens_m, D=None, PostAct=None, act="none", C=None, alpha=1.0,
                       beta=1.0, config=None, workspace=None):
     """Varlen-M grouped GEMM: A (total_M, K), B (G, N, K), cu_seqlens_m int32 (G+1,) on device."""
@@ -376,6 +406,7 @@ def gge_gemm_varlen_m(A, B, cu_seqlens_m, D=None, PostAct=None, act="none", C=No
            "gge_gemm_varlen_m")
 
 
+@_on_device_of("A")
 def gge_gemm_varlen_k(A, B, cu_seqlens_k, D=None, PostAct=None, act="none", C=None, alpha=1.0,
                       beta=1.0, config=None, workspace=None):
     """Varlen-K grouped GEMM: A (M, total_K), B (N, total_K), cu_seqlens_k int32 (G+1,) on
@@ -392,6 +423,7 @@ def gge_gemm_varlen_k(A, B, cu_seqlens_k, D=None, PostAct=None, act="none", C=No
            "gge_gemm_varlen_k")
 
 
+@_on_device_of("A_src")
 def gge_gemm_gather_k(A_src, B, a_idx, cu_seqlens_k, D=None, PostAct=None, act="none", C=None,
                       alpha=1.0, beta=1.0, config=None, workspace=None):
     """Gather-K: varlen-K GEMM whose A column k is A_src[:, a_idx[k]].  A_src (M, K_src)
@@ -409,6 +441,7 @@ def gge_gemm_gather_k(A_src, B, a_idx, cu_seqlens_k, D=None, PostAct=None, act="
            "gge_gemm_gather_k")
 
 
+@_on_device_of("A_src")
 def gge_gemm_gather_a(A_src, B, a_idx, cu_seqlens_m=None, D=None, PostAct=None, act="none",
                       C=None, alpha=1.0, beta=1.0, config=None, workspace=None):
     """Gather-A GEMM: effective A row r = A_src[a_idx[r]]; varlen-M when cu_seqlens_m is given."""
@@ -424,14 +457,20 @@ def gge_gemm_gather_a(A_src, B, a_idx, cu_seqlens_m=None, D=None, PostAct=None, 
            "gge_gemm_gather_a")
 
 
+def _cuda_device(device):
+    dev = torch.device("cuda" if device is None else device)
+    return dev if dev.index is not None else torch.device("cuda", torch.cuda.current_device())
+
+
 def gge_read_static_scratch_status(device=None):
     """Synchronise the current stream and return (status_name, where, tile) that
     gge_gemm_act_static_scratch calls recorded in the library's area; clears it."""
-    lib = load()
-    dev = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
-    detail = (c_i32 * 2)()
-    stream = ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream)
-    code = lib.gge_read_static_scratch_status(stream, detail)
+    dev = _cuda_device(device)
+    with _current(dev):
+        lib = load()
+        detail = (c_i32 * 2)()
+        stream = ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream)
+        code = lib.gge_read_static_scratch_status(stream, detail)
     return STATUS.get(code, str(code)), detail[0], detail[1]
 
 
@@ -439,23 +478,22 @@ def gge_read_device_status(device=None, workspace=None):
     """Synchronise the current stream and return (status_name, where, tile) recorded in
     the shared per-device workspace or one that it replaced (or in ``workspace``, a
     caller's); clears it."""
-    lib = load()
-    if workspace is not None:
-        places = [workspace]
-    else:
-        shared = _shared_workspace(device)
-        places = [shared] + next((old for i, old in _replaced.items() if _workspaces[i] is shared), [])
-    detail = (c_i32 * 2)()
-    for ws in places:
-        code = lib.gge_read_device_status(ctypes.c_void_p(ws.data_ptr()), _stream(ws), detail)
-        if code != 0:
-            break
+    dev = _cuda_device(device) if workspace is None else workspace.device
+    with _current(dev):
+        lib = load()
+        places = [workspace] if workspace is not None else [_shared_workspace(dev)] + _replaced.get(dev.index, [])
+        detail = (c_i32 * 2)()
+        for ws in places:
+            code = lib.gge_read_device_status(ctypes.c_void_p(ws.data_ptr()), _stream(ws), detail)
+            if code != 0:
+                break
     return STATUS.get(code, str(code)), detail[0], detail[1]
 
 
 FORM = {"default": 0, "gather_a": 1, "varlen_k": 2, "gather_k": 3}
 
 
+@_on_device_of("A")
 def gge_plan(A, B, C=None, D=None, PostAct=None, act="none", num_groups=0, gather=False,
              config=None, form=None):
     """The launch plan; form: 'default' (plain / varlen-M), 'gather_a' or 'varlen_k'."""
@@ -485,6 +523,7 @@ def _tune_args(op, A, B, C, D, PostAct, act, alpha, beta, config):
                      config=config)
 
 
+@_on_device_of("A")
 def gge_tune_candidates(op, A, B, C=None, D=None, PostAct=None, act="none", num_groups=0,
                         config=None):
     """The launch configurations gge_autotune would time for this problem (host only)."""
@@ -495,6 +534,7 @@ def gge_tune_candidates(op, A, B, C=None, D=None, PostAct=None, act="none", num_
     return [config_dict(out[i]) for i in range(min(n, 64))]
 
 
+@_on_device_of("A")
 def gge_autotune(op, A, B, idx=None, cu=None, C=None, D=None, PostAct=None, act="none",
                  alpha=1.0, beta=1.0, reps=10, config=None):
     """Time every candidate launch shape of `op` on the current stream and return
@@ -519,6 +559,7 @@ def gge_autotune(op, A, B, idx=None, cu=None, C=None, D=None, PostAct=None, act=
     return config_dict(best), ms.value
 
 
+@_on_device_of("A")
 def gge_tuned_config(op, A, B, C=None, D=None, PostAct=None, act="none", num_groups=0,
                      config=None):
     """The configuration gge_autotune stored for a problem of this key, or None."""

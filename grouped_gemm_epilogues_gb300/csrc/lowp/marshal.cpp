@@ -115,11 +115,15 @@ int device_of(PyObject* o, const char* kind) {
   return t == nullptr ? -1 : static_cast<int>(t->get_device());
 }
 
-#define GGE_CALL(expr)          \
-  gge_status code;              \
-  Py_BEGIN_ALLOW_THREADS;       \
-  code = (expr);                \
-  Py_END_ALLOW_THREADS;         \
+// Every call into the library goes through this one: with the tensors' device current (the
+// library plans and launches on that) and on its current stream, `st`; without the GIL.
+#define GGE_CALL(dev, expr)                                                              \
+  const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(dev));                  \
+  gge_stream_t st = stream(dev);                                                         \
+  gge_status code;                                                                       \
+  Py_BEGIN_ALLOW_THREADS;                                                                \
+  code = (expr);                                                                         \
+  Py_END_ALLOW_THREADS;                                                                  \
   return PyLong_FromLong(code)
 
 // mx_alloc(bytes, start, device, format, rows, cols, batch or 0, row bytes, scale bytes a batch,
@@ -204,8 +208,7 @@ PyObject* quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (dev < 0 || q == nullptr || view(a[0], "X", dev, false, &x) < 0) return nullptr;
   const int has = view(a[2], "values", dev, true, &v);
   if (has < 0) return nullptr;
-  gge_stream_t st = stream(dev);
-  GGE_CALL(gge_mx_quantize(&x, q, has ? &v : nullptr, st));
+  GGE_CALL(dev, gge_mx_quantize(&x, q, has ? &v : nullptr, st));
   END_HANDLE_TH_ERRORS
 }
 
@@ -217,8 +220,7 @@ PyObject* dequantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
   gge_tensor y;
   const gge_mx_tensor* q = mx(a[0], false);
   if (dev < 0 || q == nullptr || view(a[1], "Y", dev, false, &y) < 0) return nullptr;
-  gge_stream_t st = stream(dev);
-  GGE_CALL(gge_mx_dequantize(q, &y, st));
+  GGE_CALL(dev, gge_mx_dequantize(q, &y, st));
   END_HANDLE_TH_ERRORS
 }
 
@@ -261,9 +263,8 @@ PyObject* gemm_mx(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (ws == nullptr) return nullptr;
   void* wp = ws->data_ptr();
   const size_t wn = static_cast<size_t>(ws->numel());
-  gge_stream_t st = stream(dev);
   const bool dact = PyObject_IsTrue(a[13]) == 1;
-  GGE_CALL(dact ? gge_gemm_mx_dact(&g, wp, wn, st) : gge_gemm_mx(&g, wp, wn, st));
+  GGE_CALL(dev, dact ? gge_gemm_mx_dact(&g, wp, wn, st) : gge_gemm_mx(&g, wp, wn, st));
   END_HANDLE_TH_ERRORS
 }
 
@@ -299,8 +300,7 @@ PyObject* rmsnorm(PyObject*, PyObject* const* a, Py_ssize_t n) {
   g.weight = w;
   g.weight_dtype = wt;
   g.inv_rms = static_cast<float*>(inv);
-  gge_stream_t st = stream(dev);
-  GGE_CALL(gge_rmsnorm(&g, st));
+  GGE_CALL(dev, gge_rmsnorm(&g, st));
   END_HANDLE_TH_ERRORS
 }
 
@@ -339,13 +339,13 @@ PyObject* rmsnorm_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
     wp = ws->data_ptr();
     wn = static_cast<size_t>(ws->numel());
   } else if (dw != nullptr) {
+    const c10::cuda::CUDAGuard on(static_cast<c10::DeviceIndex>(dev));
     wn = gge_workspace_size_rmsnorm_bwd(g.dy.cols);
     own = at::empty({static_cast<int64_t>(wn)},
                     at::TensorOptions().dtype(at::kByte).device(at::kCUDA, static_cast<c10::DeviceIndex>(dev)));
     wp = own.data_ptr();
   }
-  gge_stream_t st = stream(dev);
-  GGE_CALL(gge_rmsnorm_bwd(&g, wp, wn, st));
+  GGE_CALL(dev, gge_rmsnorm_bwd(&g, wp, wn, st));
   END_HANDLE_TH_ERRORS
 }
 

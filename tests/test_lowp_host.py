@@ -2,11 +2,12 @@
 run on the CPU."""
 
 import os
+import re
 import subprocess
 
 import torch
 
-from grouped_gemm_epilogues_gb300 import build
+from grouped_gemm_epilogues_gb300 import binding as b, build
 
 LOWP = os.path.join(build.CSRC, "lowp")
 
@@ -63,8 +64,6 @@ class _Marshal:
 def test_backward_norm_does_not_keep_its_partial_sums_in_the_shared_workspace(monkeypatch):
     """They grow with the width: a captured graph would go on writing to a workspace that a
     wider call has replaced.  The compiled module takes a buffer of the call's own."""
-    from grouped_gemm_epilogues_gb300 import binding as b
-
     def refuse(*args):
         raise AssertionError("shared workspace")
 
@@ -143,3 +142,18 @@ def test_shared_memory_limit_of_first_calls_in_several_threads(tmp_path):
     assert r.returncode == 0, r.stderr
     r = subprocess.run([str(exe)], capture_output=True, text=True, timeout=60)
     assert r.stdout.split() == ["0", "0", str(232448 - 256)], r.stdout + r.stderr
+
+
+def test_compiled_module_calls_the_library_with_the_tensors_device_current():
+    """(A second device is what would show it; here, that the one macro does it for every call.)"""
+    text = open(os.path.join(LOWP, "marshal.cpp")).read()
+    macro = text[text.index("#define GGE_CALL"):]
+    macro = macro[:macro.index("\n\n")]
+    assert macro.index("CUDAGuard") < macro.index("stream(dev)") < macro.index("(expr)")
+    host_only = {"gge_mx_row_bytes", "gge_mx_scale_bytes"}
+    for name in re.findall(r"\b(gge_\w+)\(", text):
+        if name in b._SIGNATURES and name not in host_only and name != "gge_workspace_size_rmsnorm_bwd":
+            line = next(x for x in text.splitlines() if name + "(" in x and not x.startswith("//"))
+            assert line.strip().startswith("GGE_CALL(dev, "), line
+    at = text.index("gge_workspace_size_rmsnorm_bwd(")
+    assert "CUDAGuard" in text[text.rindex("{", 0, at):at]

@@ -37,6 +37,7 @@ def lib(monkeypatch):
     monkeypatch.setattr(b, "_zeroed", zeroed)
     monkeypatch.setattr(b, "load", lambda: lib)
     monkeypatch.setattr(b, "_stream", lambda t: None)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: DEV.index)
     return lib
 
 
