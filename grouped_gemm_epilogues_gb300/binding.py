@@ -13,6 +13,7 @@ import ctypes
 import functools
 import importlib.util
 import inspect
+import operator
 import os
 import threading
 
@@ -594,19 +595,25 @@ class MxTensor:
     """A microscaled matrix (gge_mx_tensor): codes (rows, bytes) or (batch, rows, bytes)
     uint8, scales a contiguous uint8 tensor of gge_mx_scale_bytes a batch, tensor_scale None
     or a one-element fp32 tensor (nvfp4), all on one CUDA device.  ``c`` holds the C struct
-    as bytes."""
+    as bytes, made once: its tensors' contents may change, the tensors may not (another tensor
+    scale is another MxTensor over the same codes and scales)."""
 
-    __slots__ = ("format", "tensor_scale", "device", "c", "_codes", "_scales", "_buffer")
+    __slots__ = ("_format", "_tensor_scale", "_device", "_c", "_codes", "_scales", "_buffer")
 
     def __init__(self, codes, scales, format, rows, cols, tensor_scale=None):
-        self.c = (_marshal or _load_marshal()).mx_wrap(codes, scales, MX_FORMAT[format], rows, cols,
-                                                       tensor_scale)
-        self.device = codes.device
-        self.format, self.tensor_scale = format, tensor_scale
+        self._c = (_marshal or _load_marshal()).mx_wrap(codes, scales, MX_FORMAT[format], rows, cols,
+                                                        tensor_scale)
+        self._device = codes.device
+        self._format, self._tensor_scale = format, tensor_scale
         self._codes, self._scales = codes, scales
 
+    c = property(operator.attrgetter("_c"))
+    device = property(operator.attrgetter("_device"))
+    format = property(operator.attrgetter("_format"))
+    tensor_scale = property(operator.attrgetter("_tensor_scale"))
+
     def _struct(self):
-        return GgeMxTensor.from_buffer_copy(self.c)
+        return GgeMxTensor.from_buffer_copy(self._c)
 
     @property
     def rows(self):
@@ -654,10 +661,10 @@ def mx_empty(rows, cols, format, device=None, batch=None, tensor_scale=None):
     b = 1 if batch is None else batch
     start = (b * rows * row + 511) & ~511
     q = MxTensor.__new__(MxTensor)
-    q._buffer, q.c = (_marshal or _load_marshal()).mx_alloc(
+    q._buffer, q._c = (_marshal or _load_marshal()).mx_alloc(
         start + b * per, start, device.index, fmt, rows, cols, 0 if batch is None else batch, row, per,
         tensor_scale)
-    q.device, q.format, q.tensor_scale = device, format, tensor_scale
+    q._device, q._format, q._tensor_scale = device, format, tensor_scale
     q._codes = q._scales = None
     return q
 
@@ -672,9 +679,9 @@ def _shared(device, need):
 
 def _on(Q, device):
     """The C struct of an MxTensor that has to be on a device."""
-    if Q.device != device:
+    if Q._device != device:
         raise ValueError("MxTensor: tensors on different devices")
-    return Q.c
+    return Q._c
 
 
 def gge_mx_quantize(X, Q, values=None):
@@ -696,10 +703,10 @@ def gge_gemm_mx(A, B, D=None, C=None, PostAct=None, act="none", alpha=1.0, beta=
                 alpha_dev=None, beta_dev=None, config=None, workspace=None):
     """D = alpha * A @ B^T + beta * C and / or PostAct = act(same) of MxTensors A (M, K) and
     B (N, K) (or batched), their tensor scales included."""
-    dev = A.device
+    dev = A._device
     ws = _shared(dev, 256) if workspace is None else _ws(dev, 256, workspace)
     code = (_marshal or _load_marshal()).gemm_mx(
-        A.c, _on(B, dev), dev.index, D, C, PostAct, ACT[act], alpha, beta, alpha_dev, beta_dev,
+        A._c, _on(B, dev), dev.index, D, C, PostAct, ACT[act], alpha, beta, alpha_dev, beta_dev,
         ctypes.addressof(config) if config is not None else 0, ws, False)
     if code:
         raise GgeError(code, "gge_gemm_mx")
@@ -708,10 +715,10 @@ def gge_gemm_mx(A, B, D=None, C=None, PostAct=None, act="none", alpha=1.0, beta=
 def gge_gemm_mx_dact(A, B, PreAct, D, act, PostAct=None, config=None, workspace=None):
     """Backward activation epilogue on MxTensors: D = act'(PreAct) * (A @ B^T), PostAct =
     act(PreAct)."""
-    dev = A.device
+    dev = A._device
     ws = _shared(dev, 256) if workspace is None else _ws(dev, 256, workspace)
     code = (_marshal or _load_marshal()).gemm_mx(
-        A.c, _on(B, dev), dev.index, D, PreAct, PostAct, ACT[act], 1.0, 1.0, None, None,
+        A._c, _on(B, dev), dev.index, D, PreAct, PostAct, ACT[act], 1.0, 1.0, None, None,
         ctypes.addressof(config) if config is not None else 0, ws, True)
     if code:
         raise GgeError(code, "gge_gemm_mx_dact")
