@@ -598,7 +598,8 @@ class MxTensor:
     as bytes, made once: its tensors' contents may change, the tensors may not (another tensor
     scale is another MxTensor over the same codes and scales)."""
 
-    __slots__ = ("_format", "_tensor_scale", "_device", "_c", "_codes", "_scales", "_buffer")
+    __slots__ = ("_format", "_tensor_scale", "_device", "_c", "_codes", "_scales", "_buffer",
+                 "_batched")
 
     def __init__(self, codes, scales, format, rows, cols, tensor_scale=None):
         self._c = (_marshal or _load_marshal()).mx_wrap(codes, scales, MX_FORMAT[format], rows, cols,
@@ -632,7 +633,7 @@ class MxTensor:
         if self._codes is None:   # mx_empty: a view of its one buffer, made when asked for
             c = self._struct()
             row = c.stride_row
-            if c.stride_batch:
+            if self._batched:
                 self._codes = self._buffer.as_strided((c.batch, c.rows, row), (c.stride_batch, row, 1))
             else:
                 self._codes = self._buffer.as_strided((c.rows, row), (row, 1))
@@ -643,7 +644,7 @@ class MxTensor:
         if self._scales is None:
             c = self._struct()
             self._scales = self._buffer.as_strided((c.batch * c.scale_stride_batch,), (1,),
-                                                   c.scales - c.codes)
+                                                   (c.scales or 0) - (c.codes or 0))
         return self._scales
 
 
@@ -657,6 +658,8 @@ def mx_empty(rows, cols, format, device=None, batch=None, tensor_scale=None):
             device = torch.device(device.type, torch.cuda.current_device())
     if device.type != "cuda":
         raise ValueError("mx_empty: not a CUDA device")
+    if rows < 0 or cols < 0 or (batch is not None and batch < 1):
+        raise ValueError("mx_empty: rows and cols may not be negative, batch not below 1")
     row, per = _mx_row_bytes(fmt, cols), _mx_scale_bytes(fmt, rows, cols)
     b = 1 if batch is None else batch
     start = (b * rows * row + 511) & ~511
@@ -666,6 +669,7 @@ def mx_empty(rows, cols, format, device=None, batch=None, tensor_scale=None):
         tensor_scale)
     q._device, q._format, q._tensor_scale = device, format, tensor_scale
     q._codes = q._scales = None
+    q._batched = batch is not None
     return q
 
 

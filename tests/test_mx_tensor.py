@@ -34,3 +34,23 @@ def test_what_the_struct_holds_cannot_be_assigned():
         with pytest.raises(AttributeError):
             setattr(q, name, value)
     assert q.tensor_scale is t
+
+
+@pytest.mark.parametrize("fmt", ["mxfp8", "mxfp4", "nvfp4"])
+def test_mx_empty_shapes(fmt):
+    """codes have a batch dimension exactly where one was asked for, however many rows."""
+    row = b._mx_row_bytes(b.MX_FORMAT[fmt], 100)
+    for rows in (0, 1, 130):
+        per = b._mx_scale_bytes(b.MX_FORMAT[fmt], rows, 100)
+        q = b.mx_empty(rows, 100, fmt, device=DEV)
+        assert q.codes.shape == (rows, row) and q.scales.shape == (per,) and q.batch == 1
+        for batch in (1, 3):
+            q = b.mx_empty(rows, 100, fmt, device=DEV, batch=batch)
+            assert q.codes.shape == (batch, rows, row) and q.scales.shape == (batch * per,) and q.batch == batch
+
+
+@pytest.mark.parametrize("rows,cols,batch", [(4, 64, 0), (4, 64, -1), (-4, 64, None), (4, -64, None), (-4, -64, 2)])
+def test_mx_empty_refuses_sizes_that_hold_nothing(rows, cols, batch):
+    """(batch=0 came out as one batch without memory)"""
+    with pytest.raises(ValueError, match="mx_empty"):
+        b.mx_empty(rows, cols, "mxfp8", device=DEV, batch=batch)
