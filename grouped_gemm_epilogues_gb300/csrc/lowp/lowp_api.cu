@@ -63,8 +63,14 @@ gge_status check_values(const gge_tensor& t, bool any_major) {
   return GGE_ERR_UNSUPPORTED;
 }
 
-// Rows of an output must not overlap.
-bool rows_apart(const gge_tensor& t) { return t.rows <= 1 || t.stride_row >= t.cols; }
+// Rows of an output must not overlap, within a batch or across batches: a batch lies
+// behind the one before, or all batches' first rows lie before the second ones.
+bool rows_apart(const gge_tensor& t) {
+  if (t.rows > 1 && t.stride_row < t.cols) return false;
+  if (t.batch <= 1 || t.rows == 0 || t.cols == 0) return true;
+  if (t.stride_batch >= (t.rows > 1 ? (t.rows - 1) * t.stride_row : 0) + t.cols) return true;
+  return t.stride_batch >= t.cols && t.rows > 1 && t.stride_row >= (t.batch - 1) * t.stride_batch + t.cols;
+}
 
 bool same_shape(const gge_tensor& t, int64_t rows, int64_t cols, int64_t batch) {
   return t.rows == rows && t.cols == cols && t.batch == batch;
@@ -231,6 +237,7 @@ gge_status plan_mx(const gge_gemm_mx_args* a, bool dact, void* ws, size_t ws_byt
     if (t == nullptr) continue;
     s = check_mn(t, M, N, L);
     if (s != GGE_OK) return s;
+    if (t != a->C && !rows_apart(*t)) return GGE_ERR_INVALID_ARG;
   }
   if (N % 8 != 0) return GGE_ERR_UNSUPPORTED;
   s = check_workspace(ws, ws_bytes);

@@ -308,7 +308,9 @@ gge_status gge_gemm_gather_a(const gge_gemm_args* args, const int32_t* a_idx,
  * them (quantisation, and the RMS norm that ends in one), their product, and
  * the norm's backward.  The pages have no counterpart: these are additions of
  * this library.  The conventions above hold (asynchronous on `stream`,
- * validated before any launch, strides in elements unless a field says bytes). */
+ * validated before any launch, strides in elements unless a field says bytes).
+ * Rows of an output may not overlap, nor may its batches: each lies behind the one
+ * before, or row r of every batch before row r + 1 of any.  Inputs may overlap. */
 
 /* Formats.  value = code * block scale (* the tensor scale, GGE_NVFP4).
  *   GGE_MXFP8  e4m3 codes, blocks of 32, scales 2^(byte - 127), byte 255 = NaN

@@ -162,3 +162,33 @@ def test_workspace_size_without_a_gpu_or_with_one(lib):
     n = [lib.gge_workspace_size_rmsnorm_bwd(c) for c in (0, 1, 1000)]
     assert lib.gge_workspace_size_rmsnorm_bwd(-1) == 0
     assert n == [0, 0, 0] or (n[0] > 0 and n[2] - n[0] == 1000 * (n[1] - n[0]))
+
+
+def batched(sb, sr=128, rows=64, cols=128, batch=3):
+    return tensor(rows, cols, batch=batch, sr=sr, sb=sb)
+
+
+OVERLAPPING = [batched(0), batched(64 * 128 - 128), batched(128), batched(128, sr=256), batched(0, rows=1)]
+# (one row a batch; batches after one another; row r of every batch side by side)
+APART = [batched(128, rows=1), batched(64 * 128), batched(128, sr=384)]
+
+
+@pytest.mark.parametrize("v", OVERLAPPING)
+def test_outputs_whose_batches_overlap_are_refused(lib, v):
+    """(they would be written in no particular order)"""
+    rows = v.rows
+    q = mx(rows, 128, batch=3)
+    x = tensor(rows, 128, batch=3)
+    assert lib.gge_mx_quantize(ref(x), ref(q), ref(v), None) == INVALID
+    assert lib.gge_mx_dequantize(ref(q), ref(v), None) == INVALID
+    B = mx(128, 128, batch=3)
+    for kw in (dict(D=v), dict(D=tensor(rows, 128, batch=3), P_=v, act=1)):
+        assert product(lib, A=q, B=B, **kw) == INVALID
+    assert product(lib, A=q, B=B, D=v, C=tensor(rows, 128, batch=3), act=3, dact=True) == INVALID
+
+
+@pytest.mark.parametrize("v", APART)
+def test_inputs_may_overlap_and_outputs_lie_apart_in_either_order(lib, v):
+    """What these calls refuse instead comes after the outputs' check: the workspace."""
+    q, B = mx(v.rows, 128, batch=3), mx(128, 128, batch=3)
+    assert product(lib, A=q, B=B, D=v, C=tensor(v.rows, 128, batch=3, sb=0), n=128) == WORKSPACE
