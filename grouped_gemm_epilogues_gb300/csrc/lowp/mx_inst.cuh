@@ -38,6 +38,8 @@ cudaError_t mx_launch_one(const MxMaps& m, const MxParams& mp, const LaunchShape
   return cudaLaunchKernelEx(&cfg, mx_gemm_kernel<BN, CG, FMT, TR>, m.a, m.b, m.sa, m.sb, mp);
 }
 
+// (Shared memory and registers; the tensor memory's columns need no count of their own: the
+// registers leave room for one CTA an SM.)
 template <int BN, int CG, int FMT, bool TR>
 int mx_units_one(size_t smem, int cluster) {
   if (allow_smem<mx_gemm_kernel<BN, CG, FMT, TR>>() != cudaSuccess) return -1;
