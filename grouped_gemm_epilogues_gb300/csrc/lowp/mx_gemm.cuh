@@ -354,8 +354,7 @@ __device__ __forceinline__ void mx_epilogue_role(const MxParams& mp, const Share
     const int32_t row = row_base + lane;
     const bool has_c = p.c != nullptr && lane < rows_valid;
     // this warp's chunks are half, half + 2, ...; the first accumulator's walk starts at
-    // its last pair, the second one's at its first: the columns both own.  A split
-    // tile's slices then rotate on, so that they finish different chunks last.
+    // its last pair, the second one's at its first: the columns both own
     const int first = (Cfg::kOverlap && acc == 0) ? kMine - 1 : 0;
     CRegs cnext = {};
     if (mp.splits == 1 && has_c && tc.n0 + (half + 2 * first) * 32 < p.N)

@@ -342,10 +342,10 @@ __global__ void __launch_bounds__(norm_threads<R>())
 // Rows too long for a block's registers: one value a lane, and a second pass that
 // reads the row again.  A scale's block is a warp's 32 (or half a warp's 16) lanes.
 template <typename T, int FMT>
-__global__ void norm_long_kernel(const __grid_constant__ NormParams p) {
+__global__ void __launch_bounds__(kMaxThreads) norm_long_kernel(const __grid_constant__ NormParams p) {
   __shared__ float slots[64];
   ptx::griddep_launch_dependents();
-  const int per_block = 1, sub = 0, t = threadIdx.x, tpr = blockDim.x;
+  const int t = threadIdx.x, tpr = blockDim.x;
   const int lane = threadIdx.x & 31;
   const int32_t cols = p.cols;
   ptx::griddep_wait();
@@ -353,10 +353,7 @@ __global__ void norm_long_kernel(const __grid_constant__ NormParams p) {
   const T* x = static_cast<const T*>(p.x);
   const T* res = static_cast<const T*>(p.residual);
   int flip = 0;
-  for (int64_t row0 = static_cast<int64_t>(blockIdx.x) * per_block; row0 < p.rows;
-       row0 += static_cast<int64_t>(gridDim.x) * per_block) {
-    const int64_t row = row0 + sub;
-    const bool live = row < p.rows;
+  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
     float ss = 0.f;
     auto value = [&](int64_t col, bool write) {
       float a = to_float<T>(x[row * p.ldx + col]);
@@ -367,23 +364,21 @@ __global__ void norm_long_kernel(const __grid_constant__ NormParams p) {
       }
       return a;
     };
-    if (live) {
 #pragma unroll 4
-      for (int32_t col = t; col < cols; col += tpr) {
-        const float a = value(col, false);
-        ss = fmaf(a, a, ss);
-      }
+    for (int32_t col = t; col < cols; col += tpr) {
+      const float a = value(col, false);
+      ss = fmaf(a, a, ss);
     }
     ss = row_sum(ss, tpr, slots, flip, 0);
     flip ^= 1;
     const float inv = __frsqrt_rn(ss / static_cast<float>(cols) + p.eps);
-    if (live && t == 0 && p.inv != nullptr) p.inv[row] = inv;
+    if (t == 0 && p.inv != nullptr) p.inv[row] = inv;
     // columns up to the end of the last scale word (whole warps take part)
     int64_t end = cols;
     if constexpr (FMT != FMT_NONE) end = scale_span<FMT>(p.q.kgroups);
     for (int64_t col = t; col - lane < end; col += tpr) {
       float a = 0.f;
-      if (live && col < cols) {
+      if (col < cols) {
         a = (value(col, true) * inv) * load_any(p.weight, col, p.w_dtype);
         if (p.y != nullptr) static_cast<T*>(p.y)[row * p.ldy + col] = from_float<T>(a);
       }
@@ -400,20 +395,20 @@ __global__ void norm_long_kernel(const __grid_constant__ NormParams p) {
         float back;
         if constexpr (FMT == FMT_MXFP8) {
           const uint32_t code = pack_e4m3x4(c, 0.f, 0.f, 0.f) & 0xffu;
-          if (live && col < ((cols + 31) & ~31)) p.q.codes[row * p.q.ld + col] = static_cast<uint8_t>(code);
+          if (col < ((cols + 31) & ~31)) p.q.codes[row * p.q.ld + col] = static_cast<uint8_t>(code);
           back = e4m3x2_to_float2(code).x;
         } else {
           const float next = __shfl_down_sync(0xffffffffu, c, 1);
           const float two[8] = {c, next, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
           const uint32_t code = pack_e2m1x8(two) & 0xffu;
-          if (live && (lane & 1) == 0 && col < ((cols + 31) & ~31))
+          if ((lane & 1) == 0 && col < ((cols + 31) & ~31))
             p.q.codes[row * p.q.ld + (col >> 1)] = static_cast<uint8_t>(code);
           back = e2m1x2_to_float2(code).x;
         }
-        if (live && lane % kLanes == 0 && block < p.q.kgroups * 4)
+        if (lane % kLanes == 0 && block < p.q.kgroups * 4)
           p.q.scales[scale_word(row, block >> 2, p.q.kgroups) + (block & 3)] =
               static_cast<uint8_t>(col < cols ? s : 0u);
-        if (live && p.q.values != nullptr && col < cols) {
+        if (p.q.values != nullptr && col < cols) {
           back *= unit;
           if constexpr (FMT == FMT_NVFP4) back *= tscale;
           store_any(p.q.values, row * p.q.ldv + col, p.q.v_dtype, back);
@@ -675,7 +670,7 @@ __global__ void __launch_bounds__(kRowThreads)
 // Rows too long for a block's registers: one value a lane, the rows read twice.  dw
 // is summed by columns in a kernel of its own.
 template <typename T>
-__global__ void norm_bwd_long_kernel(const __grid_constant__ NormBwdParams p) {
+__global__ void __launch_bounds__(kMaxThreads) norm_bwd_long_kernel(const __grid_constant__ NormBwdParams p) {
   __shared__ float slots[64];
   ptx::griddep_launch_dependents();
   const int t = threadIdx.x, tpr = blockDim.x;

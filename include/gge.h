@@ -349,7 +349,8 @@ size_t gge_mx_scale_bytes(int32_t format, int64_t rows, int64_t cols);
 
 /* q = x quantised.  x: [rows, cols, batch] in bf16, f16 or f32, with
  * stride_col == 1 or stride_row == 1 (the transpose of a row-major matrix, as
- * the weight-gradient products need it); rows may start on any element.
+ * the weight-gradient products need it, of at most 65535 * 64 rows:
+ * GGE_ERR_UNSUPPORTED beyond); rows may start on any element.
  *   GGE_MXFP8, GGE_MXFP4: a block's scale is the smallest power of two 2^e (e >=
  *     -127) with max|x| <= 2^e * (448 or 6); code = round(x / 2^e), exact but for
  *     the rounding (to nearest, ties to even).

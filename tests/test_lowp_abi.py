@@ -192,3 +192,9 @@ def test_inputs_may_overlap_and_outputs_lie_apart_in_either_order(lib, v):
     """What these calls refuse instead comes after the outputs' check: the workspace."""
     q, B = mx(v.rows, 128, batch=3), mx(128, 128, batch=3)
     assert product(lib, A=q, B=B, D=v, C=tensor(v.rows, 128, batch=3, sb=0), n=128) == WORKSPACE
+
+
+def test_transposed_source_of_too_many_rows_is_refused(lib):
+    rows = 65535 * 64 + 1
+    x = tensor(rows, 2, sr=1, sc=rows)
+    assert lib.gge_mx_quantize(ref(x), ref(mx(rows, 2)), None, None) == UNSUPPORTED
