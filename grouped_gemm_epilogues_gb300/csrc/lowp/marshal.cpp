@@ -1,7 +1,7 @@
 // Argument marshalling of the low-precision entry points for Python: torch tensors
 // in, the C structs of include/gge.h out, one call each.  The checks are those of
 // the arguments' Python side (types, devices, shapes of the plain vectors); the
-// library checks the rest.  A call this way costs about 3 us of host time, through
+// library checks the rest.  A call this way costs 2 to 3 us of host time, through
 // ctypes 6 to 9, which is what a small norm or product takes on the GPU.
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>

@@ -36,8 +36,9 @@
 // cycles; an SM takes in 64 bytes a cycle), and the power cap lowers the clock.
 // 8192^3 nvfp4 161-165 us in short bursts (6.7-6.8 PFLOP/s, 3.5 times bf16's measured
 // rate), 182-185 us under a lasting load; mxfp8 4096^3 46 us, with C, gelu and two
-// outputs 55.  A few rows are bound by the weights' bytes: 16 x 19456 x 8192 nvfp4
-// 18.2 us (4.9 TB/s; 3.3 us are the launch of any shape).
+// outputs 54; the backward activation epilogue with silu 52, with act(C) too 64.  A few
+// rows are bound by the weights' bytes: 16 x 19456 x 8192 nvfp4 18.2 us (4.9 TB/s; 3.3 us
+// are the launch of any shape).
 #pragma once
 
 #include "../gge_kernel.cuh"
