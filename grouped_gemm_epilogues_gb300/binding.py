@@ -89,6 +89,40 @@ class GgeRmsnormBwdArgs(ctypes.Structure):
                 ("inv_rms", ctypes.c_void_p), ("dweight", ctypes.c_void_p)]
 
 
+class GgeB128Tensor(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p),
+                ("dtype", c_i32), ("block_rows", c_i32),
+                ("rows", c_i64), ("cols", c_i64), ("batch", c_i64), ("stride_row", c_i64),
+                ("stride_batch", c_i64), ("scale_stride_row", c_i64), ("scale_stride_col", c_i64),
+                ("scale_stride_batch", c_i64)]
+
+
+class GgeGemmB128Args(ctypes.Structure):
+    _fields_ = [("A", GgeB128Tensor), ("B", GgeB128Tensor), ("C", ctypes.c_void_p),
+                ("D", ctypes.c_void_p), ("PostAct", ctypes.c_void_p), ("C8", ctypes.c_void_p),
+                ("D8", ctypes.c_void_p), ("PostAct8", ctypes.c_void_p),
+                ("cu_seqlens_m", ctypes.c_void_p), ("num_groups", c_i32), ("act", c_i32),
+                ("alpha", ctypes.c_float), ("beta", ctypes.c_float),
+                ("alpha_dev", ctypes.c_void_p), ("beta_dev", ctypes.c_void_p),
+                ("config", ctypes.c_void_p)]
+
+
+class GgeLayernormArgs(ctypes.Structure):
+    _fields_ = [("x", GgeTensor), ("residual", ctypes.c_void_p),
+                ("residual_out", ctypes.c_void_p), ("y", ctypes.c_void_p), ("q", ctypes.c_void_p),
+                ("values", ctypes.c_void_p), ("h8", ctypes.c_void_p), ("weight", ctypes.c_void_p),
+                ("bias", ctypes.c_void_p), ("param_dtype", c_i32), ("eps", ctypes.c_float),
+                ("mean", ctypes.c_void_p), ("rstd", ctypes.c_void_p)]
+
+
+class GgeLayernormBwdArgs(ctypes.Structure):
+    _fields_ = [("dy", GgeTensor), ("h", ctypes.c_void_p), ("h8", ctypes.c_void_p),
+                ("dh", ctypes.c_void_p), ("dx", GgeTensor), ("weight", ctypes.c_void_p),
+                ("weight_dtype", c_i32), ("reserved", c_i32), ("mean", ctypes.c_void_p),
+                ("rstd", ctypes.c_void_p), ("dweight", ctypes.c_void_p),
+                ("dbias", ctypes.c_void_p)]
+
+
 # every function include/gge.h declares, with its ctypes signature
 _SIGNATURES = {
     "gge_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(GgeGemmArgs), c_i32]),
@@ -137,6 +171,19 @@ _SIGNATURES = {
     "gge_workspace_size_rmsnorm_bwd": (ctypes.c_size_t, [c_i64]),
     "gge_rmsnorm_bwd": (c_i32, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t,
                                 ctypes.c_void_p]),
+    "gge_b128_quantize": (c_i32, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                  ctypes.c_void_p]),
+    "gge_b128_transpose": (c_i32, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                   ctypes.c_void_p]),
+    "gge_b128_dequantize": (c_i32, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
+    "gge_gemm_b128": (c_i32, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t,
+                              ctypes.c_void_p]),
+    "gge_gemm_b128_dact": (c_i32, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t,
+                                   ctypes.c_void_p]),
+    "gge_layernorm": (c_i32, [ctypes.c_void_p, ctypes.c_void_p]),
+    "gge_workspace_size_layernorm_bwd": (ctypes.c_size_t, [c_i64]),
+    "gge_layernorm_bwd": (c_i32, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t,
+                                  ctypes.c_void_p]),
 }
 
 _lib = None
@@ -749,3 +796,137 @@ def gge_rmsnorm_bwd(dY, H, weight, inv_rms, dX, dW=None, dH=None, workspace=None
     code = (_marshal or _load_marshal()).rmsnorm_bwd(dY, H, weight, inv_rms, dX, dW, dH, ws)
     if code:
         raise GgeError(code, "gge_rmsnorm_bwd")
+
+
+# ------------------------------ 8 bits with a scale for each block of 128
+
+class B128Tensor:
+    """A matrix of 8-bit codes with one fp32 scale for each block of ``block_rows`` (1 or 128)
+    rows x 128 columns (gge_b128_tensor): codes float8_e4m3fn or float8_e5m2 (rows, cols) or
+    (batch, rows, cols), rows contiguous and 16-byte aligned; scales float32 (row blocks, column
+    blocks) or (batch, ...) of any strides, on one CUDA device.  ``c`` holds the C struct as
+    bytes, made once: its tensors' contents may change, the tensors may not."""
+
+    __slots__ = ("_codes", "_scales", "_block_rows", "_device", "_c")
+
+    def __init__(self, codes, scales, block_rows=1):
+        self._c = (_marshal or _load_marshal()).b128_wrap(codes, scales, block_rows)
+        self._codes, self._scales, self._block_rows = codes, scales, block_rows
+        self._device = codes.device
+
+    c = property(operator.attrgetter("_c"))
+    codes = property(operator.attrgetter("_codes"))
+    scales = property(operator.attrgetter("_scales"))
+    block_rows = property(operator.attrgetter("_block_rows"))
+    device = property(operator.attrgetter("_device"))
+    dtype = property(operator.attrgetter("_codes.dtype"))
+    shape = property(operator.attrgetter("_codes.shape"))
+
+
+def b128_empty(rows, cols, block_rows=1, dtype=torch.float8_e4m3fn, device=None, batch=None):
+    """A B128Tensor with room for (rows, cols) or (batch, rows, cols) values on a CUDA device,
+    its rows 16-byte aligned and its scales column block by column block."""
+    device = _cuda_device(device)
+    if device.type != "cuda":
+        raise ValueError("b128_empty: not a CUDA device")
+    if rows < 0 or cols < 0 or (batch is not None and batch < 1):
+        raise ValueError("b128_empty: rows and cols may not be negative, batch not below 1")
+    if block_rows not in (1, 128) or dtype not in (torch.float8_e4m3fn, torch.float8_e5m2):
+        raise ValueError("b128_empty: block_rows is 1 or 128, dtype float8_e4m3fn or float8_e5m2")
+    lead = () if batch is None else (batch,)
+    codes = torch.empty(*lead, rows, (cols + 15) // 16 * 16, dtype=dtype, device=device)
+    scales = torch.empty(*lead, (cols + 127) // 128, -(-rows // block_rows), device=device)
+    return B128Tensor(codes[..., :cols], scales.transpose(-1, -2), block_rows)
+
+
+def _either(t, device):
+    """A tensor as it is, a B128Tensor (which has to be on the device) as its C struct."""
+    return _on(t, device) if t.__class__ is B128Tensor else t
+
+
+def gge_b128_quantize(X, Q, values=None):
+    """Q (a B128Tensor) = X quantised; X (rows, cols) or (batch, rows, cols), row-major or a
+    transposed view.  values: optional output, the numbers that the codes stand for."""
+    code = (_marshal or _load_marshal()).b128_quantize(X, _on(Q, X.device), values)
+    if code:
+        raise GgeError(code, "gge_b128_quantize")
+
+
+def gge_b128_transpose(X, Q, values=None):
+    """Q = the transpose of B128Tensor X's numbers, quantised anew along its own rows."""
+    dev = X._device
+    code = (_marshal or _load_marshal()).b128_transpose(X._c, _on(Q, dev), values, dev.index)
+    if code:
+        raise GgeError(code, "gge_b128_transpose")
+
+
+def gge_b128_dequantize(Q, Y):
+    """Y (bf16, f16 or f32) = the numbers that Q's codes stand for."""
+    code = (_marshal or _load_marshal()).b128_dequantize(_on(Q, Y.device), Y)
+    if code:
+        raise GgeError(code, "gge_b128_dequantize")
+
+
+def _gemm_b128(name, A, B, D, C, PostAct, act, alpha, beta, alpha_dev, beta_dev, config, workspace,
+               dact, cu):
+    dev = A._device
+    ws = _shared(dev, 256) if workspace is None else _ws(dev, 256, workspace)
+    code = (_marshal or _load_marshal()).gemm_b128(
+        A._c, _on(B, dev), dev.index, _either(D, dev), _either(C, dev), _either(PostAct, dev),
+        ACT[act], alpha, beta, alpha_dev, beta_dev,
+        ctypes.addressof(config) if config is not None else 0, ws, dact, cu)
+    if code:
+        raise GgeError(code, name)
+
+
+def gge_gemm_b128(A, B, D=None, C=None, PostAct=None, act="none", alpha=1.0, beta=1.0,
+                  alpha_dev=None, beta_dev=None, config=None, workspace=None):
+    """D = alpha * A @ B^T + beta * C and / or PostAct = act(same) of B128Tensors A (M, K) and
+    B (N, K) (or batched).  C, D and PostAct: tensors in 16 or 32 bits, or B128Tensors with
+    block_rows 1 (a pre-activation kept in 8 bits, the next product's operand)."""
+    _gemm_b128("gge_gemm_b128", A, B, D, C, PostAct, act, alpha, beta, alpha_dev, beta_dev, config,
+               workspace, False, None)
+
+
+def gge_gemm_b128_dact(A, B, PreAct, D, act, PostAct=None, cu_seqlens_m=None, config=None,
+                       workspace=None):
+    """Backward activation epilogue on B128Tensors: D = act'(PreAct) * (A @ B^T), PostAct =
+    act(PreAct), each a tensor or a B128Tensor.  cu_seqlens_m: as in gge_gemm_b128_varlen_m."""
+    _gemm_b128("gge_gemm_b128_dact", A, B, D, PreAct, PostAct, act, 1.0, 1.0, None, None, config,
+               workspace, True, cu_seqlens_m)
+
+
+def gge_gemm_b128_varlen_m(A, B, cu_seqlens_m, D=None, PostAct=None, act="none", C=None, alpha=1.0,
+                           beta=1.0, alpha_dev=None, beta_dev=None, config=None, workspace=None):
+    """gge_gemm_b128 of grouped rows: A (total_M, K), B (G, N, K), cu_seqlens_m int32 (G+1,) on
+    device; rows cu[g] .. cu[g+1]-1 are multiplied with B[g].  Rows of no group are not written."""
+    _gemm_b128("gge_gemm_b128_varlen_m", A, B, D, C, PostAct, act, alpha, beta, alpha_dev, beta_dev,
+               config, workspace, False, cu_seqlens_m)
+
+
+def gge_layernorm(X, weight=None, bias=None, Y=None, residual=None, residual_out=None, Q=None,
+                  values=None, H8=None, mean=None, rstd=None, eps=1e-5):
+    """h = X + residual (rounded to X's type, written to residual_out), mean and rstd = 1 /
+    sqrt(var + eps) of its rows, Y = (h - mean) * rstd * weight + bias; Q (a B128Tensor) = the
+    same quantised, values = the numbers that Q's codes stand for; H8 (a B128Tensor) = h
+    quantised, for the backward.  X (rows, cols); every output is optional."""
+    dev = X.device
+    code = (_marshal or _load_marshal()).layernorm(
+        X, weight, bias, Y, residual, residual_out, _on(Q, dev) if Q is not None else None, values,
+        _on(H8, dev) if H8 is not None else None, mean, rstd, eps)
+    if code:
+        raise GgeError(code, "gge_layernorm")
+
+
+def gge_layernorm_bwd(dY, H, weight, mean, rstd, dX, dW=None, dB=None, dH=None, workspace=None):
+    """Backward of gge_layernorm: dX (the gradient of X and of the residual) from dY, the saved H
+    (residual_out, or X, or H8), mean and rstd; dW and dB (fp32, optional); dH the gradient
+    reaching H directly.  The sums over rows take gge_workspace_size_layernorm_bwd(cols) bytes:
+    memory of the call's own from torch's allocator on the current stream, or the caller's
+    ``workspace``."""
+    dev = dY.device
+    ws = None if workspace is None else _ws(dev, 0, workspace)
+    code = (_marshal or _load_marshal()).layernorm_bwd(dY, _either(H, dev), weight, mean, rstd, dX, dW,
+                                                       dB, dH, ws)
+    if code:
+        raise GgeError(code, "gge_layernorm_bwd")

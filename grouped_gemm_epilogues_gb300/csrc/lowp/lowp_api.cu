@@ -4,7 +4,7 @@
 #include <cstring>
 #include <mutex>
 
-#include "../gge_host.h"
+#include "lowp_host.h"
 #include "lowp_launch.h"
 #include "mx_launch.h"
 
@@ -13,17 +13,11 @@ namespace {
 
 using lowp::QuantPtrs;
 
-// (a warp's and a block's columns past the last one still have to fit 32 bits)
-constexpr int64_t kMaxCols = kMaxExtent - 4096;
-
 int mx_block(int32_t f) { return f == GGE_NVFP4 ? 16 : 32; }
 int mx_bits(int32_t f) { return f == GGE_MXFP8 ? 8 : 4; }
 bool mx_known(int32_t f) { return f >= GGE_MXFP8 && f <= GGE_NVFP4; }
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int64_t mx_row_bytes(int32_t f, int64_t cols) { return ceil_div(cols, 32) * 32 * mx_bits(f) / 8; }
 int64_t mx_kgroups(int32_t f, int64_t cols) { return ceil_div(ceil_div(cols, mx_block(f)), 4); }
-
-bool is_value_type(int32_t dt) { return dt == GGE_BF16 || dt == GGE_F16 || dt == GGE_F32; }
 
 gge_status check_mx(const gge_mx_tensor& q) {
   if (!mx_known(q.format) || q.reserved != 0) return GGE_ERR_INVALID_ARG;
@@ -45,49 +39,6 @@ gge_status check_mx(const gge_mx_tensor& q) {
       (reinterpret_cast<uintptr_t>(q.scales) & 127u) != 0)
     return GGE_ERR_ALIGNMENT;
   return GGE_OK;
-}
-
-// A row-major (or, `any_major`, column-major) view of 16- or 32-bit values that
-// may start on any element.
-gge_status check_values(const gge_tensor& t, bool any_major) {
-  if (t.reserved != 0) return GGE_ERR_INVALID_ARG;
-  if (!is_value_type(t.dtype)) return GGE_ERR_UNSUPPORTED;
-  if (t.rows < 0 || t.cols < 0 || t.batch < 1) return GGE_ERR_INVALID_ARG;
-  if (t.rows > kMaxExtent || t.cols > kMaxCols || t.batch > 65535) return GGE_ERR_UNSUPPORTED;
-  if (t.rows == 0 || t.cols == 0) return GGE_OK;
-  if (t.ptr == nullptr) return GGE_ERR_INVALID_ARG;
-  if ((reinterpret_cast<uintptr_t>(t.ptr) & (elem_bytes(t.dtype) - 1)) != 0) return GGE_ERR_ALIGNMENT;
-  if (t.stride_row < 0 || t.stride_col < 0 || t.stride_batch < 0) return GGE_ERR_INVALID_ARG;
-  if (t.cols == 1 || t.stride_col == 1) return GGE_OK;
-  if (any_major && (t.rows == 1 || t.stride_row == 1)) return GGE_OK;
-  return GGE_ERR_UNSUPPORTED;
-}
-
-// Rows of an output must not overlap, within a batch or across batches: a batch lies
-// behind the one before, or all batches' first rows lie before the second ones.
-bool rows_apart(const gge_tensor& t) {
-  if (t.rows > 1 && t.stride_row < t.cols) return false;
-  if (t.batch <= 1 || t.rows == 0 || t.cols == 0) return true;
-  if (t.stride_batch >= (t.rows > 1 ? (t.rows - 1) * t.stride_row : 0) + t.cols) return true;
-  return t.stride_batch >= t.cols && t.rows > 1 && t.stride_row >= (t.batch - 1) * t.stride_batch + t.cols;
-}
-
-bool same_shape(const gge_tensor& t, int64_t rows, int64_t cols, int64_t batch) {
-  return t.rows == rows && t.cols == cols && t.batch == batch;
-}
-
-// Every row (and batch) of the view starts on a 16-byte boundary.
-bool rows_aligned(const gge_tensor& t) {
-  const int es = elem_bytes(t.dtype);
-  return aligned16(t.ptr) && (t.rows <= 1 || t.stride_row * es % 16 == 0) &&
-         (t.batch <= 1 || t.stride_batch * es % 16 == 0);
-}
-
-// Every row of `t` starts as far past a 16-byte boundary as the same row of `x`.
-bool rows_alike(const gge_tensor& t, const gge_tensor& x) {
-  const int64_t es = elem_bytes(x.dtype);
-  return ((reinterpret_cast<uintptr_t>(t.ptr) ^ reinterpret_cast<uintptr_t>(x.ptr)) & 15u) == 0 &&
-         (t.rows <= 1 || (t.stride_row - x.stride_row) * es % 16 == 0);
 }
 
 // A quantised output (and its values) as the kernels take it.
@@ -114,8 +65,6 @@ gge_status quant_ptrs(const gge_mx_tensor& q, const gge_tensor* values, QuantPtr
   }
   return GGE_OK;
 }
-
-gge_status launched(cudaError_t e) { return e == cudaSuccess ? GGE_OK : GGE_ERR_CUDA; }
 
 // ------------------------------------------------------------ the product
 

@@ -456,6 +456,168 @@ size_t gge_workspace_size_rmsnorm_bwd(int64_t cols);
 gge_status gge_rmsnorm_bwd(const gge_rmsnorm_bwd_args* args, void* workspace,
                            size_t workspace_bytes, gge_stream_t stream);
 
+/* ---- 8 bits with a scale for each block of 128 ---------------------------
+ * Operands in 8-bit floating point with one fp32 scale (of any value) for each
+ * block of 128 columns of a row, or of 128 rows x 128 columns; what makes them
+ * (quantisation, transposition, the layer norm and the product's own epilogue),
+ * their product, and the backward from activations that were kept in this form.
+ * Additions of this library, under the conventions of the section above. */
+
+/*
+ * A matrix [rows, cols, batch] of 8-bit codes; blocks run along cols (a product's K).
+ *   codes   row-major, dtype GGE_E4M3 or GGE_E5M2; base and byte strides 16-byte
+ *           aligned.  Bytes between a row's end and the next row are not touched.
+ *   scales  fp32; the scale of row r, column block b (b = col / 128) of batch l is
+ *           scales[(r / block_rows) * scale_stride_row + b * scale_stride_col +
+ *           l * scale_stride_batch].  block_rows is 1 or 128.  The kernels read
+ *           scale_stride_row == 1 best (blocks of neighbouring rows together).
+ * value = code * scale.
+ */
+typedef struct gge_b128_tensor {
+  void* codes;
+  float* scales;
+  int32_t dtype;      /* GGE_E4M3 or GGE_E5M2 */
+  int32_t block_rows; /* 1 or 128             */
+  int64_t rows, cols, batch;
+  int64_t stride_row, stride_batch; /* of codes */
+  int64_t scale_stride_row, scale_stride_col, scale_stride_batch; /* in floats */
+} gge_b128_tensor;
+
+/* q = x quantised.  x: [rows, cols, batch] in bf16, f16 or f32, with stride_col == 1
+ * or stride_row == 1 (a transposed view); rows may start on any element.  For each
+ * block, in fp32 arithmetic with the top value t = 448 (e4m3) or 57344 (e5m2):
+ *   scale = max(max|x| * (1 / t), 2^-126)     code = round(x * (1 / scale))
+ * to nearest, ties to even, at most t in size.  A block that holds an infinity or a
+ * NaN gets a NaN scale: all of it reads back as NaN.
+ * values (may be NULL): the numbers that the codes stand for, [rows, cols, batch]
+ * row-major in bf16, f16 or f32 (rounded once). */
+gge_status gge_b128_quantize(const gge_tensor* x, const gge_b128_tensor* q, const gge_tensor* values,
+                             gge_stream_t stream);
+
+/* q = the transpose of x's numbers, quantised anew along its own rows: x [rows, cols,
+ * batch] -> q [cols, rows, batch], as the weight gradient's product needs an
+ * activation that was kept in 8 bits.  values as above. */
+gge_status gge_b128_transpose(const gge_b128_tensor* x, const gge_b128_tensor* q,
+                              const gge_tensor* values, gge_stream_t stream);
+
+/* y = the numbers that q's codes stand for, row-major in bf16, f16 or f32. */
+gge_status gge_b128_dequantize(const gge_b128_tensor* q, const gge_tensor* y, gge_stream_t stream);
+
+/*
+ * D       = alpha * S + beta * C      S[m, n] = sum over blocks b of K of
+ * PostAct = act(same value, before rounding)      sA[m, b] sB[n, b] sum_{k in b} a[m, k] b[n, k]
+ *   A [M, K, L] and B [N, K, L], each with codes of either type and blocks of 1 or
+ *   128 rows.  The sum within a block runs on the tensor core in fp32; blocks are
+ *   scaled and added in fp32, in the order of K.
+ *   C, D and PostAct: [M, N, L] as a gge_tensor (16 bits or fp32, as in gge_gemm) or,
+ *   in the field that ends in 8, as a gge_b128_tensor with block_rows 1; at most one of the
+ *   two each.  An 8-bit output is quantised from the fp32 value as gge_b128_quantize does
+ *   (D8: a pre-activation kept for the backward; PostAct8: the next product's operand).
+ *   D and PostAct are optional, not both absent; PostAct is required when act is not NONE.
+ *   N must be a multiple of 8; M, K and L may be anything.  K == 0 gives beta * C.
+ *   cu_seqlens_m (may be NULL): grouped rows, as gge_gemm_varlen_m: DEVICE int32
+ *   [num_groups + 1], A [total_M, K, 1], B [N, K, num_groups], C, D and PostAct
+ *   [total_M, N, 1]; row r of group g, cu[g] <= r < cu[g + 1], is multiplied with B[g].
+ *   Rows of no group are not written.  At most 1024 groups.  An offset outside [0, total_M]
+ *   or below the one before is reported as GGE_ERR_INDEX_RANGE.
+ *   config (may be NULL): tile_n 0 (automatic), 256 (a CTA pair, 256 x 256), 128 or 64
+ *   (one CTA, 128 rows; 64 not with 8-bit outputs); num_ctas, raster_band, stages, timeout_ns;
+ *   of the flags those for no split, raster along N and the test hook.
+ * Few tiles are split along K over a cluster of 2, 4 or 8 CTAs, which add their sums in a
+ * fixed order through shared memory (not grouped rows).  The workspace holds the status
+ * words (at least 256 bytes; NULL: device errors go unrecorded).
+ */
+typedef struct gge_gemm_b128_args {
+  gge_b128_tensor A;
+  gge_b128_tensor B;
+  const gge_tensor* C;
+  const gge_tensor* D;
+  const gge_tensor* PostAct;
+  const gge_b128_tensor* C8;
+  const gge_b128_tensor* D8;
+  const gge_b128_tensor* PostAct8;
+  const int32_t* cu_seqlens_m;
+  int32_t num_groups;
+  int32_t act;
+  float alpha;
+  float beta;
+  const float* alpha_dev;
+  const float* beta_dev;
+  const gge_config* config;
+} gge_gemm_b128_args;
+gge_status gge_gemm_b128(const gge_gemm_b128_args* args, void* workspace, size_t workspace_bytes,
+                         gge_stream_t stream);
+
+/* The backward activation epilogue (as gge_gemm_dact): with S the incoming gradient and
+ * C or C8 (one of them required) the pre-activation x, D = act'(x) * S (required, in either
+ * form) and PostAct = act(x) (optional); act is not NONE, alpha and beta are not used.
+ * Grouped rows as above. */
+gge_status gge_gemm_b128_dact(const gge_gemm_b128_args* args, void* workspace,
+                              size_t workspace_bytes, gge_stream_t stream);
+
+/*
+ * Layer norm with the residual's addition:
+ *   h = round(x + residual)  (h = x without one)
+ *   mean, var = of a row of h      rstd = 1 / sqrt(var + eps)
+ *   y = (h - mean) * rstd * weight + bias
+ *   x, residual, residual_out (h), y: [rows, cols, 1] of one type (bf16, f16 or f32),
+ *     stride_col == 1, rows may start on any element; every output may be NULL, and
+ *     residual_out may be x or residual itself.  residual_out is written only when there
+ *     is a residual.
+ *   weight, bias (each may be NULL: 1 and 0): `cols` contiguous values of param_dtype.
+ *   mean, rstd: fp32 [rows].
+ *   q, values: y quantised from fp32 as gge_b128_quantize does (block_rows 1), and the
+ *     numbers that its codes stand for (values needs q).
+ *   h8: h quantised (block_rows 1), as the backward may read it.
+ */
+typedef struct gge_layernorm_args {
+  gge_tensor x;
+  const gge_tensor* residual;
+  const gge_tensor* residual_out;
+  const gge_tensor* y;
+  const gge_b128_tensor* q;
+  const gge_tensor* values;
+  const gge_b128_tensor* h8;
+  const void* weight;
+  const void* bias;
+  int32_t param_dtype; /* gge_dtype */
+  float eps;
+  float* mean;
+  float* rstd;
+} gge_layernorm_args;
+gge_status gge_layernorm(const gge_layernorm_args* args, gge_stream_t stream);
+
+/*
+ * Its backward, from the saved h (in 16 or 32 bits, or in 8 bits: exactly one of h and h8),
+ * mean and rstd:
+ *   n = (h - mean) * rstd      g = dy * weight
+ *   dx = rstd * (g - mean(g) - n * mean(g * n)) + dh
+ *   dweight = sum over rows of dy * n      dbias = sum over rows of dy   (fp32, in a fixed
+ *   order)
+ * dx is the gradient of x and of the residual alike.  dh (may be NULL): the gradient that
+ * reaches residual_out directly.  dy, h, dh and dx: [rows, cols, 1] of one type; dx may be dy,
+ * h or dh itself.  weight, dweight and dbias may be NULL.  A quantised output's dy passes
+ * through unchanged.  The workspace (256-byte aligned) must hold
+ * gge_workspace_size_layernorm_bwd(cols) bytes when dweight or dbias is given.
+ */
+typedef struct gge_layernorm_bwd_args {
+  gge_tensor dy;
+  const gge_tensor* h;
+  const gge_b128_tensor* h8;
+  const gge_tensor* dh;
+  gge_tensor dx;
+  const void* weight;
+  int32_t weight_dtype;
+  int32_t reserved;
+  const float* mean;
+  const float* rstd;
+  float* dweight;
+  float* dbias;
+} gge_layernorm_bwd_args;
+size_t gge_workspace_size_layernorm_bwd(int64_t cols);
+gge_status gge_layernorm_bwd(const gge_layernorm_bwd_args* args, void* workspace,
+                             size_t workspace_bytes, gge_stream_t stream);
+
 /* gge_gemm_act without a caller workspace, for callers that cannot allocate
  * device memory where they run the GEMM (a host framework that owns all device
  * memory through its own arena or caching allocator, or a latency-critical path

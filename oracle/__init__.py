@@ -32,11 +32,13 @@ Modules:
   tiles       -- the set of output tiles a schedule must cover exactly once.
   lowp        -- microscaled formats (quantisation, layout, decoding), RMS norm
                  and its backward.
+  b128        -- 8-bit codes with a scale for each block of 128, layer norm and
+                 its backward.
 
 Every function is pinned by ``tests/test_oracle_pins.py`` (lowp:
-``tests/test_lowp_oracle.py``) against values fixed
+``tests/test_lowp_oracle.py``, b128: ``tests/test_b128_oracle.py``) against values fixed
 by mathematics or by independent libraries.  No function here is
 "parity unpinned".
 """
 
-from . import formats, activations, gemm, fastdivmod, tiles, lowp  # noqa: F401
+from . import formats, activations, gemm, fastdivmod, tiles, lowp, b128  # noqa: F401
