@@ -839,40 +839,53 @@ def b128_empty(rows, cols, block_rows=1, dtype=torch.float8_e4m3fn, device=None,
     return B128Tensor(codes[..., :cols], scales.transpose(-1, -2), block_rows)
 
 
+def _b128(Q, device):
+    """The C struct of a B128Tensor that has to be on a device."""
+    if Q.__class__ is not B128Tensor:
+        raise TypeError("expected a B128Tensor")
+    if Q._device != device:
+        raise ValueError("B128Tensor: tensors on different devices")
+    return Q._c
+
+
 def _either(t, device):
-    """A tensor as it is, a B128Tensor (which has to be on the device) as its C struct."""
-    return _on(t, device) if t.__class__ is B128Tensor else t
+    """A tensor as it is, a B128Tensor as its C struct."""
+    return _b128(t, device) if t.__class__ is B128Tensor else t
 
 
 def gge_b128_quantize(X, Q, values=None):
     """Q (a B128Tensor) = X quantised; X (rows, cols) or (batch, rows, cols), row-major or a
     transposed view.  values: optional output, the numbers that the codes stand for."""
-    code = (_marshal or _load_marshal()).b128_quantize(X, _on(Q, X.device), values)
+    code = (_marshal or _load_marshal()).b128_quantize(X, _b128(Q, X.device), values)
     if code:
         raise GgeError(code, "gge_b128_quantize")
 
 
 def gge_b128_transpose(X, Q, values=None):
     """Q = the transpose of B128Tensor X's numbers, quantised anew along its own rows."""
+    if X.__class__ is not B128Tensor:
+        raise TypeError("expected a B128Tensor")
     dev = X._device
-    code = (_marshal or _load_marshal()).b128_transpose(X._c, _on(Q, dev), values, dev.index)
+    code = (_marshal or _load_marshal()).b128_transpose(X._c, _b128(Q, dev), values, dev.index)
     if code:
         raise GgeError(code, "gge_b128_transpose")
 
 
 def gge_b128_dequantize(Q, Y):
     """Y (bf16, f16 or f32) = the numbers that Q's codes stand for."""
-    code = (_marshal or _load_marshal()).b128_dequantize(_on(Q, Y.device), Y)
+    code = (_marshal or _load_marshal()).b128_dequantize(_b128(Q, Y.device), Y)
     if code:
         raise GgeError(code, "gge_b128_dequantize")
 
 
 def _gemm_b128(name, A, B, D, C, PostAct, act, alpha, beta, alpha_dev, beta_dev, config, workspace,
                dact, cu):
+    if A.__class__ is not B128Tensor:
+        raise TypeError("expected a B128Tensor")
     dev = A._device
     ws = _shared(dev, 256) if workspace is None else _ws(dev, 256, workspace)
     code = (_marshal or _load_marshal()).gemm_b128(
-        A._c, _on(B, dev), dev.index, _either(D, dev), _either(C, dev), _either(PostAct, dev),
+        A._c, _b128(B, dev), dev.index, _either(D, dev), _either(C, dev), _either(PostAct, dev),
         ACT[act], alpha, beta, alpha_dev, beta_dev,
         ctypes.addressof(config) if config is not None else 0, ws, dact, cu)
     if code:
@@ -912,8 +925,8 @@ def gge_layernorm(X, weight=None, bias=None, Y=None, residual=None, residual_out
     quantised, for the backward.  X (rows, cols); every output is optional."""
     dev = X.device
     code = (_marshal or _load_marshal()).layernorm(
-        X, weight, bias, Y, residual, residual_out, _on(Q, dev) if Q is not None else None, values,
-        _on(H8, dev) if H8 is not None else None, mean, rstd, eps)
+        X, weight, bias, Y, residual, residual_out, _b128(Q, dev) if Q is not None else None, values,
+        _b128(H8, dev) if H8 is not None else None, mean, rstd, eps)
     if code:
         raise GgeError(code, "gge_layernorm")
 

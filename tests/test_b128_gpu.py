@@ -244,7 +244,9 @@ def _product(m, n, k, b_rows=128, a_rows=1, act="none", c=None, d=torch.bfloat16
         else:
             got, fmt = dec(out).reshape(want.shape), FMT[t]
             r = formats.round_to(want, fmt)
-            worst = np.max(np.abs(got - r) / (tol + formats.quantum(r, fmt)))
+            fin = np.isfinite(r)     # (past its type's range an output is an infinity in both)
+            assert np.array_equal(got[~fin], r[~fin])
+            worst = np.max(np.abs(got[fin] - r[fin]) / (tol[fin] + formats.quantum(r[fin], fmt)))
             assert worst <= 1.0, (name, worst)
     return D, P
 
@@ -491,7 +493,9 @@ def test_wait_timeout_reported_and_context_survives(tile_n, splits):
     gge.gge_gemm_b128(A, B, D=D, config=cfg)
     torch.cuda.synchronize()
     status, where, _ = gge.gge_read_device_status()
-    assert status == "GGE_ERR_TIMEOUT" and where == 3
+    # (a block's sum that is never handed on stops every role: whichever waits first says so --
+    # loads 0, MMAs 1 and 2, sums 3, scales 10)
+    assert status == "GGE_ERR_TIMEOUT" and where in (0, 1, 2, 3, 10)
     assert gge.gge_read_device_status()[0] == "GGE_OK"
     _product(40, 256, 4096, config=gge.make_config(tile_n=tile_n))
 
