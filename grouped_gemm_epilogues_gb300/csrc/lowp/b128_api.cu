@@ -77,19 +77,19 @@ struct GemmPlan {
   b128::GemmParams gp;
   CUtensorMap a, b;
   LaunchShape shape;
-  int bn;
+  int tile;
   bool empty;
 };
 
-int shape_units(int bn, bool bv, size_t smem, int cluster) {
-  return bn == 256   ? b128::units_tile<256, 2>(bv, smem, cluster)
-         : bn == 128 ? b128::units_tile<128, 1>(bv, smem, cluster)
-                     : b128::units_tile<64, 1>(bv, smem, cluster);
+int shape_units(int tile, bool bv, size_t smem, int cluster) {
+  return tile == 256   ? b128::units_tile<256, 2>(bv, smem, cluster)
+         : tile == 128 ? b128::units_tile<128, 1>(bv, smem, cluster)
+                       : b128::units_tile<64, 1>(bv, smem, cluster);
 }
 
 // Resident CTAs (cluster 1) or clusters, cached.
-int tile_units(int bn, bool bv, size_t smem, int cluster) {
-  struct Entry { int dev, bn, cluster; bool bv; size_t smem; int units; };
+int tile_units(int tile, bool bv, size_t smem, int cluster) {
+  struct Entry { int dev, tile, cluster; bool bv; size_t smem; int units; };
   static std::mutex mu;
   static Entry cache[256];
   static int n = 0;
@@ -98,18 +98,18 @@ int tile_units(int bn, bool bv, size_t smem, int cluster) {
   {
     std::lock_guard<std::mutex> g(mu);
     for (int i = 0; i < n; ++i)
-      if (cache[i].dev == dev && cache[i].bn == bn && cache[i].bv == bv && cache[i].cluster == cluster &&
+      if (cache[i].dev == dev && cache[i].tile == tile && cache[i].bv == bv && cache[i].cluster == cluster &&
           cache[i].smem == smem)
         return cache[i].units;
   }
   int units;
   {
     RelaxedCaptureMode relaxed;  // the first query may run inside a stream capture
-    units = shape_units(bn, bv, smem, cluster);
+    units = shape_units(tile, bv, smem, cluster);
   }
   if (units > 0) {
     std::lock_guard<std::mutex> g(mu);
-    if (n < 256) cache[n++] = Entry{dev, bn, cluster, bv, smem, units};
+    if (n < 256) cache[n++] = Entry{dev, tile, cluster, bv, smem, units};
   }
   return units;
 }
@@ -117,9 +117,10 @@ int tile_units(int bn, bool bv, size_t smem, int cluster) {
 constexpr int kFlagsTaken = FLAG_TEST_DROP_ACC_FULL | FLAG_NO_SPLIT | FLAG_RASTER_N;
 constexpr int kMaxGroupsHost = 1024;
 
-// One way to run a product: tile shape, CTAs that share a tile's K, shared memory.
+// One way to run a product: tile shape (256 x 256 on a CTA pair, 128 x 128 or 128 x 64 on one
+// CTA), CTAs that share a tile's K, shared memory.
 struct Shape {
-  int bn, cg, splits, stages, stage_bytes, reduce_bytes, units;
+  int bn, cg, splits, stages, stage_bytes, units;
   size_t smem;
   int64_t tiles_m, tiles_n, tiles;  // (grouped rows: tiles_m and tiles as expected)
 };
@@ -140,10 +141,9 @@ bool try_shape(const Problem& q, int bn, int splits, Shape* s) {
   s->tiles = s->tiles_m * s->tiles_n * (q.groups > 0 ? 1 : q.L);
   if (splits > 1 && (s->cg == 2 || splits > q.k_tiles || s->tiles * splits > q.sms)) return false;
   s->stage_bytes = 128 * 128 + bn / s->cg * 128;
-  // the pieces (32 rows x half a tile's columns, fp32) that the other CTAs hand over
-  s->reduce_bytes = splits > 1 ? (splits - 1) * (8 / splits) * (bn / 2) * 128 : 0;
-  const int ring = 8 * (128 + (q.bv ? bn : 4)) * 4;
-  const int fixed = 1024 + 512 + 2048 + ring + 8 * q.out_stage + s->reduce_bytes +
+  const int ring = 2 * 8 * (128 + (q.bv ? std::max(bn, 128) : 4)) * 4;  // (kScaleSlots, kSlotBytes)
+  const int outputs = bn == 256 ? 8 * q.out_stage : 128 * bn * 4 + 4 * q.out_stage;  // (a tile's sums, staging)
+  const int fixed = 1024 + 512 + outputs + ring +
                     (q.groups > 0 ? 2 * (kMaxGroupsHost + 1) * 4 : 0);
   s->stages = std::min(q.max_stages, (kMaxSmemOptin - fixed) / s->stage_bytes);
   if (s->stages < 2) return false;
@@ -155,8 +155,8 @@ bool try_shape(const Problem& q, int bn, int splits, Shape* s) {
 
 // Estimated time (ns) of a shape: rounds of tiles, each its blocks of K and an epilogue.
 double cost(const Shape& s, int64_t k_tiles) {
-  const double per_k = s.bn == 64 ? 230.0 : (s.bn == 128 ? 270.0 : 320.0);
-  const double tail = s.bn == 64 ? 600.0 : (s.bn == 128 ? 1000.0 : 1500.0);
+  const double per_k = s.bn == 64 ? 200.0 : (s.bn == 128 ? 270.0 : 330.0);
+  const double tail = s.bn == 64 ? 600.0 : 1000.0;
   const int64_t rounds = s.splits > 1 ? 1 : ceil_div(s.tiles, s.units);
   const double exchange = s.splits == 1 ? 0.0 : 2500.0;
   return static_cast<double>(rounds) * (static_cast<double>(ceil_div(k_tiles, s.splits)) * per_k + tail) + exchange;
@@ -229,12 +229,12 @@ gge_status plan_b128(const gge_gemm_b128_args* a, bool dact, void* ws, size_t ws
   if (q.sms <= 0) return GGE_ERR_CUDA;
   Shape sh{};
   double best = -1.0;
-  for (int bn : {256, 128, 64}) {
-    if ((want != 0 && bn != want) || (bn == 64 && q.codes_out)) continue;
-    for (int splits = 1; splits <= (q.codes_out ? 4 : 8); splits *= 2) {
+  for (int tile : {256, 128, 64}) {
+    if ((want != 0 && tile != want) || (tile == 64 && q.codes_out)) continue;
+    for (int splits = 1; splits <= 4; splits *= 2) {
       if (splits > 1 && (G > 0 || (cfg && ((cfg->flags & FLAG_NO_SPLIT) || cfg->num_ctas > 0)))) break;
       Shape one;
-      if (!try_shape(q, bn, splits, &one)) {
+      if (!try_shape(q, tile, splits, &one)) {
         if (splits == 1) break;
         continue;
       }
@@ -248,11 +248,10 @@ gge_status plan_b128(const gge_gemm_b128_args* a, bool dact, void* ws, size_t ws
   if (best < 0.0) return GGE_ERR_CUDA;  // (every shape fits; the device could not be asked)
   const int tile_m = 128 * sh.cg;
   if (sh.tiles > kMaxExtent / 8) return GGE_ERR_UNSUPPORTED;
-  pl.bn = sh.bn;
+  pl.tile = sh.bn;
   pl.shape.smem = sh.smem;
   pl.shape.cluster = sh.cg * sh.splits;
   pl.gp.splits = sh.splits;
-  pl.gp.reduce_bytes = sh.reduce_bytes;
   pl.gp.b_rows_one = q.bv ? 1 : 0;
   pl.gp.a = view_of(a->A);
   pl.gp.b = view_of(a->B);
@@ -328,9 +327,9 @@ gge_status run_b128(const gge_gemm_b128_args* args, bool dact, void* ws, size_t 
   const gge_status s = plan_b128(args, dact, ws, ws_bytes, &pl);
   if (s != GGE_OK || pl.empty) return s;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  return launched(pl.bn == 256   ? b128::launch_tile<256, 2>(pl.a, pl.b, pl.gp, pl.shape, st)
-                  : pl.bn == 128 ? b128::launch_tile<128, 1>(pl.a, pl.b, pl.gp, pl.shape, st)
-                                 : b128::launch_tile<64, 1>(pl.a, pl.b, pl.gp, pl.shape, st));
+  return launched(pl.tile == 256   ? b128::launch_tile<256, 2>(pl.a, pl.b, pl.gp, pl.shape, st)
+                  : pl.tile == 128 ? b128::launch_tile<128, 1>(pl.a, pl.b, pl.gp, pl.shape, st)
+                                   : b128::launch_tile<64, 1>(pl.a, pl.b, pl.gp, pl.shape, st));
 }
 
 // ------------------------------------------------------------ layer norm
