@@ -126,6 +126,12 @@ int device_of(PyObject* o, const char* kind) {
   Py_END_ALLOW_THREADS;                                                                  \
   return PyLong_FromLong(code)
 
+// A workspace's size, with the tensors' device current.
+size_t size_on(int64_t dev, size_t (*size_of)(int64_t), int64_t cols) {
+  const c10::cuda::CUDAGuard on(static_cast<c10::DeviceIndex>(dev));
+  return size_of(cols);
+}
+
 // mx_alloc(bytes, start, device, format, rows, cols, batch or 0, row bytes, scale bytes a batch,
 // tensor_scale) -> (buffer, struct bytes): codes at the buffer's start, scales at `start`
 PyObject* mx_alloc(PyObject*, PyObject* const* a, Py_ssize_t n) {
@@ -596,8 +602,7 @@ PyObject* layernorm_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
     wp = ws->data_ptr();
     wn = static_cast<size_t>(ws->numel());
   } else if (dw != nullptr || db != nullptr) {
-    const c10::cuda::CUDAGuard on(static_cast<c10::DeviceIndex>(dev));
-    wn = gge_workspace_size_layernorm_bwd(g.dy.cols);
+    wn = size_on(dev, gge_workspace_size_layernorm_bwd, g.dy.cols);
     own = at::empty({static_cast<int64_t>(wn)},
                     at::TensorOptions().dtype(at::kByte).device(at::kCUDA, static_cast<c10::DeviceIndex>(dev)));
     wp = own.data_ptr();
