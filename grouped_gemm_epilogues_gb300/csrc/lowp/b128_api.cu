@@ -120,7 +120,7 @@ constexpr int kMaxGroupsHost = 1024;
 // One way to run a product: tile shape (256 x 256 on a CTA pair, 128 x 128 or 128 x 64 on one
 // CTA), CTAs that share a tile's K, shared memory.
 struct Shape {
-  int bn, cg, splits, stages, stage_bytes, units;
+  int a_rows, bn, cg, splits, stages, stage_bytes, units;
   size_t smem;
   int64_t tiles_m, tiles_n, tiles;  // (grouped rows: tiles_m and tiles as expected)
 };
@@ -140,7 +140,8 @@ bool try_shape(const Problem& q, int bn, int splits, Shape* s) {
   s->tiles_n = ceil_div(q.N, bn);
   s->tiles = s->tiles_m * s->tiles_n * (q.groups > 0 ? 1 : q.L);
   if (splits > 1 && (s->cg == 2 || splits > q.k_tiles || s->tiles * splits > q.sms)) return false;
-  s->stage_bytes = 128 * 128 + bn / s->cg * 128;
+  s->a_rows = bn < 256 && q.groups == 0 && q.M <= 32 ? 32 : 128;
+  s->stage_bytes = (s->a_rows + bn / s->cg) * 128;
   const int ring = 2 * 8 * (128 + (q.bv ? std::max(bn, 128) : 4)) * 4;  // (kScaleSlots, kSlotBytes)
   const int outputs = bn == 256 ? 8 * q.out_stage : 128 * bn * 4 + 4 * q.out_stage;  // (a tile's sums, staging)
   const int fixed = 1024 + 512 + outputs + ring +
@@ -153,13 +154,19 @@ bool try_shape(const Problem& q, int bn, int splits, Shape* s) {
   return splits == 1 || s->tiles <= s->units;
 }
 
-// Estimated time (ns) of a shape: rounds of tiles, each its blocks of K and an epilogue.
-double cost(const Shape& s, int64_t k_tiles) {
-  const double per_k = s.bn == 64 ? 200.0 : (s.bn == 128 ? 270.0 : 330.0);
-  const double tail = s.bn == 64 ? 600.0 : 1000.0;
+// Estimated time (ns) of a shape, from measured products: a block of K costs 400, 345 or 245 with
+// tiles 256, 128 or 64 wide, more with a scale for each row of B; a 256-wide tile's outputs are
+// made between its K and the next one's, small tiles' beside it; ranks that split K exchange sums.
+// (Two rounds of 256 x 256 tiles, 4096 x 1536 x 16384 with a scale for each row: 193 us; three
+// rounds of 128 x 128: 175.)
+double cost(const Shape& s, const Problem& q) {
+  const double per_k = s.bn == 64 ? (q.bv ? 295.0 : 245.0)
+                       : s.bn == 128 ? (q.bv ? 440.0 : s.a_rows < 128 ? 240.0 : 345.0)
+                                     : (q.bv ? 700.0 : 400.0);
   const int64_t rounds = s.splits > 1 ? 1 : ceil_div(s.tiles, s.units);
+  const double outputs = s.bn == 256 ? 2000.0 * static_cast<double>(rounds) : 1500.0;
   const double exchange = s.splits == 1 ? 0.0 : 2500.0;
-  return static_cast<double>(rounds) * (static_cast<double>(ceil_div(k_tiles, s.splits)) * per_k + tail) + exchange;
+  return static_cast<double>(rounds) * static_cast<double>(ceil_div(q.k_tiles, s.splits)) * per_k + outputs + exchange;
 }
 
 // One of C, D and PostAct in either form.
@@ -223,7 +230,7 @@ gge_status plan_b128(const gge_gemm_b128_args* a, bool dact, void* ws, size_t ws
   q.out_stage = out_es == 4 || q.codes_out ? 4096 : 2048;
   const int want = cfg ? cfg->tile_n : 0;
   if (want != 0 && want != 256 && want != 128 && (want != 64 || q.codes_out)) return GGE_ERR_UNSUPPORTED;
-  q.max_stages = cfg && cfg->stages > 0 ? std::min(8, static_cast<int>(cfg->stages)) : 8;
+  q.max_stages = cfg && cfg->stages > 0 ? std::min(8, static_cast<int>(cfg->stages)) : 16;
   if (q.max_stages < 2) return GGE_ERR_UNSUPPORTED;
   q.sms = sm_count();
   if (q.sms <= 0) return GGE_ERR_CUDA;
@@ -238,7 +245,7 @@ gge_status plan_b128(const gge_gemm_b128_args* a, bool dact, void* ws, size_t ws
         if (splits == 1) break;
         continue;
       }
-      const double c = cost(one, q.k_tiles);
+      const double c = cost(one, q);
       if (best < 0.0 || c < best) {
         best = c;
         sh = one;
@@ -252,6 +259,7 @@ gge_status plan_b128(const gge_gemm_b128_args* a, bool dact, void* ws, size_t ws
   pl.shape.smem = sh.smem;
   pl.shape.cluster = sh.cg * sh.splits;
   pl.gp.splits = sh.splits;
+  pl.gp.a_rows = sh.a_rows;
   pl.gp.b_rows_one = q.bv ? 1 : 0;
   pl.gp.a = view_of(a->A);
   pl.gp.b = view_of(a->B);
@@ -317,7 +325,7 @@ gge_status plan_b128(const gge_gemm_b128_args* a, bool dact, void* ws, size_t ws
     return encode_3d(m, t.codes, 1, static_cast<uint64_t>(K), static_cast<uint64_t>(t.rows),
                      static_cast<uint64_t>(t.batch), ld, sb, 128, box_rows);
   };
-  s = map(&pl.a, a->A, 128);
+  s = map(&pl.a, a->A, static_cast<uint32_t>(sh.a_rows));
   if (s == GGE_OK) s = map(&pl.b, a->B, static_cast<uint32_t>(sh.bn / sh.cg));
   return s;
 }

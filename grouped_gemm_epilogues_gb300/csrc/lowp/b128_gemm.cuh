@@ -37,8 +37,13 @@
 namespace gge {
 namespace b128 {
 
-constexpr int kMaxStages = 8;
+constexpr int kMaxStages = 16;
 constexpr int kScaleSlots = 2;   // of the scale ring,
+// A stage is a block's rows of A and of B.  Up to 32 rows of A in all (decoding) take no more room
+// than that in small tiles, so that more of B is on its way: the MMA reads 128 rows from there all
+// the same, and what it makes of others' bytes is not read.
+constexpr int kFewRows = 32;
+
 template <int BN, int CG, bool BV>
 struct GemmCfg {
   static constexpr bool kWide = BN == 256;             // the warps that hold sums finish the tile
@@ -46,7 +51,8 @@ struct GemmCfg {
   static constexpr int kBRows = BN / CG;
   static constexpr int kABytes = kBM * kRowBytes;
   static constexpr int kBBytes = kBRows * kRowBytes;
-  static constexpr int kStageBytes = kABytes + kBBytes;
+  __device__ static __forceinline__ uint32_t a_bytes(const GemmParams& gp) { return kWide ? kABytes : gp.a_rows * kRowBytes; }
+  __device__ static __forceinline__ uint32_t stage_bytes(const GemmParams& gp) { return a_bytes(gp) + kBBytes; }
   static constexpr int kBuffers = kWide ? 2 : 4;       // blocks' sums in tensor memory
   static constexpr int kTmemCols = kBuffers * BN;
   static constexpr int kScaleFloats = kBM + (BV ? (kWide ? 256 : 128) : 4);  // of a block
@@ -234,7 +240,7 @@ __device__ __forceinline__ void mma_role(const GemmParams& gp, const Shared& sh,
   Probed there{false, false};
   const int32_t hand_on = p.flags & FLAG_TEST_DROP_ACC_FULL ? 0 : 1;
   // (addresses in a descriptor are in 16 bytes; K advances by 32 bytes an MMA inside the swizzle)
-  const uint64_t adesc = smem_desc(stage0, 16u, 1024u), bdesc = smem_desc(stage0 + Cfg::kABytes, 16u, 1024u);
+  const uint64_t adesc = smem_desc(stage0, 16u, 1024u), bdesc = smem_desc(stage0 + Cfg::a_bytes(gp), 16u, 1024u);
   for (int32_t t = unit; t < num_tiles; t += units) {
     for (int32_t kt = ks.k0; kt < ks.k1; ++kt) {
       const uint32_t empty = sh.empty + 8 * stage, tfull = sh.tfull + 8 * buf;
@@ -243,7 +249,7 @@ __device__ __forceinline__ void mma_role(const GemmParams& gp, const Shared& sh,
         if (!wait_on(sh.tempty + 8 * buf, buf_phase, p, sh, 2, t)) return;
       }
       ptx::tc_fence_after();
-      const uint32_t step = static_cast<uint32_t>(stage) * (Cfg::kStageBytes / 16);
+      const uint32_t step = static_cast<uint32_t>(stage) * (Cfg::stage_bytes(gp) / 16);
       const uint32_t d = tmem_base + buf * BN;
       if (++stage == p.stages) { stage = 0; phase ^= 1u; }
       if (++buf == Cfg::kBuffers) { buf = 0; buf_phase ^= 1u; }
@@ -269,16 +275,16 @@ __device__ __forceinline__ void load_role(const GemmParams& gp, const Shared& sh
     for (int32_t kt = ks.k0; kt < ks.k1; ++kt) {
       if (!wait_on(sh.empty + 8 * stage, phase ^ 1u, p, sh, 0, t)) return;
       const uint32_t full = sh.full + 8 * stage;
-      if (CG == 1) ptx::mbar_arrive_expect_tx(full, Cfg::kStageBytes);
-      else if (rank == 0) ptx::mbar_arrive_expect_tx(full, 2 * Cfg::kStageBytes);
+      if (CG == 1) ptx::mbar_arrive_expect_tx(full, Cfg::stage_bytes(gp));
+      else if (rank == 0) ptx::mbar_arrive_expect_tx(full, 2 * Cfg::stage_bytes(gp));
       const uint32_t bar = (CG == 1) ? full : ptx::mapa(full, 0);
-      const uint32_t dst = stage0 + stage * Cfg::kStageBytes;
+      const uint32_t dst = stage0 + stage * Cfg::stage_bytes(gp);
       if (CG == 1) {
         ptx::tma_load_3d(dst, tmA, bar, kt * kBlock, row0, tc.a_batch);
-        ptx::tma_load_3d(dst + Cfg::kABytes, tmB, bar, kt * kBlock, bn0, tc.b_batch);
+        ptx::tma_load_3d(dst + Cfg::a_bytes(gp), tmB, bar, kt * kBlock, bn0, tc.b_batch);
       } else {
         ptx::tma_load_3d_pair(dst, tmA, bar, kt * kBlock, row0, tc.a_batch);
-        ptx::tma_load_3d_pair(dst + Cfg::kABytes, tmB, bar, kt * kBlock, bn0, tc.b_batch);
+        ptx::tma_load_3d_pair(dst + Cfg::a_bytes(gp), tmB, bar, kt * kBlock, bn0, tc.b_batch);
       }
       if (++stage == p.stages) { stage = 0; phase ^= 1u; }
     }
@@ -649,11 +655,11 @@ __device__ __forceinline__ float most32(float top, const float (&v)[32], int32_t
 }
 
 // D and PostAct of a warp's 32 rows from the sums in shared memory, where the numbers of an 8-bit
-// output wait for their scale.  `mine`: the tile's chunks of 32 columns that are this CTA's (a
-// cluster that splits K shares them out).  Warp-collective.
+// output wait for their scale.  The tile's chunks of 32 columns first,
+// first + step, ... below `last` are this warp's.  Warp-collective.
 template <int BN>
 __device__ __forceinline__ void finish(const GemmParams& gp, const Spot& at, uint32_t sums, uint32_t stg, int32_t splits,
-                                       int first, int last) {
+                                       int first, int last, int step) {
   const Params& p = gp.p;
   const int lane = threadIdx.x & 31, tile_row = threadIdx.x & 127;
   const float alpha = p.dact ? 1.f : (p.alpha_dev ? *p.alpha_dev : p.alpha);
@@ -671,14 +677,14 @@ __device__ __forceinline__ void finish(const GemmParams& gp, const Spot& at, uin
     const bool c_here = reads_c && (pass == 0 || p.dact) && there;
     if (c_here && at.col_base + 32 * first < p.N) fetch_c(gp, row, at.col_base + 32 * first, at.batch, c_raw);
 #pragma unroll 1
-    for (int c = first; c < last; ++c) {
+    for (int c = first; c < last; c += step) {
       const int32_t col0 = at.col_base + 32 * c, left = p.N - col0;
       if (left <= 0) break;
       float v[32];
       if (splits > 1 && pass == 0) join32<BN>(sums, tile_row, c, splits, v);
       else load32<BN>(sums, tile_row, c, v);
       const CRegs now = c_raw;
-      if (c_here && c + 1 < last && left > 32) fetch_c(gp, row, col0 + 32, at.batch, c_raw);
+      if (c_here && c + step < last && left > 32 * step) fetch_c(gp, row, col0 + 32 * step, at.batch, c_raw);
       const float unit = c_here && gp.c8.codes != nullptr ? *gp.c8.scale(row, col0 >> 7, at.batch) : 0.f;
       const char* crow = c_here && gp.c8.codes == nullptr && p.c_dtype == DT_F32
                              ? reinterpret_cast<const char*>(static_cast<const float*>(p.c) + at.batch * p.sbc +
@@ -926,7 +932,7 @@ __device__ __forceinline__ Memory memory(const GemmParams& gp) {
   const uint32_t base = (raw + 1023u) & ~1023u;
   Memory m = {};
   m.stages = base;
-  m.sums = base + gp.p.stages * Cfg::kStageBytes;
+  m.sums = base + gp.p.stages * Cfg::stage_bytes(gp);
   m.out_stage = m.sums + Cfg::kSumsBytes;
   // (right behind the scale ring)
   m.ctrl = m.out_stage + Cfg::kStagingWarps * gp.p.out_stage_bytes + kScaleSlots * Cfg::kSlotBytes;
@@ -1014,8 +1020,10 @@ __device__ __forceinline__ void hold_role(const GemmParams& gp) {
 }
 
 // The warps that turn a tile's sums into outputs.
+// `who`: 0 for those that do nothing else; 1 and 2 for the holding warpgroups, which join them for
+// the CTA's last tile (every third chunk each; staging where the stages were).
 template <int BN, int CG, bool BV>
-__device__ __forceinline__ void finish_role(const GemmParams& gp) {
+__device__ __forceinline__ void finish_role(const GemmParams& gp, int who) {
   using Cfg = GemmCfg<BN, CG, BV>;
   const Params& p = gp.p;
   const Memory m = memory<BN, CG, BV>(gp);
@@ -1023,30 +1031,41 @@ __device__ __forceinline__ void finish_role(const GemmParams& gp) {
   const int quad = (threadIdx.x >> 5) & 3;
   const int32_t num_tiles = tiles_of(gp, m);
   const int32_t splits = CG == 1 ? gp.splits : 1;
+  const bool codes = gp.d8.codes != nullptr || gp.p8.codes != nullptr;
+  const bool shared = !codes && 8 * p.out_stage_bytes <= p.stages * static_cast<int>(Cfg::stage_bytes(gp));
+  const uint32_t stg =
+      who == 0 ? m.out_stage + quad * p.out_stage_bytes : m.stages + (4 * who - 4 + quad) * p.out_stage_bytes;
   uint32_t phase = 0u;
+  int32_t t = me.unit;
+  if (splits > 1) {  // (one tile a cluster)
+    cluster_arrive();
+    cluster_wait();  // every rank's sums are in its shared memory
+    if (*m.abort_flag) return;
+  }
+  if (who > 0) {
+    if (!shared || t >= num_tiles) return;
+    const int32_t before = (num_tiles - 1 - t) / me.units;  // this CTA's other tiles
+    t += before * me.units;
+    phase = static_cast<uint32_t>(before) & 1u;
+  }
 #pragma unroll 1
-  for (int32_t t = me.unit; t < num_tiles; t += me.units) {
+  for (; t < num_tiles; t += me.units) {
     const Spot spot = spot_of<BN, CG, BV>(p, m, me, t, quad);
     int first = 0, last = BN / 32;
     if (splits == 1) {
       if (!wait_warp(m.ctrl, m.ctrl + kTileBar, phase, p, 13, t)) return;
       phase ^= 1u;
-    } else {  // (one tile a cluster)
-      cluster_arrive();
-      cluster_wait();  // every rank's sums are in its shared memory
-      if (*m.abort_flag) return;
-      // a share of the columns, or, where a row's block has to stay together, of the rows
-      if (gp.d8.codes == nullptr && gp.p8.codes == nullptr) {
-        first = static_cast<int>(me.slice) * (BN / 32) / splits;
-        last = static_cast<int>(me.slice + 1) * (BN / 32) / splits;
-      } else if (static_cast<uint32_t>(quad * splits) / 4 != me.slice) {
-        return;
-      }
+    } else if (!codes) {  // a share of the columns, or, where a row's block has to stay together, of the rows
+      first = static_cast<int>(me.slice) * (BN / 32) / splits;
+      last = static_cast<int>(me.slice + 1) * (BN / 32) / splits;
+    } else if (static_cast<uint32_t>(quad * splits) / 4 != me.slice) {
+      return;
     }
+    const bool three = shared && t + me.units >= num_tiles;
     if (spot.rows_valid > 0)
-      finish<BN>(gp, spot, m.sums, m.out_stage + quad * p.out_stage_bytes, splits, first, last);
+      finish<BN>(gp, spot, m.sums, stg, splits, three ? first + who : first, last, three ? 3 : 1);
     __syncwarp();
-    arrive_one(m.ctrl + kFreeBar);
+    if (who == 0) arrive_one(m.ctrl + kFreeBar);
   }
 }
 
@@ -1133,14 +1152,15 @@ __global__ void __launch_bounds__(GemmCfg<BN, CG, BV>::kThreads, 1)
   __syncthreads();
   if (CG == 2) ptx::cluster_sync();
   ptx::tc_fence_after();
-  if (!Cfg::kWide && warp >= Cfg::kFirstFinish) {
-    if constexpr (!Cfg::kWide) {
-      asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Cfg::kFinishRegs));
-      finish_role<BN, CG, BV>(gp);
-    }
-  } else if (warp >= Cfg::kFirstHold) {
+  if (warp >= Cfg::kFirstHold) {
+    static_assert(Cfg::kWide || Cfg::kHoldRegs == Cfg::kFinishRegs, "one share for both");
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Cfg::kHoldRegs));
-    hold_role<BN, CG, BV>(gp);
+    if constexpr (Cfg::kWide) {
+      hold_role<BN, CG, BV>(gp);
+    } else {
+      if (warp < Cfg::kFirstFinish) hold_role<BN, CG, BV>(gp);
+      finish_role<BN, CG, BV>(gp, warp < Cfg::kFirstFinish ? (warp - Cfg::kFirstHold) / 4 + 1 : 0);
+    }
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Cfg::kIssueRegs));
     const Memory m = memory<BN, CG, BV>(gp);
@@ -1161,8 +1181,8 @@ __global__ void __launch_bounds__(GemmCfg<BN, CG, BV>::kThreads, 1)
   // (worked out again: nothing is kept in registers over the main loop)
   const int last_warp = thread_now() >> 5;
   if (CG == 1 && gp.splits > 1) {
-    // (the finishing warps have waited for the sums of all ranks)
-    if (last_warp < Cfg::kFirstFinish) {
+    // (the others have waited for the sums of all ranks)
+    if (last_warp < Cfg::kFirstHold) {
       cluster_arrive();
       cluster_wait();
     }
