@@ -216,9 +216,16 @@ gge_status plan_b128(const gge_gemm_b128_args* a, bool dact, void* ws, size_t ws
   if ((s = check_out(a->D, a->D8, M, N, L, true)) != GGE_OK) return s;
   if ((s = check_out(a->PostAct, a->PostAct8, M, N, L, true)) != GGE_OK) return s;
   if (N % 8 != 0) return GGE_ERR_UNSUPPORTED;
+  pl.empty = M == 0 || N == 0;
+  if (dact && !pl.empty) {  // C is read again after D is written
+    const void* c = a->C ? a->C->ptr : a->C8->codes;
+    for (const gge_tensor* t : {a->D, a->PostAct})
+      if (t != nullptr && t->ptr == c) return GGE_ERR_INVALID_ARG;
+    for (const gge_b128_tensor* t : {a->D8, a->PostAct8})
+      if (t != nullptr && t->codes == c) return GGE_ERR_INVALID_ARG;
+  }
   s = check_workspace(ws, ws_bytes);
   if (s != GGE_OK) return s;
-  pl.empty = M == 0 || N == 0;
   if (pl.empty) return GGE_OK;
 
   const int out_es = std::max(a->D ? elem_bytes(a->D->dtype) : 0, a->PostAct ? elem_bytes(a->PostAct->dtype) : 0);

@@ -523,8 +523,9 @@ gge_status gge_b128_dequantize(const gge_b128_tensor* q, const gge_tensor* y, gg
  *   config (may be NULL): tile_n 0 (automatic), 256 (a CTA pair, 256 x 256), 128 or 64
  *   (one CTA, 128 rows; 64 not with 8-bit outputs); num_ctas, raster_band, stages, timeout_ns;
  *   of the flags those for no split, raster along N and the test hook.
- * Few tiles are split along K over a cluster of 2, 4 or 8 CTAs, which add their sums in a
- * fixed order through shared memory (not grouped rows).  The workspace holds the status
+ * Few tiles are split along K over a cluster of 2 or 4 CTAs, which add their sums in a
+ * fixed order through shared memory (not grouped rows).  D may be C itself (a gradient
+ * added to in place).  The workspace holds the status
  * words (at least 256 bytes; NULL: device errors go unrecorded).
  */
 typedef struct gge_gemm_b128_args {
@@ -551,6 +552,7 @@ gge_status gge_gemm_b128(const gge_gemm_b128_args* args, void* workspace, size_t
 /* The backward activation epilogue (as gge_gemm_dact): with S the incoming gradient and
  * C or C8 (one of them required) the pre-activation x, D = act'(x) * S (required, in either
  * form) and PostAct = act(x) (optional); act is not NONE, alpha and beta are not used.
+ * Neither output may be C or C8, which is read again after D is written: INVALID_ARG.
  * Grouped rows as above. */
 gge_status gge_gemm_b128_dact(const gge_gemm_b128_args* args, void* workspace,
                               size_t workspace_bytes, gge_stream_t stream);
