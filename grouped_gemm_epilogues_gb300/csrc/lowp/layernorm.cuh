@@ -5,10 +5,12 @@
 //
 // y leaves in 16 or 32 bits, or as codes with a scale for each 128 columns; h, too, can leave
 // in 8 bits, and the backward read it so.  The variance is that of differences from a mean: a
-// warp's sums are joined by mean and squared deviation,
-//   M2 = sum over warps of M2_w + n_w (mean_w - mean)^2,
-// with the warps' means taken relative to the first one's, so that no sum of squares is large
-// against the variance, whatever the mean.
+// thread's sums, of its own values, are joined to a warp's and those to the row's by mean and
+// squared deviation,
+//   M2 = sum over parts of M2_p + n_p (mean_p - mean)^2,
+// with the parts' means taken relative to the first one's, so that no sum of squares is large
+// against the variance, whatever the mean.  (One reduction over the warp for both sums; a warp's
+// mean first and then its deviations: 16384 x 8192 to codes and values 281 us, so 228.)
 //
 // Backward, n = (h - mean) rstd, g = dy w, for dh the gradient that reaches h directly:
 //   dx = rstd (g - mean(g) - n mean(g n)) + dh    dw = sum over rows of dy n    db = of dy
@@ -41,6 +43,16 @@ __device__ __forceinline__ void load_param(const void* w, int32_t dtype, int32_t
   }
 }
 
+// Both parameters where all eight values of both are there and aligned: one choice of the type.
+// (Outputs in codes, which are bound by instructions: 16384 x 8192 228 -> 212 us.  Outputs in 16 bits
+// are not, and lose the registers: 170 -> 212.)
+template <typename W>
+__device__ __forceinline__ void both_params(const void* w, const void* b, int32_t col, float2 (&v)[4], float2 (&u)[4]) {
+  const Raw8<W> rw = load8(static_cast<const W*>(w) + col), rb = load8(static_cast<const W*>(b) + col);
+  widen(rw, v);
+  widen(rb, u);
+}
+
 __device__ __forceinline__ float2 add2(float2 a, float b) { return __fadd2_rn(a, make_float2(b, b)); }
 __device__ __forceinline__ float2 mul2(float2 a, float b) { return __fmul2_rn(a, make_float2(b, b)); }
 
@@ -65,11 +77,12 @@ __device__ __forceinline__ int32_t columns_in(int32_t col, int32_t n, int32_t co
 
 // Quantise a lane's eight values (warp-collective) and store codes and scale; the numbers that
 // the codes stand for come back in v.
-__device__ __forceinline__ void put_codes(const View& q, int64_t row, int32_t col, int32_t cols, float2 (&v)[4],
+__device__ __forceinline__ void put_codes(const View& q, uint32_t row, int32_t col, int32_t cols, float2 (&v)[4],
                                           bool back) {
   float unit;
   const uint2 z = q.e5m2 ? quantise8<true>(v, unit) : quantise8<false>(v, unit);
-  if ((threadIdx.x & 15) == 0 && col < cols) *q.scale(row, col >> 7, 0) = unit;
+  // (one row a block)
+  if ((threadIdx.x & 15) == 0 && col < cols) q.scales[row * q.s_row + static_cast<uint32_t>(col >> 7) * q.s_col] = unit;
   store_codes8(q.codes + row * q.ld + col, z, cols - col);
   if (back) values8_any(q.e5m2 != 0, z, unit, v);
 }
@@ -99,6 +112,7 @@ __global__ void __launch_bounds__(ln_threads<R>()) ln_kernel(const __grid_consta
   const int32_t cols = p.cols;
   constexpr int D = ln_depth<T, C, R>();
   const bool has_res = p.residual != nullptr;
+  const bool whole_params = CODES && p.weight != nullptr && p.bias != nullptr && p.w_vec != 0;
   // this warp's buffers: [row in flight][chunk][x, residual]
   constexpr uint32_t kBuf = WarpRow<T>::kBytes;
   constexpr uint32_t kRow = 2 * C * kBuf;
@@ -118,6 +132,12 @@ __global__ void __launch_bounds__(ln_threads<R>()) ln_kernel(const __grid_consta
 #pragma unroll
   for (int c = 0; c < C; ++c) n_warp += columns_in(warp_col + c * tpr * 8, 256, cols);
   const float n_mine = static_cast<float>(n_warp);
+  int32_t n_own = 0;  // and this thread
+#pragma unroll
+  for (int c = 0; c < C; ++c) n_own += columns_in(col0 + c * tpr * 8, 8, cols);
+  const float n_thread = static_cast<float>(n_own), inv_thread = n_own > 0 ? 1.f / n_thread : 0.f;
+  const uint32_t holders = __ballot_sync(0xffffffffu, n_own > 0);
+  const int pivot_lane = holders != 0u ? __ffs(holders) - 1 : 0;
   const float inv_mine = n_warp > 0 ? 1.f / n_mine : 0.f;
   if (lane == 0) counts[warp] = n_mine;
   __syncthreads();
@@ -162,7 +182,7 @@ __global__ void __launch_bounds__(ln_threads<R>()) ln_kernel(const __grid_consta
     cp_async_wait<D - 1>();
     if constexpr (R == ROWS_ANY) __syncwarp();
     Raw8<T> h[C];
-    float2 sum = make_float2(0.f, 0.f);
+    float2 sum = make_float2(0.f, 0.f), v[C][4];
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       const int32_t col = col0 + c * tpr * 8;
@@ -173,36 +193,46 @@ __global__ void __launch_bounds__(ln_threads<R>()) ln_kernel(const __grid_consta
         if (p.h != nullptr && warp_col + c * tpr * 8 < cols)
           put_chunk<T, R>(static_cast<T*>(p.h) + row * p.ldh, c, col, cols, h[c]);
       }
-      float2 v[4];
-      widen(h[c], v);
+      widen(h[c], v[c]);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) sum = __fadd2_rn(sum, v[i]);
+      for (int i = 0; i < 4; ++i) sum = __fadd2_rn(sum, v[c][i]);
     }
     slot = (slot + 1) % D;
-    const float s = warp_sum(sum.x + sum.y);
-    float mean = s * inv_mine;
+    // a thread's mean and squared deviation, joined over the warp as the warps' are over the row
+    const float own = (sum.x + sum.y) * inv_thread;
     float2 dev = make_float2(0.f, 0.f);
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      const int32_t col = col0 + c * tpr * 8, wcol = warp_col + c * tpr * 8;
-      float2 v[4];
-      widen(h[c], v);
-      if (wcol >= 0 && wcol + 256 <= cols) {  // (the whole warp)
+      const int32_t col = col0 + c * tpr * 8;
+      if (col >= 0 && col + 8 <= cols) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float2 d = add2(v[i], -mean);
+          const float2 d = add2(v[c][i], -own);
           dev = __ffma2_rn(d, d, dev);
         }
       } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int32_t a = col + 2 * i, b = a + 1;
-          const float2 d = make_float2(a >= 0 && a < cols ? v[i].x - mean : 0.f, b >= 0 && b < cols ? v[i].y - mean : 0.f);
+          const float2 d = make_float2(a >= 0 && a < cols ? v[c][i].x - own : 0.f, b >= 0 && b < cols ? v[c][i].y - own : 0.f);
           dev = __ffma2_rn(d, d, dev);
         }
       }
     }
-    float m2 = warp_sum(dev.x + dev.y);
+    float mean, m2;
+    {
+      const float pivot = __shfl_sync(0xffffffffu, own, pivot_lane);
+      const float off = n_thread > 0.f ? own - pivot : 0.f;
+      float total = n_thread * off, square = fmaf(n_thread * off, off, dev.x + dev.y);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        total += __shfl_xor_sync(0xffffffffu, total, o);
+        square += __shfl_xor_sync(0xffffffffu, square, o);
+      }
+      const float d = total * inv_mine;
+      mean = pivot + d;
+      m2 = fmaxf(fmaf(-total, d, square), 0.f);
+    }
     if (tpr > 32) {
       float2* at = slots + flip * 32;
       if (lane == 0) at[warp] = make_float2(mean, m2);
@@ -236,8 +266,14 @@ __global__ void __launch_bounds__(ln_threads<R>()) ln_kernel(const __grid_consta
         }
       }
       if constexpr (!kHeld) {
-        load_param(p.weight, p.p_dtype, p.w_vec, col, cols, 1.f, w);
-        load_param(p.bias, p.p_dtype, p.w_vec, col, cols, 0.f, b);
+        if (whole_params && col + 8 <= cols) {
+          if (p.p_dtype == DT_BF16) both_params<__nv_bfloat16>(p.weight, p.bias, col, w, b);
+          else if (p.p_dtype == DT_F16) both_params<__half>(p.weight, p.bias, col, w, b);
+          else both_params<float>(p.weight, p.bias, col, w, b);
+        } else {
+          load_param(p.weight, p.p_dtype, p.w_vec, col, cols, 1.f, w);
+          load_param(p.bias, p.p_dtype, p.w_vec, col, cols, 0.f, b);
+        }
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i)
