@@ -140,7 +140,7 @@ bool try_shape(const Problem& q, int bn, int splits, Shape* s) {
   s->tiles_n = ceil_div(q.N, bn);
   s->tiles = s->tiles_m * s->tiles_n * (q.groups > 0 ? 1 : q.L);
   if (splits > 1 && (s->cg == 2 || splits > q.k_tiles || s->tiles * splits > q.sms)) return false;
-  s->a_rows = bn < 256 && q.groups == 0 && q.M <= 32 ? 32 : 128;
+  s->a_rows = bn < 256 && q.groups == 0 && q.M <= b128::kFewRows ? b128::kFewRows : 128;
   s->stage_bytes = (s->a_rows + bn / s->cg) * 128;
   const int ring = 2 * 8 * (128 + (q.bv ? std::max(bn, 128) : 4)) * 4;  // (kScaleSlots, kSlotBytes)
   const int outputs = bn == 256 ? 8 * q.out_stage : 128 * bn * 4 + 4 * q.out_stage;  // (a tile's sums, staging)

@@ -9,11 +9,13 @@
 // tcgen05.mma kind::f8f6f4 in tensor memory, is read, scaled and added to fp32 sums that stay in
 // registers over the whole of K.  What follows from that:
 //   * tensor memory holds no sums but the T_b in flight, and two warpgroups hold a tile's, a row
-//     and half of the columns a thread.  A block costs a warp its waits and a load's latency,
-//     whatever its columns, and from an MMA's end to the next one that may use its columns pass
-//     about 800 cycles.  Large products take 256 x 256 tiles on a CTA pair: 128 columns a
-//     thread, 224 registers (setmaxnreg takes them from the warpgroup that loads and issues), two
-//     buffers of 256 columns;
+//     and half of the columns a thread.  A block costs a warp its waits and loads' latency, some
+//     400 cycles, whatever its columns.  Large products take 256 x 256 tiles on a CTA pair: 128
+//     columns a thread, 224 registers (setmaxnreg takes them from the warpgroup that loads and
+//     issues), two buffers of 256 columns.  A block then takes 810 cycles, 512 of them the tensor
+//     core's: 8192^3 387 us (without the additions 335).  Measured and left: 256 x 128 tiles with
+//     four buffers (590), two MMAs of 128 columns a block, each half's buffers handed back by
+//     itself (444), the next block's first load under a block's last additions (439);
 //   * other products take 128 x 128 or 128 x 64 tiles on one CTA, with four buffers.  Their sums
 //     go to shared memory when K ends, where a third warpgroup turns them into outputs while the
 //     next tile's are added (or, split along K, while nothing else is left to do);
@@ -22,10 +24,12 @@
 //   * a thread's row has one scale a block, and with blocks of 128 rows its columns have one,
 //     too: a product and one packed fused multiply-add for two values.  With a scale for each
 //     row of B (weight gradients) two packed operations, the columns' scales out of shared memory;
-//   * scales come through a ring of their own, by two warps' cp.async, four blocks at a time and
-//     up to twelve ahead: they may lie anywhere (the rows of a group start on any row);
+//     (8192^3 598 us, 4096 x 1536 x 16384 with an fp32 C 176: shared memory's loads of them);
+//   * scales come through a ring of their own, by two warps' cp.async, eight blocks at a time and
+//     up to sixteen ahead: they may lie anywhere (the rows of a group start on any row);
 //   * few tiles are split along K over a cluster of 2 or 4 CTAs: with every rank's sums in its
-//     shared memory, each reads its share of the tile out of all of them and adds in rank order.
+//     shared memory, each reads its share of the tile out of all of them and adds in rank order
+//     (16 x 8192 x 8192 20 us: 3 of launch and first loads, 10 of the weights' bytes).
 //
 // Tile schedule, tensor maps, bounded waits and the staged stores are those of gemm_kernel
 // (gge_kernel.cuh).
@@ -38,11 +42,7 @@ namespace gge {
 namespace b128 {
 
 constexpr int kMaxStages = 16;
-constexpr int kScaleSlots = 2;   // of the scale ring,
-// A stage is a block's rows of A and of B.  Up to 32 rows of A in all (decoding) take no more room
-// than that in small tiles, so that more of B is on its way: the MMA reads 128 rows from there all
-// the same, and what it makes of others' bytes is not read.
-constexpr int kFewRows = 32;
+constexpr int kScaleSlots = 2;   // of the scale ring
 
 template <int BN, int CG, bool BV>
 struct GemmCfg {
@@ -56,7 +56,7 @@ struct GemmCfg {
   static constexpr int kBuffers = kWide ? 2 : 4;       // blocks' sums in tensor memory
   static constexpr int kTmemCols = kBuffers * BN;
   static constexpr int kScaleFloats = kBM + (BV ? (kWide ? 256 : 128) : 4);  // of a block
-  static constexpr int kSlotBlocks = 8;       // a slot of the scale ring holds so many blocks'
+  static constexpr int kSlotBlocks = 8;                // a slot of the scale ring holds so many blocks'
   static constexpr int kSlotBytes = kSlotBlocks * kScaleFloats * 4;
   static constexpr int kHalf = BN / 2;                 // columns a holding thread has
   static constexpr int kSumsBytes = kWide ? 0 : kBM * BN * 4;
