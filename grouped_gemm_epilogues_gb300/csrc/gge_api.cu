@@ -148,7 +148,7 @@ struct TmapKey {
   uint64_t d0, d1, d2, s1, s2;
   uint32_t b0, b1, b2;
   int es;
-  bool swizzle;
+  int swizzle;
   bool operator==(const TmapKey& o) const {
     return ptr == o.ptr && d0 == o.d0 && d1 == o.d1 && d2 == o.d2 && s1 == o.s1 && s2 == o.s2 &&
            b0 == o.b0 && b1 == o.b1 && b2 == o.b2 && es == o.es && swizzle == o.swizzle;
@@ -173,7 +173,7 @@ TmapCache& tmap_cache() {
 
 gge_status encode_3d(CUtensorMap* m, void* ptr, int es, uint64_t d0, uint64_t d1, uint64_t d2,
                      uint64_t s1_bytes, uint64_t s2_bytes, uint32_t b0, uint32_t b1, uint32_t b2,
-                     bool swizzle) {
+                     int swizzle) {
   const TmapKey k{ptr, d0, d1, d2, s1_bytes, s2_bytes, b0, b1, b2, es, swizzle};
   TmapCache& c = tmap_cache();
   {
@@ -193,7 +193,9 @@ gge_status encode_3d(CUtensorMap* m, void* ptr, int es, uint64_t d0, uint64_t d1
   const cuuint32_t box[3] = {b0, b1, b2};
   const cuuint32_t estr[3] = {1, 1, 1};
   CUresult r = fn(m, tmap_type(es), 3, ptr, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                  swizzle == 1   ? CU_TENSOR_MAP_SWIZZLE_128B
+                  : swizzle == 2 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                 : CU_TENSOR_MAP_SWIZZLE_NONE,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return GGE_ERR_CUDA;
   std::lock_guard<std::mutex> g(c.mu);

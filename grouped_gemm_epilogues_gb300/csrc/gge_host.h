@@ -30,10 +30,10 @@ gge_status check_view(const gge_tensor& t);
 // an output / C view: [M, N, L] N-major with 16-byte aligned rows and batches
 gge_status check_mn(const gge_tensor* t, int64_t M, int64_t N, int64_t L);
 gge_status check_workspace(void* ws, size_t bytes);
-// a tensor map of `es`-byte elements, box b0 x b1 x b2, with or without the
-// 128-byte swizzle; encoded maps are cached
+// a tensor map of `es`-byte elements, box b0 x b1 x b2, with the 128-byte swizzle (1), without
+// one (0) or with the 64-byte swizzle (2); encoded maps are cached
 gge_status encode_3d(CUtensorMap* m, void* ptr, int es, uint64_t d0, uint64_t d1, uint64_t d2,
                      uint64_t s1_bytes, uint64_t s2_bytes, uint32_t b0, uint32_t b1,
-                     uint32_t b2 = 1, bool swizzle = true);
+                     uint32_t b2 = 1, int swizzle = 1);
 
 }  // namespace gge

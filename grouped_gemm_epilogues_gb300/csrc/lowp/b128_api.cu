@@ -75,7 +75,7 @@ gge_status take_values(const gge_tensor* values, int64_t rows, int64_t cols, int
 
 struct GemmPlan {
   b128::GemmParams gp;
-  CUtensorMap a, b;
+  b128::GemmMaps maps;
   LaunchShape shape;
   int tile;
   bool empty;
@@ -129,7 +129,7 @@ struct Problem {
   int64_t M, N, L, k_tiles;
   int groups;
   bool bv, codes_out;
-  int out_stage, max_stages, sms;
+  int out_stage, wide_stage, max_stages, sms;
 };
 
 bool try_shape(const Problem& q, int bn, int splits, Shape* s) {
@@ -143,7 +143,7 @@ bool try_shape(const Problem& q, int bn, int splits, Shape* s) {
   s->a_rows = bn < 256 && q.groups == 0 && q.M <= b128::kFewRows ? b128::kFewRows : 128;
   s->stage_bytes = (s->a_rows + bn / s->cg) * 128;
   const int ring = 2 * 8 * (128 + (q.bv ? std::max(bn, 128) : 4)) * 4;  // (kScaleSlots, kSlotBytes)
-  const int outputs = bn == 256 ? 8 * q.out_stage : 128 * bn * 4 + 4 * q.out_stage;  // (a tile's sums, staging)
+  const int outputs = bn == 256 ? 8 * q.wide_stage : 128 * bn * 4 + 4 * q.out_stage;  // (a tile's sums, staging)
   const int fixed = 1024 + 512 + outputs + ring +
                     (q.groups > 0 ? 2 * (kMaxGroupsHost + 1) * 4 : 0);
   s->stages = std::min(q.max_stages, (kMaxSmemOptin - fixed) / s->stage_bytes);
@@ -235,6 +235,14 @@ gge_status plan_b128(const gge_gemm_b128_args* a, bool dact, void* ws, size_t ws
   q.bv = a->B.block_rows == 1;
   q.codes_out = a->D8 != nullptr || a->PostAct8 != nullptr;
   q.out_stage = out_es == 4 || q.codes_out ? 4096 : 2048;
+  // 16-bit outputs of 256-wide tiles leave by TMA, three chunks of a warp on their way
+  const bool c_read = a->C != nullptr || a->C8 != nullptr;
+  const auto by_tma = [&](const gge_tensor* t) {
+    return t != nullptr && !c_read && elem_bytes(t->dtype) == 2 && M > 1 && aligned16(t->ptr) && t->stride_row % 8 == 0 &&
+           (L == 1 || t->stride_batch % 8 == 0);
+  };
+  const int tma = (by_tma(a->D) ? 1 : 0) | (by_tma(a->PostAct) ? 2 : 0);
+  q.wide_stage = tma != 0 ? 3 * 2048 : q.out_stage;
   const int want = cfg ? cfg->tile_n : 0;
   if (want != 0 && want != 256 && want != 128 && (want != 64 || q.codes_out)) return GGE_ERR_UNSUPPORTED;
   q.max_stages = cfg && cfg->stages > 0 ? std::min(8, static_cast<int>(cfg->stages)) : 16;
@@ -300,7 +308,8 @@ gge_status plan_b128(const gge_gemm_b128_args* a, bool dact, void* ws, size_t ws
   p.beta = a->beta;
   p.alpha_dev = a->alpha_dev;
   p.beta_dev = a->beta_dev;
-  p.out_stage_bytes = q.out_stage;
+  p.out_stage_bytes = sh.bn == 256 ? q.wide_stage : q.out_stage;
+  pl.gp.by_tma = sh.bn == 256 ? tma : 0;
   p.f8 = 1;
   // instruction descriptor: fp32 sums, operand types (e4m3 is 0, e5m2 is 1), N >> 3, M >> 4
   p.idesc = (1u << 4) | ((a->A.dtype == GGE_E5M2 ? 1u : 0u) << 7) | ((a->B.dtype == GGE_E5M2 ? 1u : 0u) << 10) |
@@ -324,7 +333,10 @@ gge_status plan_b128(const gge_gemm_b128_args* a, bool dact, void* ws, size_t ws
     p.num_tiles = static_cast<int32_t>(sh.tiles);
   }
   pl.shape.grid = pl.shape.cluster * static_cast<int>(std::min<int64_t>(most, units));
-  if (K == 0) return GGE_OK;  // nothing is loaded
+  if (K == 0) {  // nothing is loaded
+    pl.gp.by_tma = 0;
+    return GGE_OK;
+  }
 
   const auto map = [&](CUtensorMap* m, const gge_b128_tensor& t, uint32_t box_rows) {
     const uint64_t ld = t.rows > 1 ? static_cast<uint64_t>(t.stride_row) : static_cast<uint64_t>((t.cols + 15) / 16 * 16);
@@ -332,8 +344,15 @@ gge_status plan_b128(const gge_gemm_b128_args* a, bool dact, void* ws, size_t ws
     return encode_3d(m, t.codes, 1, static_cast<uint64_t>(K), static_cast<uint64_t>(t.rows),
                      static_cast<uint64_t>(t.batch), ld, sb, 128, box_rows);
   };
-  s = map(&pl.a, a->A, static_cast<uint32_t>(sh.a_rows));
-  if (s == GGE_OK) s = map(&pl.b, a->B, static_cast<uint32_t>(sh.bn / sh.cg));
+  s = map(&pl.maps.a, a->A, static_cast<uint32_t>(sh.a_rows));
+  if (s == GGE_OK) s = map(&pl.maps.b, a->B, static_cast<uint32_t>(sh.bn / sh.cg));
+  const auto out_map = [&](CUtensorMap* m, const gge_tensor& t) {
+    const uint64_t ld = static_cast<uint64_t>(t.stride_row) * 2;
+    return encode_3d(m, t.ptr, 2, static_cast<uint64_t>(N), static_cast<uint64_t>(M), static_cast<uint64_t>(L), ld,
+                     L > 1 ? static_cast<uint64_t>(t.stride_batch) * 2 : static_cast<uint64_t>(M) * ld, 32, 32, 1, 2);
+  };
+  if (s == GGE_OK && (pl.gp.by_tma & 1)) s = out_map(&pl.maps.d, *a->D);
+  if (s == GGE_OK && (pl.gp.by_tma & 2)) s = out_map(&pl.maps.post, *a->PostAct);
   return s;
 }
 
@@ -342,9 +361,9 @@ gge_status run_b128(const gge_gemm_b128_args* args, bool dact, void* ws, size_t 
   const gge_status s = plan_b128(args, dact, ws, ws_bytes, &pl);
   if (s != GGE_OK || pl.empty) return s;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  return launched(pl.tile == 256   ? b128::launch_tile<256, 2>(pl.a, pl.b, pl.gp, pl.shape, st)
-                  : pl.tile == 128 ? b128::launch_tile<128, 1>(pl.a, pl.b, pl.gp, pl.shape, st)
-                                   : b128::launch_tile<64, 1>(pl.a, pl.b, pl.gp, pl.shape, st));
+  return launched(pl.tile == 256   ? b128::launch_tile<256, 2>(pl.maps, pl.gp, pl.shape, st)
+                  : pl.tile == 128 ? b128::launch_tile<128, 1>(pl.maps, pl.gp, pl.shape, st)
+                                   : b128::launch_tile<64, 1>(pl.maps, pl.gp, pl.shape, st));
 }
 
 // ------------------------------------------------------------ layer norm

@@ -13,7 +13,7 @@
 //     400 cycles, whatever its columns.  Large products take 256 x 256 tiles on a CTA pair: 128
 //     columns a thread, 224 registers (setmaxnreg takes them from the warpgroup that loads and
 //     issues), two buffers of 256 columns.  A block then takes 810 cycles, 512 of them the tensor
-//     core's: 8192^3 387 us (without the additions 335).  Measured and left: 256 x 128 tiles with
+//     core's: 8192^3 381 us (without the additions 335).  Measured and left: 256 x 128 tiles with
 //     four buffers (590), two MMAs of 128 columns a block, each half's buffers handed back by
 //     itself (444), the next block's first load under a block's last additions (439);
 //   * other products take 128 x 128 or 128 x 64 tiles on one CTA, with four buffers.  Their sums
@@ -24,7 +24,7 @@
 //   * a thread's row has one scale a block, and with blocks of 128 rows its columns have one,
 //     too: a product and one packed fused multiply-add for two values.  With a scale for each
 //     row of B (weight gradients) two packed operations, the columns' scales out of shared memory;
-//     (8192^3 598 us, 4096 x 1536 x 16384 with an fp32 C 176: shared memory's loads of them);
+//     (8192^3 578 us, 4096 x 1536 x 16384 with an fp32 C 176: shared memory's loads of them);
 //   * scales come through a ring of their own, by two warps' cp.async, eight blocks at a time and
 //     up to sixteen ahead: they may lie anywhere (the rows of a group start on any row);
 //   * few tiles are split along K over a cluster of 2 or 4 CTAs: with every rank's sums in its
@@ -785,6 +785,42 @@ __device__ __forceinline__ void store_codes_held(const GemmParams& gp, const Vie
   copy_codes_out(gp, q, at, stg);
 }
 
+// ... of a 16-bit output by TMA, so that the warp goes on with the next tile while they leave
+// (4096^3 with two outputs 83 -> 78 us, 8192^3 387 -> 381).  Chunk c takes the buffer c % 3 of the warp's three; what
+// else uses the buffers drains them first.  Warp-collective.
+__device__ __forceinline__ void drain_stores() {
+  if ((threadIdx.x & 31) == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+  __syncwarp();
+}
+__device__ __forceinline__ void store32_tma(const CUtensorMap* map, uint32_t stg, int c, const float2* v, int dtype,
+                                            const Spot& at) {
+  asm volatile("" : "+r"(stg));
+  const int lane = threadIdx.x & 31;
+  if (c == 0) {
+    drain_stores();
+  } else if (c == 3) {
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 2;" ::: "memory");
+    __syncwarp();
+  }
+  stg += (c % 3) * 2048;
+  const bool bf16 = dtype == DT_BF16;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = bf16 ? pack2<true>(v[4 * q + i].x, v[4 * q + i].y) : pack2<false>(v[4 * q + i].x, v[4 * q + i].y);
+    ptx::st_shared_v4(stg + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4), make_uint4(w[0], w[1], w[2], w[3]));
+  }
+  ptx::fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map),
+                 "r"(at.col_base + 32 * c), "r"(at.row_base), "r"(static_cast<int32_t>(at.batch)), "r"(stg)
+                 : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+  }
+}
+
 template <int ACT>
 __device__ __forceinline__ void act_held_t(float2 (&acc)[64]) {
 #pragma unroll
@@ -800,16 +836,21 @@ __device__ __forceinline__ void act_held(int act, float2 (&acc)[64]) {
   }
 }
 
-__device__ __forceinline__ void finish_held(const GemmParams& gp, const Spot& at, float2 (&acc)[64], uint32_t stg) {
+__device__ __forceinline__ void finish_held(const GemmParams& gp, const CUtensorMap* tmD, const CUtensorMap* tmP,
+                                            const Spot& at, float2 (&acc)[64], uint32_t stg) {
   const Params& p = gp.p;
   const float alpha = p.dact ? 1.f : (p.alpha_dev ? *p.alpha_dev : p.alpha);
+  // (a group's last rows, by themselves, end before the box)
+  const int tma = at.rows_valid == 32 ? gp.by_tma : 0;
+  if (gp.by_tma != 0 && tma == 0) drain_stores();
   if (!has_c(gp) && p.post == nullptr && gp.d8.codes == nullptr && gp.p8.codes == nullptr) {  // D alone
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
       if (at.col_base + 32 * c >= p.N) break;
 #pragma unroll
       for (int j = 0; j < 16; ++j) acc[16 * c + j] = __fmul2_rn(acc[16 * c + j], make_float2(alpha, alpha));
-      store32_pairs(stg, acc + 16 * c, p.d_dtype, p.d, p.ldd, p.sbd, at, at.col_base + 32 * c, p.N);
+      if (tma & 1) store32_tma(tmD, stg, c, acc + 16 * c, p.d_dtype, at);
+      else store32_pairs(stg, acc + 16 * c, p.d_dtype, p.d, p.ldd, p.sbd, at, at.col_base + 32 * c, p.N);
     }
     return;
   }
@@ -831,14 +872,17 @@ __device__ __forceinline__ void finish_held(const GemmParams& gp, const Spot& at
         for (int j = 0; j < 64; ++j) acc[j] = __fmul2_rn(acc[j], make_float2(alpha, alpha));
       }
       if (out != nullptr) {
+        if (gp.by_tma != 0 && !(tma & (1 << pass))) drain_stores();
 #pragma unroll
         for (int c = 0; c < 4; ++c)
           if (at.col_base + 32 * c < p.N) {
-            if (pass == 0) store32_pairs(stg, acc + 16 * c, p.d_dtype, p.d, p.ldd, p.sbd, at, at.col_base + 32 * c, p.N);
+            if (tma & (1 << pass)) store32_tma(pass == 0 ? tmD : tmP, stg, c, acc + 16 * c, pass == 0 ? p.d_dtype : p.p_dtype, at);
+            else if (pass == 0) store32_pairs(stg, acc + 16 * c, p.d_dtype, p.d, p.ldd, p.sbd, at, at.col_base + 32 * c, p.N);
             else store32_pairs(stg, acc + 16 * c, p.p_dtype, p.post, p.ldp, p.sbp, at, at.col_base + 32 * c, p.N);
           }
       }
       if (q.codes != nullptr) {
+        if (gp.by_tma != 0) drain_stores();
         float top = 0.f;
 #pragma unroll
         for (int j = 0; j < 64; ++j) top = mx::max_abs(mx::max_abs(top, acc[j].x), acc[j].y);
@@ -977,7 +1021,7 @@ __device__ __forceinline__ Spot spot_of(const Params& p, const Memory& m, const 
 // The warps that hold the sums while K runs.  (Where they finish the tile themselves, what that
 // needs is worked out after the main loop, whose registers are the sums'.)
 template <int BN, int CG, bool BV>
-__device__ __forceinline__ void hold_role(const GemmParams& gp) {
+__device__ __forceinline__ void hold_role(const GemmParams& gp, const CUtensorMap* tmD, const CUtensorMap* tmP) {
   using Cfg = GemmCfg<BN, CG, BV>;
   const Params& p = gp.p;
   const int quad = (threadIdx.x >> 5) & 3, half = (threadIdx.x >> 7) - 1;
@@ -1004,7 +1048,7 @@ __device__ __forceinline__ void hold_role(const GemmParams& gp) {
       Spot spot = spot_of<BN, CG, BV>(p, m, part<CG>(gp), t, quad);
       spot.col_base += half * Cfg::kHalf;
       if (spot.rows_valid > 0 && spot.col_base < p.N)
-        finish_held(gp, spot, acc, m.out_stage + (threadIdx.x / 32 - Cfg::kFirstHold) * p.out_stage_bytes);
+        finish_held(gp, tmD, tmP, spot, acc, m.out_stage + (threadIdx.x / 32 - Cfg::kFirstHold) * p.out_stage_bytes);
     } else {
       if (!wait_warp(m.ctrl, m.ctrl + kFreeBar, free_phase, p, 12, t)) return;
       free_phase ^= 1u;
@@ -1072,6 +1116,7 @@ __device__ __forceinline__ void finish_role(const GemmParams& gp, int who) {
 template <int BN, int CG, bool BV>
 __global__ void __launch_bounds__(GemmCfg<BN, CG, BV>::kThreads, 1)
     b128_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                     const __grid_constant__ CUtensorMap tmD, const __grid_constant__ CUtensorMap tmP,
                      const __grid_constant__ GemmParams gp) {
   using Cfg = GemmCfg<BN, CG, BV>;
   const Params& p = gp.p;
@@ -1156,9 +1201,10 @@ __global__ void __launch_bounds__(GemmCfg<BN, CG, BV>::kThreads, 1)
     static_assert(Cfg::kWide || Cfg::kHoldRegs == Cfg::kFinishRegs, "one share for both");
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Cfg::kHoldRegs));
     if constexpr (Cfg::kWide) {
-      hold_role<BN, CG, BV>(gp);
+      hold_role<BN, CG, BV>(gp, &tmD, &tmP);
+      if ((threadIdx.x & 31) == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     } else {
-      if (warp < Cfg::kFirstFinish) hold_role<BN, CG, BV>(gp);
+      if (warp < Cfg::kFirstFinish) hold_role<BN, CG, BV>(gp, &tmD, &tmP);
       finish_role<BN, CG, BV>(gp, warp < Cfg::kFirstFinish ? (warp - Cfg::kFirstHold) / 4 + 1 : 0);
     }
   } else {
@@ -1241,13 +1287,12 @@ cudaLaunchConfig_t gemm_config(int grid, size_t smem, int cluster, cudaStream_t 
 }
 
 template <int BN, int CG, bool BV>
-cudaError_t launch_one(const CUtensorMap& a, const CUtensorMap& b, const GemmParams& gp, const LaunchShape& shape,
-                       cudaStream_t stream) {
+cudaError_t launch_one(const GemmMaps& maps, const GemmParams& gp, const LaunchShape& shape, cudaStream_t stream) {
   const cudaError_t e = allow_smem<b128_gemm_kernel<BN, CG, BV>>();
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[2];
   const cudaLaunchConfig_t cfg = gemm_config<BN, CG, BV>(shape.grid, shape.smem, shape.cluster, stream, attr);
-  return cudaLaunchKernelEx(&cfg, b128_gemm_kernel<BN, CG, BV>, a, b, gp);
+  return cudaLaunchKernelEx(&cfg, b128_gemm_kernel<BN, CG, BV>, maps.a, maps.b, maps.d, maps.post, gp);
 }
 
 // (Registers leave room for one CTA an SM, so tensor memory needs no count of its own.  The
@@ -1279,10 +1324,9 @@ int units_one(size_t smem, int cluster) {
 }
 
 template <int BN, int CG>
-cudaError_t launch_tile(const CUtensorMap& a, const CUtensorMap& b, const GemmParams& gp, const LaunchShape& shape,
-                        cudaStream_t stream) {
-  return gp.b_rows_one ? launch_one<BN, CG, true>(a, b, gp, shape, stream)
-                       : launch_one<BN, CG, false>(a, b, gp, shape, stream);
+cudaError_t launch_tile(const GemmMaps& maps, const GemmParams& gp, const LaunchShape& shape, cudaStream_t stream) {
+  return gp.b_rows_one ? launch_one<BN, CG, true>(maps, gp, shape, stream)
+                       : launch_one<BN, CG, false>(maps, gp, shape, stream);
 }
 template <int BN, int CG>
 int units_tile(bool b_rows_one, size_t smem, int cluster) {
@@ -1290,8 +1334,7 @@ int units_tile(bool b_rows_one, size_t smem, int cluster) {
 }
 
 #define GGE_B128_INSTANTIATE(BN, CG)                                                                     \
-  template cudaError_t launch_tile<BN, CG>(const CUtensorMap&, const CUtensorMap&, const GemmParams&, \
-                                           const LaunchShape&, cudaStream_t);                          \
+  template cudaError_t launch_tile<BN, CG>(const GemmMaps&, const GemmParams&, const LaunchShape&, cudaStream_t); \
   template int units_tile<BN, CG>(bool, size_t, int);
 
 }  // namespace b128

@@ -92,14 +92,18 @@ struct GemmParams {
   View c8, d8, p8;     // 8-bit forms of C, D and PostAct
   int32_t b_rows_one;  // B has a scale a row: one for each of a tile's columns
   int32_t splits;      // CTAs of a cluster that share a tile's K: 1, 2 or 4
+  int32_t by_tma;      // 256-wide tiles without a C: bit 0 D, bit 1 PostAct leave by TMA
   int32_t a_rows;      // rows of A in a stage (small tiles): 128, or 32 where there are no more
+};
+
+struct GemmMaps {
+  CUtensorMap a, b, d, post;
 };
 
 // Tile shapes: 256 x 256 on a CTA pair, 128 x 128 and 128 x 64 on one CTA.
 // (one translation unit a tile shape)
 template <int BN, int CG>
-cudaError_t launch_tile(const CUtensorMap& a, const CUtensorMap& b, const GemmParams& gp, const LaunchShape& shape,
-                        cudaStream_t stream);
+cudaError_t launch_tile(const GemmMaps& maps, const GemmParams& gp, const LaunchShape& shape, cudaStream_t stream);
 // Resident CTAs, or clusters of `cluster` CTAs, on the current device, or -1.
 template <int BN, int CG>
 int units_tile(bool b_rows_one, size_t smem, int cluster);
