@@ -904,7 +904,8 @@ def gge_gemm_b128(A, B, D=None, C=None, PostAct=None, act="none", alpha=1.0, bet
 def gge_gemm_b128_dact(A, B, PreAct, D, act, PostAct=None, cu_seqlens_m=None, config=None,
                        workspace=None):
     """Backward activation epilogue on B128Tensors: D = act'(PreAct) * (A @ B^T), PostAct =
-    act(PreAct), each a tensor or a B128Tensor.  cu_seqlens_m: as in gge_gemm_b128_varlen_m."""
+    act(PreAct), each a tensor or a B128Tensor; neither output may be PreAct itself.
+    cu_seqlens_m: as in gge_gemm_b128_varlen_m."""
     _gemm_b128("gge_gemm_b128_dact", A, B, D, PreAct, PostAct, act, 1.0, 1.0, None, None, config,
                workspace, True, cu_seqlens_m)
 
