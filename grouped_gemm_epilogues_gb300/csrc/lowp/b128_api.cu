@@ -235,14 +235,17 @@ gge_status plan_b128(const gge_gemm_b128_args* a, bool dact, void* ws, size_t ws
   q.bv = a->B.block_rows == 1;
   q.codes_out = a->D8 != nullptr || a->PostAct8 != nullptr;
   q.out_stage = out_es == 4 || q.codes_out ? 4096 : 2048;
-  // 16-bit outputs of 256-wide tiles leave by TMA, three chunks of a warp on their way
+  // 16- and 8-bit outputs of 256-wide tiles leave by TMA, up to three chunks of a warp on their way
   const bool c_read = a->C != nullptr || a->C8 != nullptr;
   const auto by_tma = [&](const gge_tensor* t) {
     return t != nullptr && !c_read && elem_bytes(t->dtype) == 2 && M > 1 && aligned16(t->ptr) && t->stride_row % 8 == 0 &&
            (L == 1 || t->stride_batch % 8 == 0);
   };
-  const int tma = (by_tma(a->D) ? 1 : 0) | (by_tma(a->PostAct) ? 2 : 0);
-  q.wide_stage = tma != 0 ? 3 * 2048 : q.out_stage;
+  // (a row's end is exact to 16 bytes only: 72 columns of codes wrote 80)
+  const bool codes_tma = !c_read && M > 1 && N % 16 == 0;
+  const int tma = (by_tma(a->D) ? 1 : 0) | (by_tma(a->PostAct) ? 2 : 0) | (a->D8 && codes_tma ? 4 : 0) |
+                  (a->PostAct8 && codes_tma ? 8 : 0);
+  q.wide_stage = (tma & 3) != 0 ? 3 * 2048 : q.out_stage;
   const int want = cfg ? cfg->tile_n : 0;
   if (want != 0 && want != 256 && want != 128 && (want != 64 || q.codes_out)) return GGE_ERR_UNSUPPORTED;
   q.max_stages = cfg && cfg->stages > 0 ? std::min(8, static_cast<int>(cfg->stages)) : 16;
@@ -353,6 +356,13 @@ gge_status plan_b128(const gge_gemm_b128_args* a, bool dact, void* ws, size_t ws
   };
   if (s == GGE_OK && (pl.gp.by_tma & 1)) s = out_map(&pl.maps.d, *a->D);
   if (s == GGE_OK && (pl.gp.by_tma & 2)) s = out_map(&pl.maps.post, *a->PostAct);
+  const auto codes_map = [&](CUtensorMap* m, const gge_b128_tensor& t) {
+    const uint64_t ld = static_cast<uint64_t>(t.stride_row);
+    return encode_3d(m, t.codes, 1, static_cast<uint64_t>(N), static_cast<uint64_t>(M), static_cast<uint64_t>(L), ld,
+                     L > 1 ? static_cast<uint64_t>(t.stride_batch) : static_cast<uint64_t>(M) * ld, 128, 32);
+  };
+  if (s == GGE_OK && (pl.gp.by_tma & 4)) s = codes_map(&pl.maps.d, *a->D8);
+  if (s == GGE_OK && (pl.gp.by_tma & 8)) s = codes_map(&pl.maps.post, *a->PostAct8);
   return s;
 }
 

@@ -762,35 +762,23 @@ __device__ __forceinline__ void store32_pairs(uint32_t stg, const float2* v, int
   store32(stg, x, dtype, out, ld, sb, at, col0, N);
 }
 
-template <bool E5M2>
-__device__ __forceinline__ void store_codes_held(const GemmParams& gp, const View& q, const Spot& at,
-                                                 const float2 (&acc)[64], float top, uint32_t stg) {
-  asm volatile("" : "+r"(stg));
-  const int lane = threadIdx.x & 31;
-  float factor;
-  const float unit = block_scale<E5M2>(mx::abs_bits(top), factor);
-  if (lane < at.rows_valid) *q.scale(at.row_base + lane, at.col_base >> 7, at.batch) = unit;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    uint32_t w[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float2 a = __fmul2_rn(acc[8 * i + 2 * j], make_float2(factor, factor));
-      const float2 b = __fmul2_rn(acc[8 * i + 2 * j + 1], make_float2(factor, factor));
-      w[j] = pack4<E5M2>(a.x, a.y, b.x, b.y);
-    }
-    ptx::st_shared_v4(stg + lane * 128 + ((i ^ (lane & 7)) << 4), make_uint4(w[0], w[1], w[2], w[3]));
-  }
-  __syncwarp();
-  copy_codes_out(gp, q, at, stg);
-}
-
-// ... of a 16-bit output by TMA, so that the warp goes on with the next tile while they leave
-// (4096^3 with two outputs 83 -> 78 us, 8192^3 387 -> 381).  Chunk c takes the buffer c % 3 of the warp's three; what
-// else uses the buffers drains them first.  Warp-collective.
+// The same by TMA, so that the warp goes on with the next tile while they leave
+// (4096^3 with two outputs 83 -> 78 us, 8192^3 387 -> 381).  Chunk c of a 16-bit output takes
+// the buffer c % 3 of the warp's three, the codes of 32 rows the first two; what uses the buffers
+// otherwise drains them first.  Warp-collective.
 __device__ __forceinline__ void drain_stores() {
   if ((threadIdx.x & 31) == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
   __syncwarp();
+}
+__device__ __forceinline__ void send_box(const CUtensorMap* map, uint32_t stg, int32_t col, const Spot& at) {
+  ptx::fence_proxy_async_smem();
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map), "r"(col),
+                 "r"(at.row_base), "r"(static_cast<int32_t>(at.batch)), "r"(stg)
+                 : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+  }
 }
 __device__ __forceinline__ void store32_tma(const CUtensorMap* map, uint32_t stg, int c, const float2* v, int dtype,
                                             const Spot& at) {
@@ -811,13 +799,34 @@ __device__ __forceinline__ void store32_tma(const CUtensorMap* map, uint32_t stg
     for (int i = 0; i < 4; ++i) w[i] = bf16 ? pack2<true>(v[4 * q + i].x, v[4 * q + i].y) : pack2<false>(v[4 * q + i].x, v[4 * q + i].y);
     ptx::st_shared_v4(stg + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4), make_uint4(w[0], w[1], w[2], w[3]));
   }
-  ptx::fence_proxy_async_smem();
-  __syncwarp();
-  if (lane == 0) {
-    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map),
-                 "r"(at.col_base + 32 * c), "r"(at.row_base), "r"(static_cast<int32_t>(at.batch)), "r"(stg)
-                 : "memory");
-    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+  send_box(map, stg, at.col_base + 32 * c, at);
+}
+
+// (map: not NULL where they leave by TMA)
+template <bool E5M2>
+__device__ __forceinline__ void store_codes_held(const GemmParams& gp, const View& q, const CUtensorMap* map,
+                                                 const Spot& at, const float2 (&acc)[64], float top, uint32_t stg) {
+  asm volatile("" : "+r"(stg));
+  const int lane = threadIdx.x & 31;
+  float factor;
+  const float unit = block_scale<E5M2>(mx::abs_bits(top), factor);
+  if (lane < at.rows_valid) *q.scale(at.row_base + lane, at.col_base >> 7, at.batch) = unit;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    uint32_t w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 a = __fmul2_rn(acc[8 * i + 2 * j], make_float2(factor, factor));
+      const float2 b = __fmul2_rn(acc[8 * i + 2 * j + 1], make_float2(factor, factor));
+      w[j] = pack4<E5M2>(a.x, a.y, b.x, b.y);
+    }
+    ptx::st_shared_v4(stg + lane * 128 + ((i ^ (lane & 7)) << 4), make_uint4(w[0], w[1], w[2], w[3]));
+  }
+  if (map == nullptr) {
+    __syncwarp();
+    copy_codes_out(gp, q, at, stg);
+  } else {
+    send_box(map, stg, at.col_base, at);
   }
 }
 
@@ -882,12 +891,13 @@ __device__ __forceinline__ void finish_held(const GemmParams& gp, const CUtensor
           }
       }
       if (q.codes != nullptr) {
+        const CUtensorMap* map = tma & (4 << pass) ? (pass == 0 ? tmD : tmP) : nullptr;
         if (gp.by_tma != 0) drain_stores();
         float top = 0.f;
 #pragma unroll
         for (int j = 0; j < 64; ++j) top = mx::max_abs(mx::max_abs(top, acc[j].x), acc[j].y);
-        if (q.e5m2) store_codes_held<true>(gp, q, at, acc, top, stg);
-        else store_codes_held<false>(gp, q, at, acc, top, stg);
+        if (q.e5m2) store_codes_held<true>(gp, q, map, at, acc, top, stg);
+        else store_codes_held<false>(gp, q, map, at, acc, top, stg);
       }
       continue;
     }
@@ -941,8 +951,9 @@ __device__ __forceinline__ void finish_held(const GemmParams& gp, const CUtensor
       move_round(acc);
     }
     if (q.codes != nullptr && at.col_base < p.N) {
-      if (q.e5m2) store_codes_held<true>(gp, q, at, acc, top, stg);
-      else store_codes_held<false>(gp, q, at, acc, top, stg);
+      const CUtensorMap* const map = nullptr;
+      if (q.e5m2) store_codes_held<true>(gp, q, map, at, acc, top, stg);
+      else store_codes_held<false>(gp, q, map, at, acc, top, stg);
     }
   }
 }

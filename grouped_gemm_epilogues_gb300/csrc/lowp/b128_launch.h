@@ -92,7 +92,7 @@ struct GemmParams {
   View c8, d8, p8;     // 8-bit forms of C, D and PostAct
   int32_t b_rows_one;  // B has a scale a row: one for each of a tile's columns
   int32_t splits;      // CTAs of a cluster that share a tile's K: 1, 2 or 4
-  int32_t by_tma;      // 256-wide tiles without a C: bit 0 D, bit 1 PostAct leave by TMA
+  int32_t by_tma;      // 256-wide tiles without a C: bits 0 to 3: D, PostAct, D8, PostAct8 leave by TMA
   int32_t a_rows;      // rows of A in a stage (small tiles): 128, or 32 where there are no more
 };
 
