@@ -70,6 +70,10 @@ __device__ __forceinline__ float2 row_sum2(float a, float b, int tpr, float2* sl
   return make_float2(warp_sum(v.x), warp_sum(v.y));
 }
 
+// A sum of squares that rounding may have left below zero.  (A NaN stays one: of a row that holds an
+// infinity or a NaN nothing is a number.)
+__device__ __forceinline__ float not_below_zero(float v) { return v < 0.f ? 0.f : v; }
+
 // Columns of [col, col + n) that a row of `cols` has.
 __device__ __forceinline__ int32_t columns_in(int32_t col, int32_t n, int32_t cols) {
   return max(min(col + n, cols) - max(col, 0), 0);
@@ -231,7 +235,7 @@ __global__ void __launch_bounds__(ln_threads<R>()) ln_kernel(const __grid_consta
       }
       const float d = total * inv_mine;
       mean = pivot + d;
-      m2 = fmaxf(fmaf(-total, d, square), 0.f);
+      m2 = not_below_zero(fmaf(-total, d, square));
     }
     if (tpr > 32) {
       float2* at = slots + flip * 32;
@@ -244,7 +248,7 @@ __global__ void __launch_bounds__(ln_threads<R>()) ln_kernel(const __grid_consta
       const float square = warp_sum(fmaf(n_lane * off, off, w.y));
       const float d = total * inv_cols;
       mean = first + d;
-      m2 = fmaxf(fmaf(-total, d, square), 0.f);
+      m2 = not_below_zero(fmaf(-total, d, square));
       flip ^= 1;
     }
     // (rounded correctly: an error of rstd moves every value of the row the same way)
