@@ -8,9 +8,11 @@
 // thread's sums, of its own values, are joined to a warp's and those to the row's by mean and
 // squared deviation,
 //   M2 = sum over parts of M2_p + n_p (mean_p - mean)^2,
-// with the parts' means taken relative to the first one's, so that no sum of squares is large
-// against the variance, whatever the mean.  (One reduction over the warp for both sums; a warp's
-// mean first and then its deviations: 16384 x 8192 to codes and values 281 us, so 228.)
+// with the parts' means taken relative to one of them, and once more relative to the result where
+// that one lay far from it (see join), so that no sum of squares is large against the variance.
+// What is left of a mean far from zero is its own rounding in a thread's differences.  (One
+// reduction over the warp for both sums; a warp's mean first and then its deviations: 16384 x 8192 to
+// codes and values 281 us, so 228.)
 //
 // Backward, n = (h - mean) rstd, g = dy w, for dh the gradient that reaches h directly:
 //   dx = rstd (g - mean(g) - n mean(g n)) + dh    dw = sum over rows of dy n    db = of dy
@@ -19,6 +21,8 @@
 // shared memory by cp.async while a row is reduced in registers and written, so every value is
 // read once; a row's lie in memory (Rows) decides whether anything has to be shifted.
 #pragma once
+
+#include <type_traits>
 
 #include "b128_launch.h"
 #include "norm_rows.cuh"
@@ -70,9 +74,30 @@ __device__ __forceinline__ float2 row_sum2(float a, float b, int tpr, float2* sl
   return make_float2(warp_sum(v.x), warp_sum(v.y));
 }
 
-// A sum of squares that rounding may have left below zero.  (A NaN stays one: of a row that holds an
-// infinity or a NaN nothing is a number.)
-__device__ __forceinline__ float not_below_zero(float v) { return v < 0.f ? 0.f : v; }
+__device__ __forceinline__ void warp_sums(float& a, float& b) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    a += __shfl_xor_sync(0xffffffffu, a, o);
+    b += __shfl_xor_sync(0xffffffffu, b, o);
+  }
+}
+
+// Parts of a row joined: with off = mean_p - pivot, total = sum n_p off and square = sum (M2_p + n_p off^2),
+//   mean = pivot + total / n      M2 = square - total^2 / n.
+// The difference loses as much as square is larger than M2: where the pivot, one of the parts' means,
+// is that of a part with a value far from all others, 32 times and more.  `far`: then it has to be
+// done again relative to the mean just found.  (With M2 above two thirds of square a join keeps 24
+// units: three roundings and five additions of up to 1.5 M2, and seven of total, up to sqrt(0.75) M2.)
+struct Joined {
+  float mean, m2;
+  bool far;
+};
+__device__ __forceinline__ Joined joined(float pivot, float total, float square, float inv_n) {
+  const float d = total * inv_n, m2 = fmaf(-total, d, square);
+  // (rounding may have left M2 below zero; a NaN stays one, as of a row that holds an infinity or a
+  // NaN nothing is a number)
+  return Joined{pivot + d, m2 < 0.f ? 0.f : m2, square > 1.5f * m2};
+}
 
 // Columns of [col, col + n) that a row of `cols` has.
 __device__ __forceinline__ int32_t columns_in(int32_t col, int32_t n, int32_t cols) {
@@ -140,8 +165,6 @@ __global__ void __launch_bounds__(ln_threads<R>()) ln_kernel(const __grid_consta
 #pragma unroll
   for (int c = 0; c < C; ++c) n_own += columns_in(col0 + c * tpr * 8, 8, cols);
   const float n_thread = static_cast<float>(n_own), inv_thread = n_own > 0 ? 1.f / n_thread : 0.f;
-  const uint32_t holders = __ballot_sync(0xffffffffu, n_own > 0);
-  const int pivot_lane = holders != 0u ? __ffs(holders) - 1 : 0;
   const float inv_mine = n_warp > 0 ? 1.f / n_mine : 0.f;
   if (lane == 0) counts[warp] = n_mine;
   __syncthreads();
@@ -180,126 +203,132 @@ __global__ void __launch_bounds__(ln_threads<R>()) ln_kernel(const __grid_consta
   for (int s = 0; s + 1 < D; ++s) start(s);
   const float inv_cols = 1.f / static_cast<float>(cols);
   int slot = 0, flip = 0;
-  for (; row < rows; row += step) {
-    if constexpr (R == ROWS_ANY) __syncwarp();  // (the slot was read in the iteration before)
-    start((slot + D - 1) % D);
-    cp_async_wait<D - 1>();
-    if constexpr (R == ROWS_ANY) __syncwarp();
-    Raw8<T> h[C];
-    float2 sum = make_float2(0.f, 0.f), v[C][4];
+  // (Made twice, with a residual and without: one loop that asks each time is too much for the compiler
+  // to take apart by itself, and costs 16384 x 8192 in 16 bits 158 us for 133, 211 for 176 with a residual.)
+  const auto all_rows = [&](auto with_residual) {
+    constexpr bool kRes = decltype(with_residual)::value;
+    for (; row < rows; row += step) {
+      if constexpr (R == ROWS_ANY) __syncwarp();  // (the slot was read in the iteration before)
+      start((slot + D - 1) % D);
+      cp_async_wait<D - 1>();
+      if constexpr (R == ROWS_ANY) __syncwarp();
+      Raw8<T> h[C];
+      float2 sum = make_float2(0.f, 0.f), v[C][4];
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const int32_t col = col0 + c * tpr * 8;
-      const uint32_t src = ring + slot * ring_row + c * 2 * kBuf;
-      h[c] = take_chunk<T, R>(src, c, static_cast<const T*>(p.x) + row * p.ldx, col, cols);
-      if (has_res) {
-        h[c] = add8(h[c], take_chunk<T, R>(src + kBuf, c, static_cast<const T*>(p.residual) + row * p.ldr, col, cols));
-        if (p.h != nullptr && warp_col + c * tpr * 8 < cols)
-          put_chunk<T, R>(static_cast<T*>(p.h) + row * p.ldh, c, col, cols, h[c]);
-      }
-      widen(h[c], v[c]);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) sum = __fadd2_rn(sum, v[c][i]);
-    }
-    slot = (slot + 1) % D;
-    // a thread's mean and squared deviation, joined over the warp as the warps' are over the row
-    const float own = (sum.x + sum.y) * inv_thread;
-    float2 dev = make_float2(0.f, 0.f);
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const int32_t col = col0 + c * tpr * 8;
-      if (col >= 0 && col + 8 <= cols) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 d = add2(v[c][i], -own);
-          dev = __ffma2_rn(d, d, dev);
+      for (int c = 0; c < C; ++c) {
+        const int32_t col = col0 + c * tpr * 8;
+        const uint32_t src = ring + slot * ring_row + c * 2 * kBuf;
+        h[c] = take_chunk<T, R>(src, c, static_cast<const T*>(p.x) + row * p.ldx, col, cols);
+        if constexpr (kRes) {
+          h[c] = add8(h[c], take_chunk<T, R>(src + kBuf, c, static_cast<const T*>(p.residual) + row * p.ldr, col, cols));
+          if (p.h != nullptr && warp_col + c * tpr * 8 < cols)
+            put_chunk<T, R>(static_cast<T*>(p.h) + row * p.ldh, c, col, cols, h[c]);
         }
-      } else {
+        widen(h[c], v[c]);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int32_t a = col + 2 * i, b = a + 1;
-          const float2 d = make_float2(a >= 0 && a < cols ? v[c][i].x - own : 0.f, b >= 0 && b < cols ? v[c][i].y - own : 0.f);
-          dev = __ffma2_rn(d, d, dev);
-        }
+        for (int i = 0; i < 4; ++i) sum = __fadd2_rn(sum, v[c][i]);
       }
-    }
-    float mean, m2;
-    {
-      const float pivot = __shfl_sync(0xffffffffu, own, pivot_lane);
-      const float off = n_thread > 0.f ? own - pivot : 0.f;
-      float total = n_thread * off, square = fmaf(n_thread * off, off, dev.x + dev.y);
+      slot = (slot + 1) % D;
+      // a thread's mean and squared deviation, joined over the warp as the warps' are over the row
+      const float own = (sum.x + sum.y) * inv_thread;
+      float2 dev = make_float2(0.f, 0.f);
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        total += __shfl_xor_sync(0xffffffffu, total, o);
-        square += __shfl_xor_sync(0xffffffffu, square, o);
-      }
-      const float d = total * inv_mine;
-      mean = pivot + d;
-      m2 = not_below_zero(fmaf(-total, d, square));
-    }
-    if (tpr > 32) {
-      float2* at = slots + flip * 32;
-      if (lane == 0) at[warp] = make_float2(mean, m2);
-      asm volatile("bar.sync %0, %1;" ::"r"(sub + 1), "r"(tpr) : "memory");
-      const float2 w = lane < per ? at[sub * per + lane] : make_float2(0.f, 0.f);
-      const float first = __shfl_sync(0xffffffffu, w.x, 0);
-      const float off = n_lane > 0.f ? w.x - first : 0.f;
-      const float total = warp_sum(n_lane * off);
-      const float square = warp_sum(fmaf(n_lane * off, off, w.y));
-      const float d = total * inv_cols;
-      mean = first + d;
-      m2 = not_below_zero(fmaf(-total, d, square));
-      flip ^= 1;
-    }
-    // (rounded correctly: an error of rstd moves every value of the row the same way)
-    const float rstd = __frsqrt_rn(fmaf(m2, inv_cols, p.eps));
-    if (t == 0) {
-      if (p.mean != nullptr) p.mean[row] = mean;
-      if (p.rstd != nullptr) p.rstd[row] = rstd;
-    }
+      for (int c = 0; c < C; ++c) {
+        const int32_t col = col0 + c * tpr * 8;
+        if (col >= 0 && col + 8 <= cols) {
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const int32_t col = col0 + c * tpr * 8;
-      if (c > 0 && warp_col + c * tpr * 8 >= cols) continue;
-      float2 v[4], w[4], b[4];
-      widen(h[c], v);
-      if constexpr (CODES) {
-        if (p.h8.codes != nullptr) {
-          float2 u[4] = {v[0], v[1], v[2], v[3]};
-          put_codes(p.h8, row, col, cols, u, false);
-        }
-      }
-      if constexpr (!kHeld) {
-        if (whole_params && col + 8 <= cols) {
-          if (p.p_dtype == DT_BF16) both_params<__nv_bfloat16>(p.weight, p.bias, col, w, b);
-          else if (p.p_dtype == DT_F16) both_params<__half>(p.weight, p.bias, col, w, b);
-          else both_params<float>(p.weight, p.bias, col, w, b);
-        } else {
-          load_param(p.weight, p.p_dtype, p.w_vec, col, cols, 1.f, w);
-          load_param(p.bias, p.p_dtype, p.w_vec, col, cols, 0.f, b);
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        v[i] = __ffma2_rn(mul2(add2(v[i], -mean), rstd), kHeld ? wk[kHeld ? c : 0][i] : w[i], kHeld ? bk[kHeld ? c : 0][i] : b[i]);
-      if (p.y != nullptr) put_chunk<T, R>(static_cast<T*>(p.y) + row * p.ldy, c, col, cols, narrow<T>(v));
-      if constexpr (CODES) {
-        if (p.q.codes != nullptr) {
-          // (past the row's end the values are -mean rstd, not 0)
-          if (col + 8 > cols) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              if (col + 2 * i >= cols) v[i].x = 0.f;
-              if (col + 2 * i + 1 >= cols) v[i].y = 0.f;
-            }
+          for (int i = 0; i < 4; ++i) {
+            const float2 d = add2(v[c][i], -own);
+            dev = __ffma2_rn(d, d, dev);
           }
-          put_codes(p.q, row, col, cols, v, p.values != nullptr);
-          if (p.values != nullptr)
-            store_row8_any<R == ROWS_ALIGNED>(p.values, row * p.ldv, p.v_dtype, col, cols, v);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int32_t a = col + 2 * i, b = a + 1;
+            const float2 d = make_float2(a >= 0 && a < cols ? v[c][i].x - own : 0.f, b >= 0 && b < cols ? v[c][i].y - own : 0.f);
+            dev = __ffma2_rn(d, d, dev);
+          }
+        }
+      }
+      // (relative to the second thread's: of a row that starts elsewhere the first may hold one value.
+      // Both sums are the same bits in every lane, so `far` is the warp's)
+      Joined all;
+      const auto join_threads = [&](float pivot) {
+        const float off = own - pivot;
+        float total = n_thread * off, square = fmaf(total, off, dev.x + dev.y);
+        warp_sums(total, square);
+        all = joined(pivot, total, square, inv_mine);
+      };
+      join_threads(__shfl_sync(0xffffffffu, own, 1));
+      if (__builtin_expect(all.far, 0)) join_threads(all.mean);
+      if (tpr > 32) {
+        float2* at = slots + flip * 32;
+        if (lane == 0) at[warp] = make_float2(all.mean, all.m2);
+        asm volatile("bar.sync %0, %1;" ::"r"(sub + 1), "r"(tpr) : "memory");
+        const float2 w = lane < per ? at[sub * per + lane] : make_float2(0.f, 0.f);
+        const auto join_warps = [&](float pivot) {
+          const float off = w.x - pivot;
+          float total = n_lane * off, square = fmaf(total, off, w.y);
+          warp_sums(total, square);
+          all = joined(pivot, total, square, inv_cols);
+        };
+        join_warps(__shfl_sync(0xffffffffu, w.x, 0));
+        if (__builtin_expect(all.far, 0)) join_warps(all.mean);
+        flip ^= 1;
+      }
+      const float mean = all.mean;
+      // (rounded correctly: an error of rstd moves every value of the row the same way)
+      const float rstd = __frsqrt_rn(fmaf(all.m2, inv_cols, p.eps));
+      if (t == 0) {
+        if (p.mean != nullptr) p.mean[row] = mean;
+        if (p.rstd != nullptr) p.rstd[row] = rstd;
+      }
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        const int32_t col = col0 + c * tpr * 8;
+        if (c > 0 && warp_col + c * tpr * 8 >= cols) continue;
+        float2 v[4], w[4], b[4];
+        widen(h[c], v);
+        if constexpr (CODES) {
+          if (p.h8.codes != nullptr) {
+            float2 u[4] = {v[0], v[1], v[2], v[3]};
+            put_codes(p.h8, row, col, cols, u, false);
+          }
+        }
+        if constexpr (!kHeld) {
+          if (whole_params && col + 8 <= cols) {
+            if (p.p_dtype == DT_BF16) both_params<__nv_bfloat16>(p.weight, p.bias, col, w, b);
+            else if (p.p_dtype == DT_F16) both_params<__half>(p.weight, p.bias, col, w, b);
+            else both_params<float>(p.weight, p.bias, col, w, b);
+          } else {
+            load_param(p.weight, p.p_dtype, p.w_vec, col, cols, 1.f, w);
+            load_param(p.bias, p.p_dtype, p.w_vec, col, cols, 0.f, b);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          v[i] = __ffma2_rn(mul2(add2(v[i], -mean), rstd), kHeld ? wk[kHeld ? c : 0][i] : w[i], kHeld ? bk[kHeld ? c : 0][i] : b[i]);
+        if (p.y != nullptr) put_chunk<T, R>(static_cast<T*>(p.y) + row * p.ldy, c, col, cols, narrow<T>(v));
+        if constexpr (CODES) {
+          if (p.q.codes != nullptr) {
+            // (past the row's end the values are -mean rstd, not 0)
+            if (col + 8 > cols) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                if (col + 2 * i >= cols) v[i].x = 0.f;
+                if (col + 2 * i + 1 >= cols) v[i].y = 0.f;
+              }
+            }
+            put_codes(p.q, row, col, cols, v, p.values != nullptr);
+            if (p.values != nullptr)
+              store_row8_any<R == ROWS_ALIGNED>(p.values, row * p.ldv, p.v_dtype, col, cols, v);
+          }
         }
       }
     }
-  }
+  };
+  if (has_res) all_rows(std::true_type{});
+  else all_rows(std::false_type{});
 }
 
 // Sum over a whole block.

@@ -1,13 +1,17 @@
 """Rows that the layer norm's joins of threads and warps could get wrong: an infinity or a NaN in any
-place.  Such a row has no variance, so its rstd, and with it all of its y, is NaN."""
+place, and one value far from all others where a row begins.
+
+The tolerances are those of test_layernorm_gpu.py, derived there.  What is not finite has none: a row
+that holds an infinity or a NaN has no variance, so its rstd, and with it all of its y, is NaN."""
 
 import numpy as np
 import pytest
 import torch
 
 from grouped_gemm_epilogues_gb300 import binding as gge
+from oracle import b128
 
-from test_layernorm_gpu import DEV, EPS, TYPES, _empty, _numbers, _rand
+from test_layernorm_gpu import DEV, EPS, TYPES, _empty, _forward_ref, _near, _numbers, _rand
 
 pytestmark = pytest.mark.gpu
 LIES = ("aligned", "alike", "any")   # where rows start against 16 bytes: on them, alike, each elsewhere
@@ -70,3 +74,32 @@ def test_rows_that_are_not_finite(cols, lie, dtype, codes):
     gge.gge_layernorm_bwd(dy, h8 if codes else x, w, mean, rstd, dx)
     gge.gge_layernorm_bwd(dy, h80 if codes else clean, w, mean0, rstd0, dx0)
     assert torch.isnan(dx[hit]).all() and torch.equal(dx[rest], dx0[rest])
+
+
+@pytest.mark.parametrize("cols", [64, 255, 256, 513, 777, 2056, 4096, 12288, 16384])
+@pytest.mark.parametrize("skew", range(8))
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("codes", [False, True])
+def test_one_value_far_from_the_others(cols, skew, dtype, codes):
+    """A channel that stands out, in the first place, the first thread's or the first warp's columns:
+    mean, variance and y are as good as for any row."""
+    rows = 300
+    g = torch.Generator().manual_seed(cols + skew)
+    x = torch.randn(rows, cols, generator=g)
+    at = [0, 7, 1, 40][skew % 4]
+    x[:, at] = torch.exp(torch.empty(rows).uniform_(4.0, 9.0, generator=g))
+    x = x.to(dtype).to(DEV)
+    wide, out = (torch.zeros(rows, cols + 8 - cols % 8 + 8, dtype=dtype, device=DEV) for _ in range(2))
+    wide[:, skew:skew + cols] = x
+    w = _rand(1, cols, torch.float32, 3)[0]
+    mean, rstd = torch.empty(rows, device=DEV), torch.empty(rows, device=DEV)
+    q = _empty(rows, cols) if codes else None
+    y = out[:, skew:skew + cols]
+    gge.gge_layernorm(wide[:, skew:skew + cols], w, Y=y, Q=q, mean=mean, rstd=rstd, eps=EPS)
+    _, rmean, rrstd, ry, tm, tr, ty = _forward_ref(x, w, None)
+    _near(rstd, rrstd, tr, "rstd")
+    _near(mean, rmean, tm, "mean")
+    _near(y, ry, ty, "y")
+    if codes:
+        value, scale = b128.off_codes(_numbers(q), q.scales.cpu().numpy(), ry, ty)
+        assert value <= 1.0 and scale <= 1.0, (value, scale)
