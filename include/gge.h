@@ -457,7 +457,7 @@ gge_status gge_rmsnorm_bwd(const gge_rmsnorm_bwd_args* args, void* workspace,
                            size_t workspace_bytes, gge_stream_t stream);
 
 /* ---- 8 bits with a scale for each block of 128 ---------------------------
- * Operands in 8-bit floating point with one fp32 scale (of any value) for each
+ * Operands in 8-bit floating point with one fp32 scale for each
  * block of 128 columns of a row, or of 128 rows x 128 columns; what makes them
  * (quantisation, transposition, the layer norm and the product's own epilogue),
  * their product, and the backward from activations that were kept in this form.
@@ -508,7 +508,10 @@ gge_status gge_b128_dequantize(const gge_b128_tensor* q, const gge_tensor* y, gg
  * PostAct = act(same value, before rounding)      sA[m, b] sB[n, b] sum_{k in b} a[m, k] b[n, k]
  *   A [M, K, L] and B [N, K, L], each with codes of either type and blocks of 1 or
  *   128 rows.  The sum within a block runs on the tensor core in fp32; blocks are
- *   scaled and added in fp32, in the order of K.
+ *   scaled and added in fp32, in the order of K.  A block's term is its sum times the
+ *   product sA sB, which is rounded to fp32 first: a product below 2^-126 loses up to
+ *   2^-150, so the term as much times its sum (which is 2^25 at most in e4m3, 2^39 in
+ *   e5m2); one of 2^128 or more makes the term an infinity or a NaN.
  *   C, D and PostAct: [M, N, L] as a gge_tensor (16 bits or fp32, as in gge_gemm) or,
  *   in the field that ends in 8, as a gge_b128_tensor with block_rows 1; at most one of the
  *   two each.  An 8-bit output is quantised from the fp32 value as gge_b128_quantize does
