@@ -232,6 +232,61 @@ __device__ __forceinline__ void record_status(const Params& p, int32_t code, int
   }
 }
 
+// Grouped rows: the offsets to shared memory, each held to [0, M] and to the largest before it, and
+// the tiles before each group.  Offsets that have to be moved are reported.  Whatever they are, no row
+// is then in two groups, and the groups' tiles are at most the (M / TILE_M + G) tiles_n that the host
+// counts (lengths taken of unchecked offsets leave 32 bits, and tiles of such groups the matrices).
+// Every offset is read once: all that follows goes by the copies.  Run by one warp.
+template <int TILE_M>
+__device__ __forceinline__ void take_groups(const Params& p, int32_t* prefix, int32_t* cu) {
+  const int lane = threadIdx.x & 31, G = p.num_groups;
+  const int per = (G + 32) / 32;  // of the G + 1 offsets
+  const int i0 = min(lane * per, G + 1), i1 = min(i0 + per, G + 1);
+  int32_t most = 0;  // (of this lane's)
+#pragma unroll 1
+  for (int i = i0; i < i1; ++i) {
+    const int32_t at = __ldg(p.cu_seqlens + i), held = min(max(at, 0), p.M);
+    most = max(most, held);
+    cu[i] = held;
+    if (held != at) record_status(p, DEV_INDEX_RANGE, 5, min(i, G - 1));
+  }
+  int32_t before = most;  // ... and of all lanes up to this one
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int32_t y = __shfl_up_sync(0xffffffffu, before, o);
+    if (lane >= o) before = max(before, y);
+  }
+  before = __shfl_up_sync(0xffffffffu, before, 1);
+  most = lane > 0 ? before : 0;
+#pragma unroll 1
+  for (int i = i0; i < i1; ++i) {
+    if (cu[i] < most) record_status(p, DEV_INDEX_RANGE, 5, i - 1);
+    cu[i] = most = max(most, cu[i]);
+  }
+  __syncwarp();
+  const int each = (G + 31) / 32;
+  const int g0 = min(lane * each, G), g1 = min(g0 + each, G);
+  const auto tiles = [&](int g) {
+    return static_cast<int32_t>((static_cast<uint32_t>(cu[g + 1] - cu[g]) + TILE_M - 1u) / TILE_M) * p.tiles_n;
+  };
+  int32_t mine = 0;
+#pragma unroll 1
+  for (int g = g0; g < g1; ++g) mine += tiles(g);
+  int32_t incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int32_t y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  int32_t run = incl - mine;
+#pragma unroll 1
+  for (int g = g0; g < g1; ++g) {
+    prefix[g] = run;
+    run += tiles(g);
+  }
+  if (lane == 31) prefix[G] = incl;
+}
+
 // Slow path of a bounded mbarrier wait: wait until the phase completes, the
 // CTA aborts, or timeout_ns of %globaltimer pass (then record and abort).
 // `sleep`: probe with the sleeping try_wait (the thread issues nothing until the
@@ -1670,38 +1725,8 @@ __global__ void __launch_bounds__(KernelCfg<BN, GATHER, CG>::kThreads, 1)
   // Everything above touched only this CTA's shared memory and TMEM; from here
   // on global memory that an earlier kernel in the stream may write is read.
   ptx::griddep_wait();
-  // varlen-M: copy cu_seqlens and build the per-group tile prefix (warp 0)
-  if (p.num_groups > 0 && warp == 0) {
-    const int G = p.num_groups;
-    const int per = (G + 31) / 32;
-    const int g0 = min(lane * per, G), g1 = min(g0 + per, G);
-    int32_t mine = 0;
-    for (int g = g0; g < g1; ++g) {
-      const int32_t lo = __ldg(p.cu_seqlens + g), hi = __ldg(p.cu_seqlens + g + 1);
-      if (lo < 0 || hi > p.M || hi < lo) record_status(p, DEV_INDEX_RANGE, 5, g);
-      const int32_t len = max(0, min(hi, p.M) - max(lo, 0));
-      mine += ((len + Cfg::kTileM - 1) / Cfg::kTileM) * p.tiles_n;
-    }
-    int32_t incl = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int32_t y = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += y;
-    }
-    int32_t run = incl - mine;
-    for (int g = g0; g < g1; ++g) {
-      const int32_t lo = __ldg(p.cu_seqlens + g), hi = __ldg(p.cu_seqlens + g + 1);
-      const int32_t clo = max(lo, 0);
-      const int32_t len = max(0, min(hi, p.M) - clo);
-      prefix[g] = run;
-      cu_s[g] = clo;
-      run += ((len + Cfg::kTileM - 1) / Cfg::kTileM) * p.tiles_n;
-    }
-    if (lane == 31) {
-      prefix[G] = incl;
-      cu_s[G] = min(max(__ldg(p.cu_seqlens + G), 0), p.M);
-    }
-  }
+  // varlen-M: copy cu_seqlens and build the per-group tile prefix
+  if (p.num_groups > 0 && warp == 0) take_groups<Cfg::kTileM>(p, prefix, cu_s);
   // varlen-K: each group's K columns [start, end).  A group that breaks the
   // rules (out of [0, total_K], decreasing, or a start that is not a whole
   // 16 bytes into a K-major row) is recorded and contracts nothing.

@@ -1174,40 +1174,7 @@ __global__ void __launch_bounds__(GemmCfg<BN, CG, BV>::kThreads, 1)
   }
   ptx::griddep_wait();
   // grouped rows: the offsets, and the tiles before each group
-  if (p.num_groups > 0 && warp == 0) {
-    const int G = p.num_groups;
-    const int per = (G + 31) / 32;
-    const int g0 = min(lane * per, G), g1 = min(g0 + per, G);
-    const auto group = [&](int g, int32_t& lo, int32_t& len) {
-      const int32_t from = __ldg(p.cu_seqlens + g), to = __ldg(p.cu_seqlens + g + 1);
-      const bool bad = from < 0 || to > p.M || to < from;
-      lo = max(from, 0);
-      len = max(0, min(to, p.M) - lo);
-      return bad;
-    };
-    int32_t mine = 0, lo, len;
-    for (int g = g0; g < g1; ++g) {
-      if (group(g, lo, len)) record_status(p, DEV_INDEX_RANGE, 5, g);
-      mine += ((len + Cfg::kTileM - 1) / Cfg::kTileM) * p.tiles_n;
-    }
-    int32_t incl = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int32_t y = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += y;
-    }
-    int32_t run = incl - mine;
-    for (int g = g0; g < g1; ++g) {
-      group(g, lo, len);
-      m.prefix[g] = run;
-      m.cu[g] = lo;
-      run += ((len + Cfg::kTileM - 1) / Cfg::kTileM) * p.tiles_n;
-    }
-    if (lane == 31) {
-      m.prefix[G] = incl;
-      m.cu[G] = min(max(__ldg(p.cu_seqlens + G), 0), p.M);
-    }
-  }
+  if (p.num_groups > 0 && warp == 0) take_groups<Cfg::kTileM>(p, m.prefix, m.cu);
   __syncthreads();
   if (CG == 2) ptx::cluster_sync();
   ptx::tc_fence_after();

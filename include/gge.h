@@ -244,8 +244,9 @@ gge_status gge_gemm_dact(const gge_gemm_args* args, void* workspace, size_t work
  * groups), C / D / PostAct are [total_M, N, 1].  Group g owns rows
  * cu_seqlens_m[g] .. cu_seqlens_m[g+1]-1 and multiplies them by B[:,:,g];
  * rows outside every group are not written.  cu_seqlens_m: DEVICE int32
- * [G+1], non-decreasing, cu[0] >= 0, cu[G] <= total_M (violations are
- * clamped and reported as GGE_ERR_INDEX_RANGE by gge_read_device_status).
+ * [G+1], non-decreasing, cu[0] >= 0, cu[G] <= total_M (an offset that breaks
+ * this is held to [0, total_M] and to the largest before it, and reported as
+ * GGE_ERR_INDEX_RANGE by gge_read_device_status).
  * 1 <= G <= 1024.  act as in gge_gemm_act.
  * Page: quack/dense_gemm_sm90.py, GemmSm90 with VarlenArguments(mCuSeqlensM). */
 gge_status gge_gemm_varlen_m(const gge_gemm_args* args, const int32_t* cu_seqlens_m,
@@ -522,7 +523,7 @@ gge_status gge_b128_dequantize(const gge_b128_tensor* q, const gge_tensor* y, gg
  *   [num_groups + 1], A [total_M, K, 1], B [N, K, num_groups], C, D and PostAct
  *   [total_M, N, 1]; row r of group g, cu[g] <= r < cu[g + 1], is multiplied with B[g].
  *   Rows of no group are not written.  At most 1024 groups.  An offset outside [0, total_M]
- *   or below the one before is reported as GGE_ERR_INDEX_RANGE.
+ *   or below one before it is held to these bounds and reported as GGE_ERR_INDEX_RANGE.
  *   config (may be NULL): tile_n 0 (automatic), 256 (a CTA pair, 256 x 256), 128 or 64
  *   (one CTA, 128 rows; 64 not with 8-bit outputs); num_ctas, raster_band, stages, timeout_ns;
  *   of the flags those for no split, raster along N and the test hook.
