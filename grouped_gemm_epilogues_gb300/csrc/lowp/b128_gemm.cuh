@@ -16,7 +16,8 @@
 //     400 cycles, whatever its columns.  Large products take 256 x 256 tiles on a CTA pair: 128
 //     columns a thread, 224 registers (setmaxnreg takes them from the warpgroup that loads and
 //     issues), two buffers of 256 columns.  A block then takes 810 cycles, 512 of them the tensor
-//     core's: 8192^3 381 us (without the additions 335).  Measured and left: 256 x 128 tiles with
+//     core's: 8192^3 380 us at 2.07 GHz (without the additions 335; over seconds, at the power cap's
+//     1.72 GHz, 423).  Measured and left: 256 x 128 tiles with
 //     four buffers (590), two MMAs of 128 columns a block, each half's buffers handed back by
 //     itself (444), the next block's first load under a block's last additions (439);
 //   * other products take 128 x 128 or 128 x 64 tiles on one CTA, with four buffers.  Their sums

@@ -4,9 +4,9 @@
 // Blocks run along a result's columns.  The source may hold those contiguously, or be the
 // transpose of a row-major matrix (its own columns contiguous along the result's rows), in
 // 16 or 32 bits or as codes: a 128 x 128 tile then goes through shared memory.  Every form
-// reads the source once.  8192 x 8192 bf16 in 44 us either way (201 MB, 4.6 TB/s; with the values
-// written too 60, 5.6 TB/s); codes of 16384 x 4096 turned in 37 us (134 MB, 3.6 TB/s; with values
-// 52), bound by the phases of a tile: load, scales, codes, store.
+// reads the source once.  8192 x 8192 bf16 in 44 us either way, rows as they lie 38 (201 MB, 4.6 and 5.3
+// TB/s; with the values written too 60, 5.6 TB/s); codes of 16384 x 4096 turned in 38 us (138 MB, 3.7
+// TB/s; with values 52), bound by the phases of a tile: load, scales, codes, store.
 #include "b128_launch.h"
 #include "rows.cuh"
 
