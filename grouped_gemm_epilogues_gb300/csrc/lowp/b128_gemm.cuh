@@ -934,6 +934,10 @@ __device__ __forceinline__ void finish_held(const GemmParams& gp, const CUtensor
           for (int j = 0; j < 4; ++j) acc[4 * g + j] = make_float2(v[2 * j], v[2 * j + 1]);
         }
         if (here && c + 1 < 4 && col0 + 32 < p.N) fetch_c(gp, row, col0 + 32, at.batch, c_raw);
+        if (col0 >= p.N) {  // (columns past N stay zero: an 8-bit PostAct takes its scale of all 128)
+#pragma unroll
+          for (int j = 0; j < 16; ++j) acc[j] = make_float2(0.f, 0.f);
+        }
       }
       if (pass == 1) {
         float v[32];
