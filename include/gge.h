@@ -571,7 +571,8 @@ gge_status gge_gemm_b128_dact(const gge_gemm_b128_args* args, void* workspace,
  *     residual_out may be x or residual itself.  residual_out is written only when there
  *     is a residual.
  *   weight, bias (each may be NULL: 1 and 0): `cols` contiguous values of param_dtype.
- *   mean, rstd: fp32 [rows].
+ *   mean, rstd: fp32 [rows].  A row that holds an infinity or a NaN has a NaN rstd and y, as may one
+ *     whose squares leave fp32 (values above 2^63 in size).
  *   q, values: y quantised from fp32 as gge_b128_quantize does (block_rows 1), and the
  *     numbers that its codes stand for (values needs q).
  *   h8: h quantised (block_rows 1), as the backward may read it.
