@@ -9,7 +9,7 @@
 // squared deviation,
 //   M2 = sum over parts of M2_p + n_p (mean_p - mean)^2,
 // with the parts' means taken relative to one of them, and once more relative to the result where
-// that one lay far from it (see join), so that no sum of squares is large against the variance.
+// that one lay far from it (see Joined), so that no sum of squares is large against the variance.
 // What is left of a mean far from zero is its own rounding in a thread's differences.  (One
 // reduction over the warp for both sums; a warp's mean first and then its deviations: 16384 x 8192 to
 // codes and values 281 us, so 228.)
